@@ -21,6 +21,10 @@ buffers; the stage entry points (``build_index``, ``rope_qk``,
 ``build_summaries``, ``local_attn``, ``summary_attn``) run one stage each.
 Every wrapper checks its tensors' dtypes and element counts against the
 config before calling the library.
+
+The causal sequence operators next to them (windowed attention of packed token
+sequences and its gradients, the paged key-value cache for one token at a
+time) are in ``seq.py`` and are names of this package too.
 """
 from __future__ import annotations
 
@@ -40,9 +44,10 @@ FLAG_DIAG_STALL = 0x8         # diagnostic: each tensor-core kernel withholds on
 FLAG_SUMMARY_ONE_TILE = 0x10  # force the one-tile build of the tensor-core query x summary kernel
 FLAG_SUMMARY_TWO_TILE = 0x20  # force the two-tile build
 DEVERR_COORD_RANGE, DEVERR_DUPLICATE, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_LENGTHS, DEVERR_PAGE = 0x8, 0x10  # the sequence operators' (include/pack3d_seq.h)
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "SHAPE", 3: "ALIGNMENT", 4: "DTYPE", 5: "NOT_PERMUTATION",
-          6: "WORKSPACE", 7: "CUDA", 8: "TIMEOUT"}
+          6: "WORKSPACE", 7: "CUDA", 8: "TIMEOUT", 9: "LENGTHS", 10: "PAGE"}
 
 ENTRY_POINTS = ("pack3d_default_config", "pack3d_validate_config", "pack3d_workspace_bytes",
                 "pack3d_build_index", "pack3d_rope", "pack3d_rope_qk", "pack3d_build_summaries", "pack3d_local_attn",
@@ -530,3 +535,8 @@ class _LazyAutograd:
 
 
 _Pack3DAutograd = _LazyAutograd
+
+
+from .seq import (  # noqa: E402  (needs the library and the checks above)
+    SEQ_ENTRY_POINTS, PagedCache, SeqConfig, cache_append, cache_attn, cache_attn_workspace_bytes, cache_evict,
+    make_seq_config, validate_seq, window_attention, window_attn, window_attn_bwd, window_attn_bwd_workspace_bytes)

@@ -674,6 +674,8 @@ pack3d_status pack3d_check_status(int32_t* err_word, void* stream) {
   if (e != cudaSuccess) return cuda_status(e);
   if (h & PACK3D_DEVERR_TIMEOUT) return PACK3D_ERR_TIMEOUT;
   if (h & (PACK3D_DEVERR_COORD_RANGE | PACK3D_DEVERR_DUPLICATE)) return PACK3D_ERR_NOT_PERMUTATION;
+  if (h & PACK3D_DEVERR_LENGTHS) return PACK3D_ERR_LENGTHS;
+  if (h & PACK3D_DEVERR_PAGE) return PACK3D_ERR_PAGE;
   return PACK3D_OK;
 }
 
@@ -688,6 +690,8 @@ const char* pack3d_status_string(pack3d_status s) {
     case PACK3D_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case PACK3D_ERR_CUDA: return "CUDA runtime error";
     case PACK3D_ERR_TIMEOUT: return "device-side wait timed out";
+    case PACK3D_ERR_LENGTHS: return "sequence offsets or lengths out of order or out of range";
+    case PACK3D_ERR_PAGE: return "page number outside the page pool";
   }
   return "unknown status";
 }

@@ -1,0 +1,214 @@
+// The paged key-value cache's row moves: new rows appended, and the cache cut
+// to a budget by accumulated attention weight.
+#include "seq.cuh"
+
+namespace pack3d {
+namespace seq {
+namespace {
+
+// ---- append -----------------------------------------------------------------
+// One thread moves one 16-byte chunk of a key or value row: both sides of the
+// copy are coalesced, and a row finds its sequence by a binary search of cu.
+__global__ void __launch_bounds__(256) cache_append_kernel(const Cache c, const int32_t* __restrict__ cu, long rows,
+                                                           const uint4* __restrict__ k, const uint4* __restrict__ v,
+                                                           int chunks) {
+  const long total = rows * chunks;
+  for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
+    const long row = i / chunks;
+    const int chunk = (int)(i - row * chunks);
+    int b = (int)row;
+    long in = 0;
+    if (cu) {
+      int lo = 0, hi = c.B;                 // last b with cu[b] <= row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(cu + mid) <= row) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      const int c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+      if (c0 < 0 || c1 < c0 || c1 > rows) {
+        set_err(c.err, PACK3D_DEVERR_LENGTHS);
+        continue;
+      }
+      if (row < c0 || row >= c1) continue;  // no sequence's row
+      in = row - c0;
+    }
+    const long at = __ldg(c.lengths + b) + in;
+    if (at - in < 0 || at >= c.cap) {
+      set_err(c.err, PACK3D_DEVERR_LENGTHS);
+      continue;
+    }
+    const long to = pool_row(c, c.table + (size_t)b * c.max_pages, (int)at);
+    if (to < 0) continue;
+    ((uint4*)c.k_pages)[to * chunks + chunk] = __ldg(k + i);
+    ((uint4*)c.v_pages)[to * chunks + chunk] = __ldg(v + i);
+  }
+}
+
+// ---- eviction -----------------------------------------------------------------
+// Select: one CTA per sequence.  The weights become 32-bit keys whose unsigned
+// order is the weights' order; the key of the last slot that stays is found by
+// a radix search from the top byte down (four histograms of 256 bins).  Then
+// every warp counts, over its own run of slots, those that stay for sure and
+// those that equal that key, one scan over the warps turns the counts into
+// places, and a second walk writes the kept slots in order: of the equal ones
+// the first few stay.
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;                                 // NaN: below every number
+  const uint32_t u = __float_as_uint(w + 0.f);           // -0 becomes 0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c, const float* __restrict__ weights,
+                                                                   int budget, int recent, int new_cap,
+                                                                   int32_t* __restrict__ kept,
+                                                                   float* __restrict__ new_weights,
+                                                                   int32_t* __restrict__ new_lengths) {
+  __shared__ uint32_t hist[256];
+  __shared__ int s_need;
+  __shared__ uint32_t s_prefix;
+  __shared__ int2 warp_count[kSelWarps];
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = cached(c, b);
+  const float* w = weights + (size_t)b * c.cap;
+  int32_t* kb = kept + (size_t)b * budget;
+  float* nw = new_weights + (size_t)b * new_cap;
+  const int m = min(n, budget);
+  if (tid == 0) new_lengths[b] = m;
+  for (int i = m + tid; i < new_cap; i += kSelThreads) nw[i] = 0.f;
+  for (int i = m + tid; i < budget; i += kSelThreads) kb[i] = -1;
+  if (n <= budget) {
+    for (int i = tid; i < n; i += kSelThreads) {
+      kb[i] = i;
+      nw[i] = w[i];
+    }
+    return;
+  }
+  // n > budget >= sinks + recent: the slots [lo, hi) compete for `need` places.
+  const int lo = c.sinks, hi = n - recent;
+  if (tid == 0) {
+    s_need = budget - c.sinks - recent;
+    s_prefix = 0;
+  }
+  __syncthreads();
+  const bool any = s_need > 0;
+  if (any) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+      for (int i = lo + tid; i < hi; i += kSelThreads) {
+        const uint32_t key = weight_key(w[i]);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int left = s_need;
+        int d = 255;
+        while (d > 0 && (int)hist[d] < left) left -= hist[d--];
+        s_need = left;                                   // places among the keys with this prefix
+        s_prefix = prefix | ((uint32_t)d << shift);
+      }
+      __syncthreads();
+    }
+  }
+  const uint32_t last = s_prefix;
+  const int equal_places = any ? s_need : 0;
+  // Warp `warp` walks the slots [begin, end), 32 at a time.
+  const int per = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int begin = min(n, warp * per), end = min(n, begin + per);
+  auto look = [&](int i, bool* sure, bool* equal) {
+    *sure = *equal = false;
+    if (i >= end) return;
+    if (i < lo || i >= hi) *sure = true;
+    else if (any) {
+      const uint32_t key = weight_key(w[i]);
+      *sure = key > last;
+      *equal = key == last;
+    }
+  };
+  int sure_n = 0, equal_n = 0;
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    bool sure, equal;
+    look(i0 + lane, &sure, &equal);
+    sure_n += __popc(__ballot_sync(0xffffffffu, sure));
+    equal_n += __popc(__ballot_sync(0xffffffffu, equal));
+  }
+  if (lane == 0) warp_count[warp] = make_int2(sure_n, equal_n);
+  __syncthreads();
+  int sure_at = 0, equal_at = 0;
+  for (int i = 0; i < warp; ++i) {
+    sure_at += warp_count[i].x;
+    equal_at += warp_count[i].y;
+  }
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    bool sure, equal;
+    look(i, &sure, &equal);
+    const uint32_t sb = __ballot_sync(0xffffffffu, sure), eb = __ballot_sync(0xffffffffu, equal);
+    const uint32_t below = (1u << lane) - 1u;
+    const int e = equal_at + __popc(eb & below);         // equal slots before this one
+    const int at = sure_at + __popc(sb & below) + min(e, equal_places);
+    if (sure || (equal && e < equal_places)) {
+      kb[at] = i;
+      nw[at] = w[i];
+    }
+    sure_at += __popc(sb);
+    equal_at += __popc(eb);
+  }
+}
+
+// Copies the kept rows to the new pages: one thread per 16-byte chunk of a key
+// and a value row.
+__global__ void __launch_bounds__(256) cache_move_kernel(const Cache c, const int32_t* __restrict__ kept, int budget,
+                                                         const int32_t* __restrict__ new_table, int new_max_pages,
+                                                         int chunks) {
+  const long total = (long)budget * chunks;
+  const int b = blockIdx.y;
+  Cache to = c;
+  to.max_pages = new_max_pages;
+  for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
+    const int slot = (int)(i / chunks), chunk = (int)(i - (long)slot * chunks);
+    const int from = __ldg(kept + (size_t)b * budget + slot);
+    if (from < 0) continue;
+    const long src = pool_row(c, c.table + (size_t)b * c.max_pages, from);
+    const long dst = pool_row(to, new_table + (size_t)b * new_max_pages, slot);
+    if (src < 0 || dst < 0) continue;
+    uint4* k = (uint4*)c.k_pages;
+    uint4* v = (uint4*)c.v_pages;
+    const uint4 a = k[src * chunks + chunk], d = v[src * chunks + chunk];
+    k[dst * chunks + chunk] = a;
+    v[dst * chunks + chunk] = d;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const Cache& c, const int32_t* cu, long rows, const void* k, const void* v,
+                                cudaStream_t st) {
+  const int chunks = c.Hkv * kDh * c.elem_bytes / 16;
+  const long want = (rows * chunks + 255) / 256;
+  const unsigned grid = (unsigned)min(want, 148L * 16);
+  cache_append_kernel<<<grid, 256, 0, st>>>(c, cu, rows, (const uint4*)k, (const uint4*)v, chunks);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_evict(const Cache& c, const float* weights, int budget, int recent,
+                               const int32_t* new_table, int new_max_pages, int32_t* kept, float* new_weights,
+                               int32_t* new_lengths, cudaStream_t st) {
+  cache_select_kernel<<<c.B, kSelThreads, 0, st>>>(c, weights, budget, recent, new_max_pages * c.page, kept,
+                                                   new_weights, new_lengths);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int chunks = c.Hkv * kDh * c.elem_bytes / 16;
+  const long want = ((long)budget * chunks + 255) / 256;
+  const dim3 grid((unsigned)min(want, 148L * 16), c.B);
+  cache_move_kernel<<<grid, 256, 0, st>>>(c, kept, budget, new_table, new_max_pages, chunks);
+  return cudaGetLastError();
+}
+
+}  // namespace seq
+}  // namespace pack3d

@@ -1,0 +1,83 @@
+// Causal windowed attention of packed sequences and its gradients, row by row:
+// one warp owns one query row of one head (forward, dq) or one key row of one
+// key head (dk, dv).
+#include "seq.cuh"
+
+namespace pack3d {
+namespace seq {
+namespace {
+
+constexpr int kWarps = 8;
+
+// What a CTA without a tile does: it reports wrong offsets, or fills the rows
+// that belong to no sequence.
+template <typename T>
+__device__ __forceinline__ void no_query_tile(const Win& w, const Tiles& all, void* rows, float* lse) {
+  if (all.bad) {
+    if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
+  } else if (w.zero_outside && blockIdx.y == 0) {
+    fill_outside(w, w.cu_q, w.Tq, rows, w.Hq * kDh * (int)sizeof(T) / 4, 0u, blockIdx.x, gridDim.x, all);
+    if (lse) fill_outside(w, w.cu_q, w.Tq, lse, w.Hq, 0xff800000u, blockIdx.x, gridDim.x, all);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void no_key_tile(const Win& w, const Tiles& all) {
+  if (all.bad || !w.zero_outside || blockIdx.y != 0) return;
+  const int words = w.Hkv * kDh * (int)sizeof(T) / 4;
+  fill_outside(w, w.cu_k, w.Tk, w.dk, words, 0u, blockIdx.x, gridDim.x, all);
+  fill_outside(w, w.cu_k, w.Tk, w.dv, words, 0u, blockIdx.x, gridDim.x, all);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) window_rows_kernel(const Win w) {
+  Tile s;
+  Tiles all;
+  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &all)) return no_query_tile<T>(w, all, w.out, w.lse);
+  const int r = s.t * kWarps + (threadIdx.x >> 5);
+  if (r < s.lq) out_row<T>(w, s, r, blockIdx.y);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) window_dq_rows_kernel(const Win w) {
+  Tile s;
+  Tiles all;
+  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &all)) return no_query_tile<T>(w, all, w.dq, nullptr);
+  const int r = s.t * kWarps + (threadIdx.x >> 5);
+  if (r >= s.lq) return;
+  delta_row<T>(w, (size_t)(s.q0 + r) * w.Hq + blockIdx.y);
+  __syncwarp();
+  dq_row<T>(w, s, r, blockIdx.y);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win w) {
+  Tile s;
+  Tiles all;
+  if (!find_tile(w, blockIdx.x, kWarps, true, &s, &all)) return no_key_tile<T>(w, all);
+  const int j = s.t * kWarps + (threadIdx.x >> 5);
+  if (j < s.lk) dkv_row<T>(w, s, j, blockIdx.y);
+}
+
+}  // namespace
+
+cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st) {
+  const dim3 grid((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq);
+  if (dtype == PACK3D_BF16) window_rows_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(w);
+  else window_rows_kernel<float><<<grid, 32 * kWarps, 0, st>>>(w);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_bwd(const Win& w, int dtype, cudaStream_t st) {
+  const dim3 gq((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq), gk((unsigned)tile_grid(w.Tk, kWarps, w.B), w.Hkv);
+  if (dtype == PACK3D_BF16) {
+    window_dq_rows_kernel<__nv_bfloat16><<<gq, 32 * kWarps, 0, st>>>(w);
+    window_dkv_rows_kernel<__nv_bfloat16><<<gk, 32 * kWarps, 0, st>>>(w);
+  } else {
+    window_dq_rows_kernel<float><<<gq, 32 * kWarps, 0, st>>>(w);
+    window_dkv_rows_kernel<float><<<gk, 32 * kWarps, 0, st>>>(w);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace seq
+}  // namespace pack3d

@@ -73,7 +73,9 @@ typedef enum {
     PACK3D_ERR_NOT_PERMUTATION = 5, /* coords are not a bijection onto the lattice */
     PACK3D_ERR_WORKSPACE = 6,       /* workspace missing or too small              */
     PACK3D_ERR_CUDA = 7,            /* a CUDA runtime call failed                  */
-    PACK3D_ERR_TIMEOUT = 8          /* a bounded device-side wait ran out          */
+    PACK3D_ERR_TIMEOUT = 8,         /* a bounded device-side wait ran out          */
+    PACK3D_ERR_LENGTHS = 9,         /* sequence offsets or lengths out of range    */
+    PACK3D_ERR_PAGE = 10            /* a page number outside the page pool         */
 } pack3d_status;
 
 typedef enum { PACK3D_F32 = 0, PACK3D_BF16 = 1 } pack3d_dtype;
@@ -82,6 +84,8 @@ typedef enum { PACK3D_F32 = 0, PACK3D_BF16 = 1 } pack3d_dtype;
 #define PACK3D_DEVERR_COORD_RANGE 0x1  /* a coordinate outside the lattice */
 #define PACK3D_DEVERR_DUPLICATE   0x2  /* two tokens share one site        */
 #define PACK3D_DEVERR_TIMEOUT     0x4  /* a pipeline wait gave up          */
+#define PACK3D_DEVERR_LENGTHS     0x8  /* sequence offsets or lengths out of range (pack3d_seq.h) */
+#define PACK3D_DEVERR_PAGE        0x10 /* a page number outside the pool (pack3d_seq.h)           */
 
 /* config.flags */
 #define PACK3D_FLAG_SIMT_SUMMARY  0x1  /* bf16: use the CUDA-core query x summary
@@ -411,8 +415,10 @@ pack3d_status pack3d_forward_backward(const pack3d_config *cfg, const int32_t *c
                                       int32_t *err_word, void *stream);
 
 /* Synchronises `stream`, reads the device error word, resets it to 0 and maps
- * it: COORD_RANGE/DUPLICATE -> PACK3D_ERR_NOT_PERMUTATION, TIMEOUT ->
- * PACK3D_ERR_TIMEOUT, none -> PACK3D_OK.  A failed CUDA call -> PACK3D_ERR_CUDA. */
+ * it: TIMEOUT -> PACK3D_ERR_TIMEOUT, COORD_RANGE/DUPLICATE ->
+ * PACK3D_ERR_NOT_PERMUTATION, LENGTHS -> PACK3D_ERR_LENGTHS, PAGE ->
+ * PACK3D_ERR_PAGE (the first of these that is set), none -> PACK3D_OK.  A failed
+ * CUDA call -> PACK3D_ERR_CUDA. */
 pack3d_status pack3d_check_status(int32_t *err_word, void *stream);
 
 /* Static text for a status code. */
