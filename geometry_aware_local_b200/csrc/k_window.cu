@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win 
 }  // namespace
 
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st) {
+  if (dtype == PACK3D_BF16 && w.Tk > 0) return launch_window_attn_tc(w, st);
   const dim3 grid((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq);
   if (dtype == PACK3D_BF16) window_rows_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(w);
   else window_rows_kernel<float><<<grid, 32 * kWarps, 0, st>>>(w);

@@ -1,0 +1,437 @@
+// Causal windowed attention of packed sequences on sm_100a tensor cores (bf16).
+//
+//   o[i,h] = sum_{j in V(i)} softmax_j(c <q[i,h], k[j,g]>) v[j,g]
+// with V(i) the window behind token i and the sequence's first `sinks` keys.
+//
+// One CTA = one 128-row query tile of one key head: rows are (token, query
+// head) pairs of the group, 128/G tokens of one sequence x G heads, so the
+// heads that share keys share every key tile.  The tile's visible keys are one
+// range [lo, hi] (the first token's window to the last token) and, where the
+// window has moved past them, the sinks as one short tile in front.  Keys come
+// in tiles of 128 from lo on; the last tile, and the sinks' one, are cut to a
+// multiple of 32 columns, so the work follows the range in steps of 32 keys.
+// Masks are evaluated only in the 32-column chunks that some row sees in part.
+//   * the last warp loads the Q tile and a ring of K / V tiles by TMA (boxes of
+//     32 keys x 64 dims, 128-byte swizzle);
+//   * one warp issues tcgen05.mma: S = Q K^T (M=128, N = the tile's columns,
+//     K=64) into tensor memory and O += P V (N=64) with P from tensor memory;
+//   * four softmax warps (thread = row = TMEM lane) run the online softmax in
+//     base 2 with a lazily moved maximum: O is rescaled only when a row maximum
+//     grows by more than 2^8.
+// Two CTAs per SM (256 tensor-memory columns each: S 128, P 64, O 64) hide each
+// other's hand-offs.  At d_h = 64 an exponential pairs with only 256 MMA flops,
+// so the softmax warps set the pace.
+//
+// A key that a row does not see has P = 0 exactly; where its value row holds a
+// NaN or an infinity, 0 times it is a NaN.  A row whose result is not finite is
+// therefore computed again from its visible keys alone (out_row).
+#include <cuda.h>
+
+#include "seq.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace pack3d {
+namespace seq {
+namespace {
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kMmaWarp = 4, kTmaWarp = 5, kThreads = 192;
+constexpr int kColS = 0, kColP = kBN, kColO = kBN + kBN / 2, kTmemCols = 256;
+constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2, kChunkBytes = 32 * kDh * 2;
+constexpr int kStages = 2;
+constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;     // K at +0, V at +kTileBytes
+constexpr int kBarOff = kStageOff + kStages * kStageBytes;
+// barriers: full[S], empty[S], qfull, s_full, s_free, p_full, p_free, o_final, drain
+constexpr int kNumBars = 2 * kStages + 7;
+constexpr int kCtlOff = kBarOff + kNumBars * 8;
+constexpr int kTileOff = kCtlOff + 32;                               // Tile, Tiles and the answer of find_tile
+constexpr int kSmemBytes = kTileOff + 64 + 1024;
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(sizeof(Tile) + sizeof(Tiles) + 4 <= 64, "tile slot");
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kDh, true);   // V MN-major
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The tile's key tiles: number j starts at key begin(j) of the sequence and
+// has cols(j) columns, a multiple of 32.
+struct KeyTiles {
+  int lo, hi;       // the tile's range of keys
+  int sink_cols;    // columns of the sinks' tile in front of it, or 0
+  int n;
+  __device__ __forceinline__ int begin(int j) const {
+    return sink_cols ? (j == 0 ? 0 : lo + (j - 1) * kBN) : lo + j * kBN;
+  }
+  __device__ __forceinline__ int cols(int j) const {
+    return sink_cols && j == 0 ? sink_cols : min(kBN, (hi - begin(j) + 32) & ~31);
+  }
+};
+
+// Keys of the queries at positions p0 .. p1 (p0 <= p1) of a sequence.
+__device__ __forceinline__ KeyTiles key_tiles(const Win& w, int p0, int p1) {
+  KeyTiles k;
+  k.hi = p1;
+  k.sink_cols = 0;
+  if (p1 < 0) {
+    k.lo = 0;
+    k.n = 0;
+    return k;
+  }
+  k.lo = window_low(w, max(p0, 0));
+  const int sinks = min(w.sinks, k.lo);
+  // One range from key 0 where that takes no more columns than the sinks apart
+  // (it does where the sinks' columns would reach the window).
+  if (sinks > 0) {
+    if (((sinks + 31) & ~31) >= k.lo) k.lo = 0;
+    else k.sink_cols = (sinks + 31) & ~31;
+  }
+  k.n = (k.hi - k.lo) / kBN + 1 + (k.sink_cols ? 1 : 0);
+  return k;
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const Win w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y;
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const uint32_t bar0 = sbase + kBarOff;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  const uint32_t qfull = bar0 + 8 * (2 * kStages);
+  const uint32_t s_full = qfull + 8, s_free = qfull + 16, p_full = qfull + 24, p_free = qfull + 32,
+                 o_final = qfull + 40, drain = qfull + 48;
+  volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
+  Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
+  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
+  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  const int tokens = kBM >> w.gshift;     // per tile
+
+  if (warp == 0) {
+    Tile s;
+    Tiles all;
+    const bool found = find_tile(w, blockIdx.x, tokens, false, &s, &all);
+    if (lane == 0) {
+      *tile_slot = s;
+      *tiles_slot = all;
+      *found_slot = found;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(qfull, 1);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(s_free, 4);
+    ptx::mbar_init(p_full, 4);
+    ptx::mbar_init(p_free, 1);
+    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(drain, 1);
+    ctl->abort = 0;
+    ctl->issued = 0;
+    ctl->limit_ns = w.wait_ns;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  if (!*found_slot) {
+    const Tiles all = *tiles_slot;
+    if (all.bad) {
+      if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
+    } else if (w.zero_outside && blockIdx.y == 0) {
+      fill_outside(w, w.cu_q, w.Tq, w.out, w.Hq * kDh / 2, 0u, blockIdx.x, gridDim.x, all);
+      if (w.lse) fill_outside(w, w.cu_q, w.Tq, w.lse, w.Hq, 0xff800000u, blockIdx.x, gridDim.x, all);
+    }
+    return;
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Tile s = *tile_slot;
+  s.t = s.n - 1 - s.t;      // the tiles with most keys first
+  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
+  const int p0 = position(s, r0), p1 = position(s, r1);
+  const KeyTiles kt = key_tiles(w, p0, p1);
+  const int T = kt.n;
+
+  if (warp == kTmaWarp) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0 && T > 0) {
+      ptx::tma_prefetch(&tmQ);
+      ptx::tma_prefetch(&tmK);
+      ptx::tma_prefetch(&tmV);
+      ptx::mbar_expect_tx(qfull, kQBytes);
+      ptx::tma_load_4d(sbase, &tmQ, 0, 0, g, s.q0 + r0, qfull);
+      const int T_load = w.stall ? T - 1 : T;
+      int issued = 0;
+      for (int j = 0; j < T_load; ++j) {
+        const int st = j % kStages;
+        if (j >= kStages && !wait(empty(st), ((j / kStages) - 1) & 1)) break;
+        const uint32_t dst = sbase + kStageOff + st * kStageBytes;
+        const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
+        ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
+        for (int c = 0; c < cols / 32; ++c) ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
+        for (int c = 0; c < cols / 32; ++c)
+          ptx::tma_load_3d(dst + kTileBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
+        issued = j + 1;
+      }
+      ctl->issued = issued;
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0 && T > 0) {
+      const uint32_t tS = tmem + kColS, tP = tmem + kColP, tO = tmem + kColO;
+      auto issue_s = [&](int j) {
+        const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
+        const uint32_t idesc = ptx::idesc_bf16_f32(kBM, kt.cols(j), false);
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk)
+          ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(kaddr + kk * 32, 16, 1024), idesc, kk > 0);
+        ptx::tc_commit(s_full);
+      };
+      auto issue_pv = [&](int j) {
+        const uint32_t vaddr = sbase + kStageOff + (j % kStages) * kStageBytes + kTileBytes;
+        const int steps = kt.cols(j) / 16;
+        for (int kk = 0; kk < steps; ++kk)
+          ptx::mma_ts(tO, tP + kk * 8, ptx::smem_desc_sw128(vaddr + kk * 2048, 8192, 1024), kIdescPV,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(p_free);
+        ptx::tc_commit(empty(j % kStages));
+        if (j == T - 1) ptx::tc_commit(o_final);
+      };
+      bool ok = wait(qfull, 0) && wait(full(0), 0);
+      if (ok) {
+        ptx::tc_fence_after();
+        issue_s(0);
+      }
+      for (int j = 0; ok && j < T; ++j) {
+        if (j + 1 < T) {
+          if (!(ok = wait(s_free, j & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
+          ptx::tc_fence_after();
+          issue_s(j + 1);
+        }
+        if (!(ok = wait(p_full, j & 1))) break;
+        ptx::tc_fence_after();
+        issue_pv(j);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax warps: thread = row = tensor-memory lane ----------------
+    const int lane_base = warp * 32;
+    const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
+    const uint32_t tP = trow + kColP, tO = trow + kColO;
+    const float c = w.scale_log2;
+    const int row = lane_base + lane;
+    const int r = r0 + (row >> w.gshift);               // this row's token in its sequence
+    const bool valid = r <= r1;
+    const int p = valid ? position(s, r) : -1;          // rows past the sequence see nothing
+    const int low = window_low(w, p);
+    const int low_last = window_low(w, p1);             // the tile's last window start
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    auto warp_arrive = [&](uint32_t bar) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+    };
+    for (int j = 0; j < T; ++j) {
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
+      ptx::tc_fence_after();
+      const int k0 = kt.begin(j), cols = kt.cols(j);
+      uint32_t sv[kBN];
+#pragma unroll
+      for (int q = 0; q < kBN / 64; ++q)
+        if (64 * q < cols) {
+          if (64 * q + 32 < cols) ptx::tmem_ld64_sync(trow + kColS + 64 * q, sv + 64 * q);
+          else ptx::tmem_ld32_sync(trow + kColS + 64 * q, sv + 64 * q);
+        }
+      warp_arrive(s_free);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kBN / 32; ++q) {
+        if (32 * q >= cols) break;
+        const int c0 = k0 + 32 * q;                     // the chunk's first key
+        // Seen in full by every row of the tile: behind the last row's window
+        // start and not past the first row's own key (and every row valid).
+        if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {
+          const int a = max(low - c0, 0), z = p - c0;   // visible columns [a, z] and those below the sinks
+          uint32_t see = z < 0 ? 0u : (z >= 31 ? 0xffffffffu : (2u << z) - 1u);
+          const int first = min(max(w.sinks - c0, 0), 32);
+          const uint32_t sink = first >= 32 ? 0xffffffffu : (1u << first) - 1u;
+          see &= (a >= 32 ? 0u : 0xffffffffu << a) | sink;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((see >> k) & 1u)) sv[32 * q + k] = __float_as_uint(-INFINITY);
+        }
+        float m4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m4[i] = fmaxf(__uint_as_float(sv[32 * q + 2 * i]), __uint_as_float(sv[32 * q + 2 * i + 1]));
+#pragma unroll
+        for (int k = 8; k < 32; k += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m4[i] = max3(m4[i], __uint_as_float(sv[32 * q + k + 2 * i]), __uint_as_float(sv[32 * q + k + 2 * i + 1]));
+        mx = max3(mx, max3(m4[0], m4[1], m4[2]), m4[3]);
+      }
+      const float mxs = mx * c;
+      float f = 1.f;
+      if (j == 0) m_used = mxs;
+      else if (mxs > m_used + kRescaleThreshold) {
+        f = ptx::ex2(m_used - mxs);
+        m_used = mxs;
+      }
+      const bool rescale = j > 0 && __any_sync(0xffffffffu, f != 1.f);
+      if (j > 0) {
+        // P of the previous tile has been read by its O += P V.
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free, (j - 1) & 1)))) break;
+        ptx::tc_fence_after();
+      }
+      // A row that has seen no key yet (maximum -infinity) has only scores of
+      // -infinity here: any finite shift gives their weight 0.
+      const float shift = m_used == -INFINITY ? 0.f : -m_used;
+      const float2 c2 = make_float2(c, c), nm2 = make_float2(shift, shift);
+      float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int q = 0; q < kBN / 32; ++q) {
+        if (32 * q >= cols) break;
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = 32 * q + 2 * k;
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nm2);
+          const float2 pr = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+          rs[k & 1] = __fadd2_rn(rs[k & 1], pr);
+          pk[k] = pack_bf16x2(pr.x, pr.y);
+        }
+        ptx::tmem_st16(tP + 16 * q, pk);
+      }
+      if (rescale) {
+        uint32_t o[16];
+#pragma unroll
+        for (int q = 0; q < kDh / 16; ++q) {
+          ptx::tmem_ld16_sync(tO + 16 * q, o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          ptx::tmem_st16(tO + 16 * q, o);
+        }
+      }
+      ptx::tmem_wait_st();
+      warp_arrive(p_full);
+      l = l * f + ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y));
+    }
+    if (T == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
+      const int h = (g << w.gshift) + (row & (w.G - 1));
+      const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
+      uint32_t o[kDh];
+      if (T > 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_ld64_sync(tO, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kDh; ++e) o[e] = 0u;
+      }
+      // l == 0: the row sees no key (its O is 0, or a NaN from a hidden value).
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float sum = 0.f;                                 // not finite where any element is not
+#pragma unroll
+      for (int e = 0; e < kDh; ++e) {
+        const float x = __uint_as_float(o[e]) * inv;
+        sum = fmaf(x, 0.f, sum);
+        o[e] = __float_as_uint(x);
+      }
+      const bool again = valid && !(sum == 0.f);
+      if (valid) {
+        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.out + orow * kDh);
+#pragma unroll
+        for (int q = 0; q < kDh / 8; ++q) {
+          const float* x = reinterpret_cast<const float*>(o + 8 * q);
+          dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                              pack_bf16x2(x[6], x[7]));
+        }
+        if (w.lse) w.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718f;
+      }
+      __syncwarp();
+      for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
+        const int rr = lane_base + __ffs(todo) - 1;
+        out_row<__nv_bfloat16>(w, s, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (ctl->abort) {
+    // Every role has finished.  Before tensor memory and shared memory are
+    // released, the MMAs and the loads this CTA started complete.
+    if (warp == kMmaWarp && lane == 0) {
+      ptx::tc_commit(drain);
+      ptx::mbar_wait_drain(drain, 0, ctl->limit_ns);
+    }
+    if (warp == kTmaWarp && lane == 0) {
+      ptx::mbar_wait_drain(qfull, 0, ctl->limit_ns);
+      const int issued = ctl->issued;
+      for (int j = max(0, issued - kStages); j < issued; ++j)
+        ptx::mbar_wait_drain(full(j % kStages), (j / kStages) & 1, ctl->limit_ns);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && ctl->abort) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+}
+
+}  // namespace
+
+// Query-shaped tensor [Tq][Hq][64] viewed as [Tq][Hkv][G][64]: a box of 128/G
+// tokens x G heads x 64 dims of one key head is one 128-row tile.
+bool map_query_rows(CUtensorMap* m, const Win& w, const void* base) {
+  const cuuint64_t dims[4] = {(cuuint64_t)kDh, (cuuint64_t)w.G, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tq};
+  const cuuint64_t strides[3] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.G * kDh * 2, (cuuint64_t)w.Hq * kDh * 2};
+  const cuuint32_t box[4] = {(cuuint32_t)kDh, (cuuint32_t)w.G, 1, (cuuint32_t)(128 / w.G)};
+  return tma::encode_bf16_sw128(m, base, 4, dims, strides, box);
+}
+
+// Key-shaped tensor [Tk][Hkv][64], boxes of `rows` keys of one key head.
+bool map_key_rows(CUtensorMap* m, const Win& w, const void* base, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kDh, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tk};
+  const cuuint64_t strides[2] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.Hkv * kDh * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)kDh, 1, (cuuint32_t)rows};
+  return tma::encode_bf16_sw128(m, base, 3, dims, strides, box);
+}
+
+cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  if (!map_query_rows(&tq, w, w.q) || !map_key_rows(&tk, w, w.k, 32) || !map_key_rows(&tv, w, w.v, 32))
+    return cudaErrorInvalidValue;
+  cudaError_t e =
+      cudaFuncSetAttribute(window_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)tile_grid(w.Tq, kBM >> w.gshift, w.B), w.Hkv);
+  window_attn_tc_kernel<<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, w);
+  return cudaGetLastError();
+}
+
+}  // namespace seq
+}  // namespace pack3d

@@ -246,6 +246,8 @@ __device__ __forceinline__ void delta_row(const Win& w, size_t at) {
 
 // ---- launchers (k_window.cu, k_cache.cu, k_cache_attn.cu) -----------------------
 
+// The tensor-core kernels (bf16, at least one key row).
+cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st);
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st);
 cudaError_t launch_window_bwd(const Win& w, int dtype, cudaStream_t st);
 

@@ -93,15 +93,16 @@ def test_values_of_every_size(p3, cuda_device, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_hidden_nan_and_infinity(p3, cuda_device, dtype):
-    """A NaN or an infinity in a row reaches exactly the results whose definition reads it."""
+    """A NaN or an infinity in a row reaches exactly the results whose definition reads it.  The others are held to
+    the definition without that row (a row that a product with 0 spoilt is computed again on another path, which
+    rounds its probabilities elsewhere: both are within the tolerance of the definition, not of the same bits)."""
     dev = cuda_device
     lens, W, S = [90, 260], 40, 3
     for bad_row, value in ((200, float("nan")), (95, float("inf")), (349, float("nan"))):
         q, k, v, dout = inputs(lens, lens, 4, 2, dtype, dev, 7, pad=9)
         cfg = p3.make_seq_config(Hq=4, Hkv=2, window=W, sinks=S, dtype="bf16" if dtype == torch.bfloat16 else "f32")
         cu = offsets(lens, dev)
-        clean, clean_lse = p3.window_attn(cfg, q, k, v, cu)
-        clean_grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, clean, clean_lse, dout)
+        r = ref.window(q[:350], k[:350], v[:350], lens, lens, W, S, cfg.softmax_scale, dout[:350])
         v[bad_row], k[bad_row] = value, value
         v[350:], k[350:], q[350:], dout[350:] = (float("nan"),) * 4      # rows of no sequence
         out, lse = p3.window_attn(cfg, q, k, v, cu)
@@ -110,21 +111,21 @@ def test_hidden_nan_and_infinity(p3, cuda_device, dtype):
         j, b = int(pos[bad_row]), int(seq[bad_row])
         reads = (seq == b) & (pos >= j) & ((pos - j < W) | (j < S))
         assert torch.isnan(out[:350][reads].float()).all()
-        assert torch.equal(out[:350][~reads], clean[:350][~reads])
-        assert torch.equal(lse[:350][~reads], clean_lse[:350][~reads])
+        ref.close(out[:350][~reads], r["out"][~reads], r["out_tol"][~reads], "out")
+        ref.close(lse[:350][~reads], r["lse"][~reads], r["lse_tol"][~reads], "lse")
         assert (out[350:] == 0).all()
         grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout)
         dq = grads[0][:350]
         assert torch.isnan(dq[reads].float()).any(-1).all()
-        assert torch.equal(dq[~reads], clean_grads[0][:350][~reads])
+        ref.close(dq[~reads], r["dq"][~reads], r["dq_tol"][~reads], "dq")
         # a key that only unspoilt queries see keeps its gradients
         spoilt = torch.zeros(350, dtype=torch.bool, device=dev)
         for i in torch.nonzero(reads).flatten().tolist():
             p = int(pos[i])
             spoilt |= (seq == b) & (pos <= p) & ((p - pos < W) | (pos < S))
-        for g, c in zip(grads[1:], clean_grads[1:]):
+        for g, n in zip(grads[1:], ("dk", "dv")):
             assert torch.isnan(g[:350][spoilt].float()).any(-1).all()
-            assert torch.equal(g[:350][~spoilt], c[:350][~spoilt])
+            ref.close(g[:350][~spoilt], r[n][~spoilt], r[n + "_tol"][~spoilt], n)
             assert (g[350:] == 0).all()
 
 
@@ -137,17 +138,17 @@ def test_hidden_query_nan(p3, cuda_device, dtype):
         q, k, v, dout = inputs(lens, lens, 4, 2, dtype, dev, 9)
         cfg = p3.make_seq_config(Hq=4, Hkv=2, window=W, sinks=S, dtype="bf16" if dtype == torch.bfloat16 else "f32")
         cu = offsets(lens, dev)
-        out, lse = p3.window_attn(cfg, q, k, v, cu)
-        clean = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout)
+        r = ref.window(q, k, v, lens, lens, W, S, cfg.softmax_scale, dout)
         (q if which == "q" else dout)[150] = float("nan")
         out, lse = p3.window_attn(cfg, q, k, v, cu)
         grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout)
         rows = torch.arange(310, device=dev) == 150
         j = torch.arange(310, device=dev)
         keys = (j <= 150) & ((150 - j < W) | (j < S))
-        assert torch.isnan(grads[0][rows].float()).all() and torch.equal(grads[0][~rows], clean[0][~rows])
-        for g, c in zip(grads[1:], clean[1:]):
-            assert torch.equal(g[~keys], c[~keys])
+        assert torch.isnan(grads[0][rows].float()).all()
+        ref.close(grads[0][~rows], r["dq"][~rows], r["dq_tol"][~rows], "dq")
+        for g, n in zip(grads[1:], ("dk", "dv")):
+            ref.close(g[~keys], r[n][~keys], r[n + "_tol"][~keys], n)
             assert torch.isnan(g[keys].float()).any(-1).all()
 
 
