@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win 
 }  // namespace
 
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st) {
-  if (dtype == PACK3D_BF16 && w.Tk > 0) return launch_window_attn_tc(w, st);
+  if (dtype == PACK3D_BF16 && w.Tk > 0) return launch_window_attn_tc(w, st);   // Tq > 0: checked by the caller
   const dim3 grid((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq);
   if (dtype == PACK3D_BF16) window_rows_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(w);
   else window_rows_kernel<float><<<grid, 32 * kWarps, 0, st>>>(w);
@@ -69,6 +69,7 @@ cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st) {
 }
 
 cudaError_t launch_window_bwd(const Win& w, int dtype, cudaStream_t st) {
+  if (dtype == PACK3D_BF16 && w.Tq > 0 && w.Tk > 0) return launch_window_bwd_tc(w, st);
   const dim3 gq((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq), gk((unsigned)tile_grid(w.Tk, kWarps, w.B), w.Hkv);
   if (dtype == PACK3D_BF16) {
     window_dq_rows_kernel<__nv_bfloat16><<<gq, 32 * kWarps, 0, st>>>(w);

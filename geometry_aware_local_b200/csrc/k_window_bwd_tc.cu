@@ -1,0 +1,797 @@
+// Gradients of the causal windowed attention on sm_100a tensor cores (bf16).
+//
+// With c = scale log2(e), lse2 the row's log-sum-exp in base 2 and
+// D = <dout, out>, over the visible pairs:
+//   P = 2^(c S - lse2), S = Q K^T (recomputed),  dP = dout V^T,  dS = P (dP - D)
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dout.
+//
+// window_dq_tc_kernel: one 128-row query tile of one key head per CTA (rows,
+//   key range and sinks as in the forward), 64 keys a step, two CTAs per SM.
+//   S and dP go to tensor memory (N = the step's columns, K = 64); the softmax
+//   warps (thread = row) write dS as packed bf16 into tensor memory; dQ += dS K
+//   with the same K tile read MN-major.  It also forms D of its rows and
+//   leaves it for the second kernel.
+//
+// window_dkv_tc_kernel: one 128-key tile of one key head per CTA and the
+//   queries whose window reaches it, 128 rows a step, one CTA per SM.  S and dP
+//   (M = 128 rows, N = 128 keys) go to tensor memory; four softmax warpgroups
+//   (one per 32-key chunk) write dS and P as bf16 into shared memory,
+//   MN-major; a second MMA warp accumulates dK += dS^T Q and dV += P^T dout
+//   (M = 128 keys, N = 64, K = 128 rows) in tensor memory.  Chunks that no row
+//   of the step sees are written as zeros without an exponential.
+//
+// The first key tile of a sequence holds its sinks, which every later query
+// sees.  Their gradients from the queries beyond the tile's window are formed
+// by further CTAs of the same kernel, kFarSteps query tiles each, which like
+// the tile itself leave float partial sums of the sink rows; window_sink_kernel
+// adds them in a fixed order.  No atomics: the same inputs give the same bits.
+//
+// A gradient row that is not finite may be spoilt by 0 times a NaN or an
+// infinity of a row it does not depend on; it is computed again from its
+// visible pairs alone (dq_row, dkv_row).
+#include "seq_tc.cuh"
+
+namespace pack3d {
+namespace seq {
+namespace {
+
+constexpr int kQTileBytes = kRowsPerTile * kDh * 2;   // 16 KiB
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  ptx::tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
+
+// ============================================================================
+// Query side
+// ============================================================================
+namespace q_side {
+
+constexpr int kBN = 64;
+constexpr int kThreads = 192;                   // 4 softmax warps, MMA warp, TMA warp
+constexpr int kMmaWarp = 4, kTmaWarp = 5;
+constexpr int kColS = 0, kColDP = kBN, kColDS = 2 * kBN, kColDQ = 2 * kBN + kBN / 2, kTmemCols = 256;
+static_assert(kColDQ + kDh <= kTmemCols, "tensor memory plan");
+constexpr int kKVBytes = kBN * kDh * 2;         // 8 KiB
+constexpr int kStages = 4;
+constexpr int kQOff = 0, kDOOff = kQTileBytes, kStageOff = 2 * kQTileBytes;
+constexpr int kStageBytes = 2 * kKVBytes;       // K at +0, V at +kKVBytes
+constexpr int kBarOff = kStageOff + kStages * kStageBytes;
+// barriers: full[S], empty[S], qfull, s_full, s_free, p_full, p_free, o_final, drain
+constexpr int kNumBars = 2 * kStages + 7;
+constexpr int kCtlOff = kBarOff + kNumBars * 8;
+constexpr int kTileOff = kCtlOff + 32;
+constexpr int kSmemBytes = kTileOff + 64 + 1024;
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(sizeof(Tile) + sizeof(Tiles) + 4 <= 64 && kBarOff % 8 == 0, "tile slot");
+constexpr uint32_t kIdescDQ = ptx::idesc_bf16_f32(kRowsPerTile, kDh, true);  // dQ: N = 64 dims, K MN-major
+
+__global__ void __launch_bounds__(kThreads, 2)
+window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Win w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y;
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const uint32_t bar0 = sbase + kBarOff;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  const uint32_t qfull = bar0 + 8 * (2 * kStages);
+  const uint32_t s_full = qfull + 8, s_free = qfull + 16, p_full = qfull + 24, p_free = qfull + 32,
+                 o_final = qfull + 40, drain = qfull + 48;
+  volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
+  Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
+  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
+  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  const int tokens = kRowsPerTile >> w.gshift;
+
+  if (warp == 0) {
+    Tile s;
+    Tiles all;
+    const bool found = find_tile(w, blockIdx.x, tokens, false, &s, &all);
+    if (lane == 0) {
+      *tile_slot = s;
+      *tiles_slot = all;
+      *found_slot = found;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(qfull, 1);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(s_free, 4);
+    ptx::mbar_init(p_full, 4);
+    ptx::mbar_init(p_free, 1);
+    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(drain, 1);
+    ctl->abort = 0;
+    ctl->issued = 0;
+    ctl->limit_ns = w.wait_ns;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  if (!*found_slot) {
+    const Tiles all = *tiles_slot;
+    if (all.bad) {
+      if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
+    } else if (w.zero_outside && blockIdx.y == 0) {
+      fill_outside(w, w.cu_q, w.Tq, w.dq, w.Hq * kDh / 2, 0u, blockIdx.x, gridDim.x, all);
+    }
+    return;
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Tile s = *tile_slot;
+  s.t = s.n - 1 - s.t;      // the tiles with most keys first
+  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
+  const int p0 = position(s, r0), p1 = position(s, r1);
+  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
+  const int T = kt.n;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0 && T > 0) {
+      ptx::tma_prefetch(&tmQ);
+      ptx::tma_prefetch(&tmO);
+      ptx::tma_prefetch(&tmK);
+      ptx::tma_prefetch(&tmV);
+      ptx::mbar_expect_tx(qfull, 2 * kQTileBytes);
+      ptx::tma_load_4d(sbase + kQOff, &tmQ, 0, 0, g, s.q0 + r0, qfull);
+      ptx::tma_load_4d(sbase + kDOOff, &tmO, 0, 0, g, s.q0 + r0, qfull);
+      const int T_load = w.stall ? T - 1 : T;
+      int issued = 0;
+      for (int j = 0; j < T_load; ++j) {
+        const int st = j % kStages;
+        if (j >= kStages && !wait(empty(st), ((j / kStages) - 1) & 1)) break;
+        const uint32_t dst = sbase + kStageOff + st * kStageBytes;
+        const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
+        ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
+        for (int c = 0; c < cols / 32; ++c) {
+          ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
+          ptx::tma_load_3d(dst + kKVBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
+        }
+        issued = j + 1;
+      }
+      ctl->issued = issued;
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && T > 0) {
+      const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDS = tmem + kColDS, tDQ = tmem + kColDQ;
+      auto issue_sdp = [&](int j) {
+        const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
+        const uint32_t vaddr = kaddr + kKVBytes;
+        const uint32_t idesc = ptx::idesc_bf16_f32(kRowsPerTile, kt.cols(j), false);
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk)
+          ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kQOff + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(kaddr + kk * 32, 16, 1024), idesc, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk)
+          ptx::mma_ss(tDP, ptx::smem_desc_sw128(sbase + kDOOff + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(vaddr + kk * 32, 16, 1024), idesc, kk > 0);
+        ptx::tc_commit(s_full);
+      };
+      auto issue_dq = [&](int j) {
+        const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
+        const int steps = kt.cols(j) / 16;
+        for (int kk = 0; kk < steps; ++kk)
+          ptx::mma_ts(tDQ, tDS + kk * 8, ptx::smem_desc_sw128(kaddr + kk * 2048, 8192, 1024), kIdescDQ,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(p_free);
+        ptx::tc_commit(empty(j % kStages));
+        if (j == T - 1) ptx::tc_commit(o_final);
+      };
+      bool ok = wait(qfull, 0) && wait(full(0), 0);
+      if (ok) {
+        ptx::tc_fence_after();
+        issue_sdp(0);
+      }
+      for (int j = 0; ok && j < T; ++j) {
+        if (j + 1 < T) {
+          if (!(ok = wait(s_free, j & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
+          ptx::tc_fence_after();
+          issue_sdp(j + 1);
+        }
+        if (!(ok = wait(p_full, j & 1))) break;
+        ptx::tc_fence_after();
+        issue_dq(j);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax warps: thread = row = tensor-memory lane ----------------
+    const int lane_base = warp * 32;
+    const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
+    const int row = lane_base + lane;
+    const int r = r0 + (row >> w.gshift);
+    const bool valid = r <= r1;
+    const int h = (g << w.gshift) + (row & (w.G - 1));
+    const size_t orow = (size_t)(s.q0 + (valid ? r : r0)) * w.Hq + h;
+    const int p = valid ? position(s, r) : -1;
+    const int low = window_low(w, p), low_last = window_low(w, p1);
+    // D of the row, in float from the bf16 rows; rows past the sequence see
+    // nothing, whatever their lse2 and D are.
+    float delta = 0.f, lse2 = 0.f;
+    if (valid) {
+      const uint4* a = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.out + orow * kDh);
+      const uint4* d = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.dout + orow * kDh);
+      float x[8], y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        chunk_to_float(__ldg(a + i), x, __nv_bfloat16());
+        chunk_to_float(__ldg(d + i), y, __nv_bfloat16());
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+      }
+      w.delta[orow] = delta;
+      const float lse = w.lse[orow];
+      lse2 = p >= 0 ? lse * kLog2e : 0.f;
+    }
+    const float2 c2 = make_float2(w.scale_log2, w.scale_log2), nl2 = make_float2(-lse2, -lse2);
+    const float2 nd2 = make_float2(-delta, -delta);
+    bool ok = true;
+    for (int j = 0; j < T; ++j) {
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
+      ptx::tc_fence_after();
+      const int k0 = kt.begin(j), cols = kt.cols(j);
+      uint32_t sv[64], dv[64];
+      if (cols == 64) {
+        ptx::tmem_ld64_sync(trow + kColS, sv);
+        ptx::tmem_ld64_sync(trow + kColDP, dv);
+      } else {
+        ptx::tmem_ld32_sync(trow + kColS, sv);
+        ptx::tmem_ld32_sync(trow + kColDP, dv);
+      }
+      warp_arrive(s_free);
+      uint32_t pk[32];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (32 * q >= cols) break;
+        const int c0 = k0 + 32 * q;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = 32 * q + 2 * k;
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2);
+          const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd2);
+          const float2 ds = __fmul2_rn(make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), t);
+          pk[16 * q + k] = pack_bf16x2(ds.x, ds.y);
+        }
+        if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {   // some row sees the chunk in part
+          const uint32_t see = visible_bits(w, p, low, c0);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t keep = ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+            pk[16 * q + k] &= keep;
+          }
+        }
+      }
+      // dS of the previous step is read by its dQ MMAs until p_free: wait only
+      // now, so this step's exponentials overlap them.
+      if (j > 0) {
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free, (j - 1) & 1)))) break;
+        ptx::tc_fence_after();
+      }
+      ptx::tmem_st16(trow + kColDS, pk);
+      if (cols == 64) ptx::tmem_st16(trow + kColDS + 16, pk + 16);
+      ptx::tmem_wait_st();
+      warp_arrive(p_full);
+    }
+    if (T == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
+      uint32_t o[kDh];
+      if (T > 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_ld64_sync(trow + kColDQ, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kDh; ++e) o[e] = 0u;
+      }
+      float sum = 0.f;                                 // not finite where any element is not
+#pragma unroll
+      for (int e = 0; e < kDh; ++e) {
+        const float x = __uint_as_float(o[e]) * w.scale;
+        sum = fmaf(x, 0.f, sum);
+        o[e] = __float_as_uint(x);
+      }
+      const bool again = valid && !(sum == 0.f);
+      if (valid) {
+        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.dq + orow * kDh);
+#pragma unroll
+        for (int q = 0; q < kDh / 8; ++q) {
+          const float* x = reinterpret_cast<const float*>(o + 8 * q);
+          dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                              pack_bf16x2(x[6], x[7]));
+        }
+      }
+      __syncwarp();
+      for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
+        const int rr = lane_base + __ffs(todo) - 1;
+        dq_row<__nv_bfloat16>(w, s, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (ctl->abort) {
+    // Every role has finished: the MMAs and loads this CTA started complete
+    // before its tensor and shared memory are released.
+    if (warp == kMmaWarp && lane == 0) {
+      ptx::tc_commit(drain);
+      ptx::mbar_wait_drain(drain, 0, ctl->limit_ns);
+    }
+    if (warp == kTmaWarp && lane == 0) {
+      ptx::mbar_wait_drain(qfull, 0, ctl->limit_ns);
+      const int issued = ctl->issued;
+      for (int j = max(0, issued - kStages); j < issued; ++j)
+        ptx::mbar_wait_drain(full(j % kStages), (j / kStages) & 1, ctl->limit_ns);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && ctl->abort) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+}
+
+}  // namespace q_side
+
+// ============================================================================
+// Key side
+// ============================================================================
+namespace k_side {
+
+constexpr int kKeys = 128;                      // keys per CTA (M of the dK / dV accumulators)
+constexpr int kSoftmaxWarps = 16;               // four warpgroups, one 32-key chunk each
+// Two MMA warps: the first issues each step's S and dP, the second its dK / dV
+// accumulation, so that S and dP of the next step never queue behind it.
+constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kMmaWarp = kSoftmaxWarps, kMmaWarp2 = kSoftmaxWarps + 1, kTmaWarp = kSoftmaxWarps + 2;
+constexpr int kColS = 0, kColDP = 128, kColDK = 256, kColDV = 320, kTmemCols = 512;
+constexpr int kKeyTileBytes = kKeys * kDh * 2;  // 16 KiB
+// The operand buffer holds dS^T (two 16 KiB halves: keys 0-63, 64-127) and then P^T.
+constexpr int kOpBytes = 4 * kQTileBytes, kPInOp = 2 * kQTileBytes;
+constexpr int kKOff = 0, kVOff = kKeyTileBytes, kStageOff = 2 * kKeyTileBytes;
+constexpr int kStageBytes = 2 * kQTileBytes;    // Q at +0, dout at +kQTileBytes
+constexpr int kStages = 4;
+constexpr int kOpOff = kStageOff + kStages * kStageBytes;
+constexpr int kBarOff = kOpOff + kOpBytes;
+// barriers: full[S], empty[S], kvfull, o_final, s_full, s_free, p_full, p_free, drain[2]
+constexpr int kNumBars = 2 * kStages + 8;
+constexpr int kCtlOff = kBarOff + kNumBars * 8;
+constexpr int kTileOff = kCtlOff + 32;
+constexpr int kRedoOff = kTileOff + 64;         // one byte per key row
+constexpr int kSmemBytes = kRedoOff + kKeys + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRowsPerTile, kKeys, false);      // S, dP: N = 128 keys
+constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32_ab(kKeys, kDh, true, true);      // dK, dV: A, B MN-major
+
+// Query tiles a CTA of the sinks' far queries takes: long enough that its
+// partial sums (at most 64 rows x 128 floats) are small beside what it reads.
+constexpr int kFarSteps = 16;
+
+// First query row of a sequence beyond the windows of its first key tile: from
+// there on only the sinks of that tile are seen.  lq where there is none.
+__device__ __forceinline__ int far_begin(const Win& w, int lq, int lk) {
+  if (w.sinks == 0 || w.window == 0) return lq;
+  const long r = (long)min(kKeys, lk) - 1 + w.window - (lk - lq);     // past the last position that sees the last key
+  return (int)min((long)lq, max(0L, r));
+}
+__device__ __forceinline__ int far_chunks(const Win& w, int lq, int lk) {
+  if (lk == 0) return 0;
+  const int per = kFarSteps * (kRowsPerTile >> w.gshift);
+  return (lq - far_begin(w, lq, lk) + per - 1) / per;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Win w,
+                     int key_grid) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y;
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const uint32_t bar0 = sbase + kBarOff;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  const uint32_t kvfull = bar0 + 8 * (2 * kStages);
+  const uint32_t o_final = kvfull + 8, s_full = kvfull + 16, s_free = kvfull + 24, p_full = kvfull + 32,
+                 p_free = kvfull + 40;
+  auto drain = [&](int i) { return kvfull + 48 + 8 * i; };
+  volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
+  Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
+  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
+  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
+  volatile uint8_t* redo = smem + kRedoOff;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  const int tokens = kRowsPerTile >> w.gshift;
+  const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
+  const int x = far ? blockIdx.x - key_grid : blockIdx.x;
+
+  if (warp == 0) {
+    Tile s;
+    Tiles all;
+    const bool found = far ? find_piece(w, x, [&](int lq, int lk) { return far_chunks(w, lq, lk); }, &s, &all)
+                           : find_tile(w, x, kKeys, true, &s, &all);
+    if (lane == 0) {
+      *tile_slot = s;
+      *tiles_slot = all;
+      *found_slot = found;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(kvfull, 1);
+    ptx::mbar_init(s_full, 1);
+    ptx::mbar_init(s_free, kSoftmaxWarps);
+    ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(p_full, kSoftmaxWarps);
+    ptx::mbar_init(p_free, 1);
+    ptx::mbar_init(drain(0), 1);
+    ptx::mbar_init(drain(1), 1);
+    ctl->abort = 0;
+    ctl->issued = 0;
+    ctl->limit_ns = w.wait_ns;
+    ptx::fence_mbar_init();
+  }
+  if (threadIdx.x < kKeys) redo[threadIdx.x] = 0;
+  __syncthreads();
+  if (!*found_slot) {
+    const Tiles all = *tiles_slot;
+    if (!far && !all.bad && w.zero_outside && blockIdx.y == 0) {
+      fill_outside(w, w.cu_k, w.Tk, w.dk, w.Hkv * kDh / 2, 0u, x, key_grid, all);
+      fill_outside(w, w.cu_k, w.Tk, w.dv, w.Hkv * kDh / 2, 0u, x, key_grid, all);
+    }
+    return;
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Tile s = *tile_slot;
+  // Keys j0 .. of the sequence and the query rows ra .. rb that see some of them.
+  const int shift = s.lk - s.lq;                        // position minus row
+  const int j0 = far ? 0 : s.t * kKeys, j1 = min(s.lk, j0 + kKeys) - 1;
+  int ra, rb;
+  if (far) {
+    ra = far_begin(w, s.lq, s.lk) + s.t * kFarSteps * tokens;
+    rb = min(s.lq, ra + kFarSteps * tokens) - 1;
+  } else {
+    ra = max(0, j0 - shift);
+    rb = s.lq - 1;
+    if (w.window > 0) rb = min(rb, j1 + w.window - 1 - shift);
+  }
+  const int nsteps = rb >= ra ? (rb - ra) / tokens + 1 : 0;
+  // Rows below `split_rows` of this tile leave float partial sums.
+  const int split_rows = far || (j0 == 0 && far_chunks(w, s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0 && nsteps > 0) {
+      ptx::tma_prefetch(&tmQ);
+      ptx::tma_prefetch(&tmO);
+      ptx::tma_prefetch(&tmK);
+      ptx::tma_prefetch(&tmV);
+      ptx::mbar_expect_tx(kvfull, 2 * kKeyTileBytes);
+      ptx::tma_load_3d(sbase + kKOff, &tmK, 0, g, s.k0 + j0, kvfull);
+      ptx::tma_load_3d(sbase + kVOff, &tmV, 0, g, s.k0 + j0, kvfull);
+      const int nsteps_load = w.stall ? nsteps - 1 : nsteps;
+      int issued = 0;
+      for (int t = 0; t < nsteps_load; ++t) {
+        const int st = t % kStages;
+        if (t >= kStages && !wait(empty(st), ((t / kStages) - 1) & 1)) break;
+        const uint32_t dst = sbase + kStageOff + st * kStageBytes;
+        const int tok0 = s.q0 + ra + t * tokens;
+        ptx::mbar_expect_tx(full(st), kStageBytes);
+        ptx::tma_load_4d(dst, &tmQ, 0, 0, g, tok0, full(st));
+        ptx::tma_load_4d(dst + kQTileBytes, &tmO, 0, 0, g, tok0, full(st));
+        issued = t + 1;
+      }
+      ctl->issued = issued;
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
+    if (lane == 0 && nsteps > 0) {
+      const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDK = tmem + kColDK, tDV = tmem + kColDV;
+      auto issue_sdp = [&](int t) {
+        const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
+        const uint32_t oaddr = qaddr + kQTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk)
+          ptx::mma_ss(tS, ptx::smem_desc_sw128(qaddr + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024), kIdescS, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk)
+          ptx::mma_ss(tDP, ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024), kIdescS, kk > 0);
+        ptx::tc_commit(s_full);
+      };
+      auto issue_dkv = [&](int t) {
+        const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
+        const uint32_t oaddr = qaddr + kQTileBytes;
+        const uint32_t op = sbase + kOpOff;
+#pragma unroll
+        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
+          ptx::mma_ss(tDK, ptx::smem_desc_sw128(op + kk * 2048, 2 * 8192, 1024),
+                      ptx::smem_desc_sw128(qaddr + kk * 2048, 8192, 1024), kIdescKV, (t > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
+          ptx::mma_ss(tDV, ptx::smem_desc_sw128(op + kPInOp + kk * 2048, 2 * 8192, 1024),
+                      ptx::smem_desc_sw128(oaddr + kk * 2048, 8192, 1024), kIdescKV, (t > 0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(p_free);
+        ptx::tc_commit(empty(t % kStages));
+        if (t == nsteps - 1) ptx::tc_commit(o_final);
+      };
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        ok = wait(kvfull, 0);
+        for (int t = 0; ok && t < nsteps; ++t) {
+          if (!(ok = wait(full(t % kStages), (t / kStages) & 1))) break;
+          if (t > 0 && !(ok = wait(s_free, (t - 1) & 1))) break;
+          ptx::tc_fence_after();
+          issue_sdp(t);
+        }
+      } else {
+        for (int t = 0; ok && t < nsteps; ++t) {
+          if (!(ok = wait(p_full, t & 1))) break;
+          ptx::tc_fence_after();
+          issue_dkv(t);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax warps: thread = query row of the step ----------------
+    const int c = warp >> 2;                     // 32-key chunk of the tile
+    const int lane_base = (warp & 3) * 32;
+    const int rl = lane_base + lane;             // row inside the step's tile
+    const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
+    const float2 c2 = make_float2(w.scale_log2, w.scale_log2);
+    const int h = (g << w.gshift) + (rl & (w.G - 1));
+    const int c0 = j0 + 32 * c;                  // the chunk's first key
+    bool ok = true;
+    for (int t = 0; t < nsteps; ++t) {
+      const int rs = ra + t * tokens;            // the step's first row
+      const int r = rs + (rl >> w.gshift);
+      const bool valid = r <= rb;
+      const int p = valid ? r + shift : -1;
+      float lse2 = 0.f, delta = 0.f;
+      if (valid && p >= 0) {
+        const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
+        lse2 = __ldg(w.lse + orow) * kLog2e;
+        delta = __ldg(w.delta + orow);
+      }
+      const int ps = rs + shift, pe = min(rs + tokens - 1, rb) + shift;   // the step's positions
+      // Whether any row of the step sees a key of the chunk, and whether all rows see all of it.
+      const bool some = c0 <= j1 && c0 <= pe && (c0 + 31 >= window_low(w, max(ps, 0)) || c0 < w.sinks) &&
+                        !(far && c0 >= w.sinks);
+      const bool whole = !far && c0 + 31 <= ps && c0 >= window_low(w, pe) && rs + tokens - 1 <= rb;
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full, t & 1)))) break;
+      ptx::tc_fence_after();
+      uint32_t pd[16], pp[16];
+      if (some) {
+        uint32_t sv[32], dv[32];
+        ptx::tmem_ld32x2_sync(trow + kColS + 32 * c, trow + kColDP + 32 * c, sv, dv);
+        warp_arrive(s_free);
+        const float2 nl2 = make_float2(-lse2, -lse2), nd2 = make_float2(-delta, -delta);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), c2, nl2);
+          const float2 tt = __fadd2_rn(make_float2(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])), nd2);
+          const float2 pr = make_float2(ptx::ex2(xx.x), ptx::ex2(xx.y));
+          const float2 ds = __fmul2_rn(pr, tt);
+          pd[k] = pack_bf16x2(ds.x, ds.y);
+          pp[k] = pack_bf16x2(pr.x, pr.y);
+        }
+        if (!whole) {
+          const uint32_t see = visible_bits(w, p, window_low(w, p), c0);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t keep = ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+            pd[k] &= keep;
+            pp[k] &= keep;
+          }
+        }
+      } else {
+        warp_arrive(s_free);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pd[k] = pp[k] = 0u;
+      }
+      // The previous step's dK / dV MMAs read the operand buffer: wait for them
+      // only now, so this step's exponentials overlap them.
+      if (t > 0 && !(ok = __all_sync(0xffffffffu, wait(p_free, (t - 1) & 1)))) break;
+      // Row rl of the MN-major operands: keys 32c .. 32c+31 are 16-byte chunks
+      // (c & 1) * 4 + m of half c / 2.
+      const uint32_t op = sbase + kOpOff + (uint32_t)(c >> 1) * kQTileBytes;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t off = ptx::sw128_offset((uint32_t)rl, (uint32_t)(((c & 1) * 4 + m) * 8));
+        ptx::st_shared_v4(op + off, pd[4 * m], pd[4 * m + 1], pd[4 * m + 2], pd[4 * m + 3]);
+        ptx::st_shared_v4(op + kPInOp + off, pp[4 * m], pp[4 * m + 1], pp[4 * m + 2], pp[4 * m + 3]);
+      }
+      ptx::fence_proxy_async_smem();
+      warp_arrive(p_full);
+    }
+    if (nsteps == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
+      // Accumulator lane = key of this tile.  The warpgroups share the 128
+      // accumulator columns (dK 64, then dV 64): 32 each.
+      const int col0 = 32 * c;
+      const bool is_k = col0 < kDh;
+      uint32_t o[32];
+      if (nsteps > 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_ld32_sync(trow + kColDK + col0, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      const float f = is_k ? w.scale : 1.f;
+      float sum = 0.f;                                 // not finite where any element is not
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const float y = __uint_as_float(o[e]) * f;
+        sum = fmaf(y, 0.f, sum);
+        o[e] = __float_as_uint(y);
+      }
+      // Partial sums of the sink rows.  A sequence's first slot is its tile's,
+      // the next ones its far CTAs' (x counts the far CTAs of all sequences).
+      int slot = x + s.b + 1;
+      if (split_rows > 0 && !far)
+        slot = pieces_before(w, s.b, [&](int lq, int lk) { return far_chunks(w, lq, lk); }) + s.b;
+      if (rl < split_rows) {
+        float4* dst = reinterpret_cast<float4*>(w.part + (((size_t)slot * w.Hkv + g) * w.sinks + rl) * 2 * kDh + col0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                               __uint_as_float(o[4 * q + 3]));
+      } else if (!far && j0 + rl <= j1) {
+        __nv_bfloat16* base = (__nv_bfloat16*)(is_k ? w.dk : w.dv);
+        uint4* dst = reinterpret_cast<uint4*>(base + ((size_t)(s.k0 + j0 + rl) * w.Hkv + g) * kDh + (col0 % kDh));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* y = reinterpret_cast<const float*>(o + 8 * q);
+          dst[q] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                              pack_bf16x2(y[6], y[7]));
+        }
+        if (!(sum == 0.f)) redo[rl] = 1;
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (ctl->abort) {
+    // Every role has finished: the MMAs of both issuing warps and the
+    // producer's loads complete before tensor and shared memory are released.
+    if ((warp == kMmaWarp || warp == kMmaWarp2) && lane == 0) {
+      const uint32_t d = drain(warp - kMmaWarp);
+      ptx::tc_commit(d);
+      ptx::mbar_wait_drain(d, 0, ctl->limit_ns);
+    }
+    if (warp == kTmaWarp && lane == 0) {
+      ptx::mbar_wait_drain(kvfull, 0, ctl->limit_ns);
+      const int issued = ctl->issued;
+      for (int t = max(0, issued - kStages); t < issued; ++t)
+        ptx::mbar_wait_drain(full(t % kStages), (t / kStages) & 1, ctl->limit_ns);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (ctl->abort) {
+    if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+    return;
+  }
+  for (int rl = warp; rl < kKeys; rl += kThreads / 32)
+    if (redo[rl]) dkv_row<__nv_bfloat16>(w, s, j0 + rl, g);
+}
+
+// dK and dV of the sink rows of sequences with far queries: the tile's partial
+// sums and the far CTAs', added in order.  One CTA per (sequence, key head),
+// one warp per sink row.
+__global__ void __launch_bounds__(256) window_sink_kernel(const Win w) {
+  const int b = blockIdx.x, g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Tile s;
+  Tiles all;
+  find_tile(w, 0, 1, false, &s, &all);        // checks the offsets
+  if (all.bad) return;
+  s.b = b;
+  s.q0 = __ldg(w.cu_q + b);
+  s.lq = __ldg(w.cu_q + b + 1) - s.q0;
+  s.k0 = __ldg(w.cu_k + b);
+  s.lk = __ldg(w.cu_k + b + 1) - s.k0;
+  s.t = 0;
+  s.n = far_chunks(w, s.lq, s.lk);
+  if (s.n == 0) return;
+  const int before = pieces_before(w, b, [&](int lq, int lk) { return far_chunks(w, lq, lk); });
+  for (int j = warp; j < min(w.sinks, s.lk); j += 8) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i <= s.n; ++i) {
+      const float4 y = *reinterpret_cast<const float4*>(
+          w.part + (((size_t)(before + b + i) * w.Hkv + g) * w.sinks + j) * 2 * kDh + 4 * lane);
+      sum.x += y.x;
+      sum.y += y.y;
+      sum.z += y.z;
+      sum.w += y.w;
+    }
+    // Lanes 0-15 hold dK's 64 dims, 16-31 dV's.
+    const size_t at = ((size_t)(s.k0 + j) * w.Hkv + g) * kDh;
+    __nv_bfloat16* base = (__nv_bfloat16*)(lane < 16 ? w.dk : w.dv) + at + 4 * (lane & 15);
+    *reinterpret_cast<uint2*>(base) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+    const float zero = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
+    const bool again = __any_sync(0xffffffffu, !(zero == 0.f));
+    __syncwarp();
+    if (again) dkv_row<__nv_bfloat16>(w, s, j, g);
+  }
+}
+
+// CTAs of the sinks' far queries, whatever the offsets are.
+long far_grid(const Win& w) {
+  if (w.sinks == 0 || w.window == 0) return 0;
+  return w.Tq / ((long)kFarSteps * (kRowsPerTile >> w.gshift)) + w.B;
+}
+
+}  // namespace k_side
+}  // namespace
+
+size_t window_bwd_part_bytes(const Win& w, int dtype) {
+  if (dtype != PACK3D_BF16 || w.sinks == 0 || w.window == 0) return 0;
+  // A slot for every sequence's first tile and one for every far CTA.
+  return (size_t)(k_side::far_grid(w) + w.B) * w.Hkv * w.sinks * 2 * kDh * sizeof(float);
+}
+
+cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
+  // First, so that a thread that has made no CUDA call yet (autograd's) has the
+  // device's context when the tensor maps are encoded.
+  cudaError_t e = cudaFuncSetAttribute(q_side::window_dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       q_side::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_side::window_dkv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             k_side::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tq, to, tk, tv, tk128, tv128;
+  if (!map_query_rows(&tq, w, w.q) || !map_query_rows(&to, w, w.dout) || !map_key_rows(&tk, w, w.k, 32) ||
+      !map_key_rows(&tv, w, w.v, 32) || !map_key_rows(&tk128, w, w.k, k_side::kKeys) ||
+      !map_key_rows(&tv128, w, w.v, k_side::kKeys))
+    return cudaErrorInvalidValue;
+  const dim3 gq((unsigned)tile_grid(w.Tq, kRowsPerTile >> w.gshift, w.B), w.Hkv);
+  q_side::window_dq_tc_kernel<<<gq, q_side::kThreads, q_side::kSmemBytes, st>>>(tq, to, tk, tv, w);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int key_grid = (int)tile_grid(w.Tk, k_side::kKeys, w.B);
+  const dim3 gk((unsigned)(key_grid + k_side::far_grid(w)), w.Hkv);
+  k_side::window_dkv_tc_kernel<<<gk, k_side::kThreads, k_side::kSmemBytes, st>>>(tq, to, tk128, tv128, w, key_grid);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || w.sinks == 0 || w.window == 0) return e;
+  k_side::window_sink_kernel<<<dim3(w.B, w.Hkv), 256, 0, st>>>(w);
+  return cudaGetLastError();
+}
+
+}  // namespace seq
+}  // namespace pack3d

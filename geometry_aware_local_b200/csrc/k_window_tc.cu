@@ -25,20 +25,16 @@
 // A key that a row does not see has P = 0 exactly; where its value row holds a
 // NaN or an infinity, 0 times it is a NaN.  A row whose result is not finite is
 // therefore computed again from its visible keys alone (out_row).
-#include <cuda.h>
-
-#include "seq.cuh"
-#include "tc_ptx.cuh"
-#include "tma_host.cuh"
+#include "seq_tc.cuh"
 
 namespace pack3d {
 namespace seq {
 namespace {
 
-constexpr int kBM = 128, kBN = 128;
+constexpr int kBM = kRowsPerTile, kBN = 128;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kThreads = 192;
 constexpr int kColS = 0, kColP = kBN, kColO = kBN + kBN / 2, kTmemCols = 256;
-constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2, kChunkBytes = 32 * kDh * 2;
+constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2;
 constexpr int kStages = 2;
 constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;     // K at +0, V at +kTileBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
@@ -56,42 +52,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// The tile's key tiles: number j starts at key begin(j) of the sequence and
-// has cols(j) columns, a multiple of 32.
-struct KeyTiles {
-  int lo, hi;       // the tile's range of keys
-  int sink_cols;    // columns of the sinks' tile in front of it, or 0
-  int n;
-  __device__ __forceinline__ int begin(int j) const {
-    return sink_cols ? (j == 0 ? 0 : lo + (j - 1) * kBN) : lo + j * kBN;
-  }
-  __device__ __forceinline__ int cols(int j) const {
-    return sink_cols && j == 0 ? sink_cols : min(kBN, (hi - begin(j) + 32) & ~31);
-  }
-};
-
-// Keys of the queries at positions p0 .. p1 (p0 <= p1) of a sequence.
-__device__ __forceinline__ KeyTiles key_tiles(const Win& w, int p0, int p1) {
-  KeyTiles k;
-  k.hi = p1;
-  k.sink_cols = 0;
-  if (p1 < 0) {
-    k.lo = 0;
-    k.n = 0;
-    return k;
-  }
-  k.lo = window_low(w, max(p0, 0));
-  const int sinks = min(w.sinks, k.lo);
-  // One range from key 0 where that takes no more columns than the sinks apart
-  // (it does where the sinks' columns would reach the window).
-  if (sinks > 0) {
-    if (((sinks + 31) & ~31) >= k.lo) k.lo = 0;
-    else k.sink_cols = (sinks + 31) & ~31;
-  }
-  k.n = (k.hi - k.lo) / kBN + 1 + (k.sink_cols ? 1 : 0);
-  return k;
 }
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -166,7 +126,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   s.t = s.n - 1 - s.t;      // the tiles with most keys first
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const int p0 = position(s, r0), p1 = position(s, r1);
-  const KeyTiles kt = key_tiles(w, p0, p1);
+  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
   const int T = kt.n;
 
   if (warp == kTmaWarp) {
@@ -272,11 +232,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         // Seen in full by every row of the tile: behind the last row's window
         // start and not past the first row's own key (and every row valid).
         if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {
-          const int a = max(low - c0, 0), z = p - c0;   // visible columns [a, z] and those below the sinks
-          uint32_t see = z < 0 ? 0u : (z >= 31 ? 0xffffffffu : (2u << z) - 1u);
-          const int first = min(max(w.sinks - c0, 0), 32);
-          const uint32_t sink = first >= 32 ? 0xffffffffu : (1u << first) - 1u;
-          see &= (a >= 32 ? 0u : 0xffffffffu << a) | sink;
+          const uint32_t see = visible_bits(w, p, low, c0);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (!((see >> k) & 1u)) sv[32 * q + k] = __float_as_uint(-INFINITY);
@@ -404,30 +360,15 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 
 }  // namespace
 
-// Query-shaped tensor [Tq][Hq][64] viewed as [Tq][Hkv][G][64]: a box of 128/G
-// tokens x G heads x 64 dims of one key head is one 128-row tile.
-bool map_query_rows(CUtensorMap* m, const Win& w, const void* base) {
-  const cuuint64_t dims[4] = {(cuuint64_t)kDh, (cuuint64_t)w.G, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tq};
-  const cuuint64_t strides[3] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.G * kDh * 2, (cuuint64_t)w.Hq * kDh * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)kDh, (cuuint32_t)w.G, 1, (cuuint32_t)(128 / w.G)};
-  return tma::encode_bf16_sw128(m, base, 4, dims, strides, box);
-}
-
-// Key-shaped tensor [Tk][Hkv][64], boxes of `rows` keys of one key head.
-bool map_key_rows(CUtensorMap* m, const Win& w, const void* base, int rows) {
-  const cuuint64_t dims[3] = {(cuuint64_t)kDh, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tk};
-  const cuuint64_t strides[2] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.Hkv * kDh * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)kDh, 1, (cuuint32_t)rows};
-  return tma::encode_bf16_sw128(m, base, 3, dims, strides, box);
-}
-
 cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st) {
-  CUtensorMap tq, tk, tv;
-  if (!map_query_rows(&tq, w, w.q) || !map_key_rows(&tk, w, w.k, 32) || !map_key_rows(&tv, w, w.v, 32))
-    return cudaErrorInvalidValue;
+  // First, so that a thread that has made no CUDA call yet (autograd's) has the
+  // device's context when the tensor maps are encoded.
   cudaError_t e =
       cudaFuncSetAttribute(window_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
+  CUtensorMap tq, tk, tv;
+  if (!map_query_rows(&tq, w, w.q) || !map_key_rows(&tk, w, w.k, 32) || !map_key_rows(&tv, w, w.v, 32))
+    return cudaErrorInvalidValue;
   const dim3 grid((unsigned)tile_grid(w.Tq, kBM >> w.gshift, w.B), w.Hkv);
   window_attn_tc_kernel<<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, w);
   return cudaGetLastError();

@@ -31,6 +31,7 @@ struct Win {
   void* dk;
   void* dv;
   float* delta;                   // workspace [Tq, Hq]: <dout, out>
+  float* part;                    // workspace: partial gradients of the sink rows
   int zero_outside;               // rows of no sequence become 0 instead of staying as they were
   int32_t* err;
   unsigned long long wait_ns;
@@ -61,12 +62,13 @@ __device__ __forceinline__ bool sees(const Win& w, int p, int j) {
   return j <= p && (j >= window_low(w, p) || j < w.sinks);
 }
 
-// Tile number x of all sequences' tiles (`per` rows of queries, or of keys with
-// over_keys, a tile; every sequence starts a new one), found by one warp: it
-// adds up the sequences' tile counts 32 at a time.  On the way it checks every
-// offset.  All 32 lanes call it and get the same answer: whether there is such
-// a tile (never where an offset is wrong).
-__device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool over_keys, Tile* out, Tiles* all) {
+// Piece number x of all sequences' pieces, count(lq, lk) of them for a sequence
+// of lq queries and lk keys, found by one warp: it adds up the counts 32
+// sequences at a time.  On the way it checks every offset.  All 32 lanes call
+// it and get the same answer: whether there is such a piece (never where an
+// offset is wrong).
+template <typename Count>
+__device__ __forceinline__ bool find_piece(const Win& w, int x, Count count, Tile* out, Tiles* all) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   bool found = false, wrong = false;
@@ -77,8 +79,7 @@ __device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool ove
     const int k0 = in ? __ldg(w.cu_k + b) : 0, k1 = in ? __ldg(w.cu_k + b + 1) : 0;
     const bool off = in && (q0 < 0 || q1 < q0 || q1 > w.Tq || k0 < 0 || k1 < k0 || k1 > w.Tk);
     wrong |= __any_sync(0xffffffffu, off);
-    const int rows = off ? 0 : (over_keys ? k1 - k0 : q1 - q0);
-    const int n = (rows + per - 1) / per;
+    const int n = !in || off ? 0 : count(q1 - q0, k1 - k0);
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -103,6 +104,22 @@ __device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool ove
   all->total = base;
   all->bad = wrong;
   return found && !wrong;
+}
+
+// Pieces of the sequences before sequence b (one warp; the offsets are known to
+// be right).
+template <typename Count>
+__device__ __forceinline__ int pieces_before(const Win& w, int b, Count count) {
+  int n = 0;
+  for (int i = threadIdx.x & 31; i < b; i += 32)
+    n += count(__ldg(w.cu_q + i + 1) - __ldg(w.cu_q + i), __ldg(w.cu_k + i + 1) - __ldg(w.cu_k + i));
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Tile number x of all sequences' tiles: `per` rows of queries, or of keys with
+// over_keys, a tile; every sequence starts a new one.
+__device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool over_keys, Tile* out, Tiles* all) {
+  return find_piece(w, x, [=](int lq, int lk) { return ((over_keys ? lk : lq) + per - 1) / per; }, out, all);
 }
 
 // Grid size that covers every tile whatever the offsets are, and has at least
@@ -246,8 +263,11 @@ __device__ __forceinline__ void delta_row(const Win& w, size_t at) {
 
 // ---- launchers (k_window.cu, k_cache.cu, k_cache_attn.cu) -----------------------
 
-// The tensor-core kernels (bf16, at least one key row).
+// The tensor-core kernels (bf16; at least one key row and one query row).
 cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st);
+cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st);
+// Bytes of Win::part for a call of this size.
+size_t window_bwd_part_bytes(const Win& w, int dtype);
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st);
 cudaError_t launch_window_bwd(const Win& w, int dtype, cudaStream_t st);
 

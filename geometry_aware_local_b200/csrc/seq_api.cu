@@ -94,8 +94,10 @@ seq::Cache make_cache(const pack3d_seq_config& c, int32_t batch, const int32_t* 
   return r;
 }
 
-size_t bwd_bytes(const pack3d_seq_config& c, int64_t q_rows) {
-  return ((size_t)q_rows * c.Hq * 4 + 1023) / 1024 * 1024;
+// The backward's workspace: Win::delta, then Win::part.
+size_t delta_bytes(const seq::Win& w) { return ((size_t)w.Tq * w.Hq * 4 + 1023) / 1024 * 1024; }
+size_t bwd_bytes(const seq::Win& w, int dtype) {
+  return delta_bytes(w) + (seq::window_bwd_part_bytes(w, dtype) + 1023) / 1024 * 1024;
 }
 
 }  // namespace
@@ -155,7 +157,7 @@ pack3d_status pack3d_window_attn(const pack3d_seq_config* cfg, int32_t batch, in
 size_t pack3d_window_attn_bwd_workspace_bytes(const pack3d_seq_config* cfg, int32_t batch, int64_t q_rows,
                                               int64_t k_rows) {
   if (pack3d_validate_seq_config(cfg) != PACK3D_OK || check_rows(batch, q_rows, k_rows) != PACK3D_OK) return 0;
-  return bwd_bytes(*cfg, q_rows);
+  return bwd_bytes(make_win(*cfg, batch, q_rows, k_rows, nullptr, nullptr), cfg->dtype);
 }
 
 pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config* cfg, int32_t batch, int64_t q_rows, int64_t k_rows,
@@ -170,13 +172,13 @@ pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config* cfg, int32_t batch
   if (!cu_q || !cu_k || (q_rows > 0 && (!q || !out || !lse || !dout || !dq)) ||
       (k_rows > 0 && (!k || !v || !dk || !dv)))
     return PACK3D_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < bwd_bytes(*cfg, q_rows))
+  seq::Win w = make_win(*cfg, batch, q_rows, k_rows, cu_q, cu_k);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < bwd_bytes(w, cfg->dtype))
     return PACK3D_ERR_WORKSPACE;
   const void* ptrs[] = {q, k, v, out, dout, dq, dk, dv};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return PACK3D_ERR_ALIGNMENT;
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return PACK3D_ERR_ALIGNMENT;
-  seq::Win w = make_win(*cfg, batch, q_rows, k_rows, cu_q, cu_k);
   w.q = q;
   w.k = k;
   w.v = v;
@@ -187,6 +189,7 @@ pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config* cfg, int32_t batch
   w.dk = dk;
   w.dv = dv;
   w.delta = (float*)workspace;
+  w.part = (float*)((char*)workspace + delta_bytes(w));
   w.zero_outside = zero_outside != 0;
   w.err = err_word;
   return cuda_status(seq::launch_window_bwd(w, cfg->dtype, (cudaStream_t)stream));

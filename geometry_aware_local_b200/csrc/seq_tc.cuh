@@ -1,0 +1,83 @@
+// Shared parts of the tensor-core kernels of the causal sequence operators: the
+// key tiles a query tile reads, the visibility of a 32-key chunk as a bit mask
+// and the TMA maps.
+#pragma once
+
+#include <cuda.h>
+
+#include "seq.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace pack3d {
+namespace seq {
+
+constexpr int kRowsPerTile = 128;                     // (token, query head) rows of a query tile
+constexpr int kChunkBytes = 32 * kDh * 2;             // 32 keys of one head
+
+// The key tiles of a query tile: number j starts at key begin(j) of the
+// sequence and has cols(j) columns, a multiple of 32, BN at most.
+template <int BN>
+struct KeyTiles {
+  int lo, hi;       // the tile's range of keys
+  int sink_cols;    // columns of the sinks' tile in front of it, or 0
+  int n;
+  __device__ __forceinline__ int begin(int j) const {
+    return sink_cols ? (j == 0 ? 0 : lo + (j - 1) * BN) : lo + j * BN;
+  }
+  __device__ __forceinline__ int cols(int j) const {
+    return sink_cols && j == 0 ? sink_cols : min(BN, (hi - begin(j) + 32) & ~31);
+  }
+};
+
+// Keys of the queries at positions p0 .. p1 (p0 <= p1) of a sequence.
+template <int BN>
+__device__ __forceinline__ KeyTiles<BN> key_tiles(const Win& w, int p0, int p1) {
+  KeyTiles<BN> k;
+  k.hi = p1;
+  k.sink_cols = 0;
+  if (p1 < 0) {
+    k.lo = 0;
+    k.n = 0;
+    return k;
+  }
+  k.lo = window_low(w, max(p0, 0));
+  const int sinks = min(w.sinks, k.lo);
+  // One range from key 0 where the sinks' columns would reach the window.
+  if (sinks > 0) {
+    if (((sinks + 31) & ~31) >= k.lo) k.lo = 0;
+    else k.sink_cols = (sinks + 31) & ~31;
+  }
+  k.n = (k.hi - k.lo) / BN + 1 + (k.sink_cols ? 1 : 0);
+  return k;
+}
+
+// Bit k: the query at position p (window start `low`) sees key c0 + k.  p < 0:
+// none.
+__device__ __forceinline__ uint32_t visible_bits(const Win& w, int p, int low, int c0) {
+  const int a = max(low - c0, 0), z = p - c0;
+  const uint32_t upto = z < 0 ? 0u : (z >= 31 ? 0xffffffffu : (2u << z) - 1u);
+  const int first = min(max(w.sinks - c0, 0), 32);
+  const uint32_t sink = first >= 32 ? 0xffffffffu : (1u << first) - 1u;
+  return upto & ((a >= 32 ? 0u : 0xffffffffu << a) | sink);
+}
+
+// Query-shaped tensor [Tq][Hq][64] viewed as [Tq][Hkv][G][64]: a box of 128/G
+// tokens x G heads x 64 dims of one key head is one 128-row tile.
+inline bool map_query_rows(CUtensorMap* m, const Win& w, const void* base) {
+  const cuuint64_t dims[4] = {(cuuint64_t)kDh, (cuuint64_t)w.G, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tq};
+  const cuuint64_t strides[3] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.G * kDh * 2, (cuuint64_t)w.Hq * kDh * 2};
+  const cuuint32_t box[4] = {(cuuint32_t)kDh, (cuuint32_t)w.G, 1, (cuuint32_t)(kRowsPerTile / w.G)};
+  return tma::encode_bf16_sw128(m, base, 4, dims, strides, box);
+}
+
+// Key-shaped tensor [Tk][Hkv][64], boxes of `rows` keys of one key head.
+inline bool map_key_rows(CUtensorMap* m, const Win& w, const void* base, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kDh, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tk};
+  const cuuint64_t strides[2] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.Hkv * kDh * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)kDh, 1, (cuuint32_t)rows};
+  return tma::encode_bf16_sw128(m, base, 3, dims, strides, box);
+}
+
+}  // namespace seq
+}  // namespace pack3d
