@@ -1,94 +1,701 @@
-// Attention of one new token per sequence over the paged cache, one warp per
-// (sequence, query head).
+// Attention of one new token per sequence over the paged cache.
+//
+// Every visible key and value row is read once and serves the G query heads of
+// its key head; there is no reuse beyond that, so HBM bounds the work and the
+// kernels read straight into registers, one tile of 16 slots ahead, without
+// shared memory.
+//
+// Split and join.  The work is one line of units - (sequence, key head, tile of
+// 16 visible slots), sequences of very different lengths behind one another -
+// cut into equal runs, one per CTA, and each CTA's run into eight, one per
+// warp: every processor reads the same number of rows whatever the lengths
+// are.  A warp keeps the online softmax (maximum, sum, weighted values) of the
+// piece of a (sequence, key head) it is in.  A piece that is whole is written
+// out; the others of a CTA are joined in shared memory, and what is still part
+// of a longer one goes to the workspace (two slots a CTA at most: the run's
+// first and last), where cache_join_kernel adds the parts in order.  Short
+// caches, and batches that fill the GPU by themselves, take one CTA per
+// (sequence, key head) and no second launch.
+//
+// bf16: mma.sync m16n8k16 with the heads as rows.  The tile's keys are the B
+// operand of S = Q K^T and its values that of O += P V, both as they come from
+// memory: a lane's 16-byte chunks are the fragments of a permuted contraction
+// index (Q is permuted the same way), and the values' token pairs are formed
+// with byte permutes.  The tensor cores matter little here; they keep the issue
+// slots free for the loads.  P is rounded to bf16 for the product.
+// float: 16 lanes share a row, two rows at a time, on CUDA cores.
 #include "seq.cuh"
 
 namespace pack3d {
 namespace seq {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(32) cache_attn_row_kernel(const Cache c, const T* __restrict__ q, T* out,
-                                                            float* lse, float* row_lse) {
-  const int b = blockIdx.x, h = blockIdx.y, g = h / c.G;
-  const int n = cached(c, b), low = c.window > 0 ? max(0, n - c.window) : 0;
-  const size_t at = (size_t)b * c.Hq + h, step = (size_t)c.Hkv * kDh;
-  const T* k = (const T*)c.k_pages + (size_t)g * kDh;
-  const T* v = (const T*)c.v_pages + (size_t)g * kDh;
-  const int32_t* row = c.table + (size_t)b * c.max_pages;
-  const float2 qq = load2(q + at * kDh);
-  float m = -INFINITY, l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
-  for (int j = 0; j < n; ++j) {
-    if (j >= c.sinks && j < low) continue;
-    const long src = pool_row(c, row, j);
-    if (src < 0) continue;
-    const float x = dot2(qq, load2(k + src * step)) * c.scale;
-    const float2 vv = load2(v + src * step);
-    float f = 1.f;
-    if (x > m) {
-      f = expf(m - x);
-      m = x;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kSlots = 16;                 // visible slots of a unit
+
+// Softmax state of one piece: for each head the maximum (log2 units), the sum
+// and the weighted values.
+template <int G>
+struct alignas(16) Piece {
+  float o[G][kDh];
+  float m[G], l[G];
+};
+
+struct DecodeArgs {
+  Cache c;
+  const void* q;
+  void* out;
+  float* lse;        // nullable
+  float* row_lse2;   // with weights: log2 of each row's denominator
+  float* logits;     // with weights: scaled log2 scores [B * Hq][cap], by visible slot
+  void* part;        // Piece [CTAs][2]
+  int split;         // 0: one CTA per (sequence, key head)
+};
+
+// The visible slots of a sequence: first the sinks [0, s0), then [lo, n).
+struct Seen {
+  int lo, s0, count;
+  __device__ __forceinline__ int slot(int i) const { return i < s0 ? i : i - s0 + lo; }
+};
+__device__ __forceinline__ Seen seen(const Cache& c, int n) {
+  Seen v;
+  v.lo = c.window > 0 && n > c.window ? n - c.window : 0;
+  v.s0 = min(c.sinks, v.lo);
+  v.count = v.s0 + n - v.lo;
+  return v;
+}
+__device__ __forceinline__ int units_of(const Cache& c, int b) {
+  return (seen(c, cached(c, b)).count + kSlots - 1) / kSlots;
+}
+
+// Where a unit lies: tile t of a (sequence, key head) with so many tiles.
+struct Unit {
+  int b, g, t, tiles;
+};
+// Tiles [t0, t1) of a (sequence, key head), in shared memory; b < 0: none.
+struct Span {
+  int b, g, t0, t1;
+};
+
+// All sequences' units (one warp), and with `u` >= 0 where unit u lies.
+__device__ __forceinline__ long find_unit(const Cache& c, long u, Unit* at) {
+  const int lane = threadIdx.x & 31;
+  long base = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const int tiles = b0 + lane < c.B ? units_of(c, b0 + lane) : 0;
+    long incl = (long)tiles * c.Hkv;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
     }
-    const float e = x == -INFINITY ? 0.f : expf(x - m);
-    l = l * f + e;
-    o.x = fmaf(e, vv.x, o.x * f);
-    o.y = fmaf(e, vv.y, o.y * f);
+    const long first = base + incl - (long)tiles * c.Hkv;
+    const uint32_t hit = __ballot_sync(0xffffffffu, u >= first && u < first + (long)tiles * c.Hkv);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      at->b = b0 + src;
+      at->tiles = __shfl_sync(0xffffffffu, tiles, src);
+      const int in = (int)(u - __shfl_sync(0xffffffffu, first, src));
+      at->g = in / at->tiles;
+      at->t = in - at->g * at->tiles;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  store2(out + at * kDh, make_float2(o.x * inv, o.y * inv));
+  return base;
+}
+
+// Units of one CTA's run: at least one per warp.
+__device__ __forceinline__ long run_units(long total, int ctas) { return max((total + ctas - 1) / ctas, (long)kWarps); }
+
+// d += A B for the rows 0-7 of A (8-15 are zero, and so is what they give).
+__device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  float z0, z1;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%9,%10,%11,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(z0), "=f"(z1)
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(d[0]), "f"(d[1]), "f"(0.f));
+  (void)z0;
+  (void)z1;
+}
+
+// Pool rows of the tile's 16 slots, lane i < 16 for slot i; -1 where there is
+// none (past the end, or a page outside the pool: reported and left out).
+__device__ __forceinline__ int tile_rows(const Cache& c, const int32_t* table, const Seen& v, int t) {
+  const int i = t * kSlots + (threadIdx.x & 15);
+  return i < v.count ? (int)pool_row(c, table, v.slot(i)) : -1;
+}
+
+template <typename T, int G> struct Worker;
+
+// ---- bf16 -------------------------------------------------------------------------
+// Lane (r, x) = (lane / 4, lane % 4): head row r; of the keys, token r (and
+// 8 + r) and the 16-byte chunks x and x + 4; of the values, the tokens 2x, 2x+1,
+// 8+2x, 8+2x+1 and the chunk r.
+template <int G> struct Worker<__nv_bfloat16, G> {
+  struct Data {
+    uint4 k[4], v[4];
+  };
+  uint32_t q[8];
+  float o[8][2];
+  float m, l;
+
+  __device__ __forceinline__ void begin(const DecodeArgs& a, int b, int g) {
+    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
+    if (r < G) {
+      const uint4* p = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + ((size_t)b * a.c.Hq + g * G + r) * kDh);
+      c0 = __ldg(p + x);
+      c1 = __ldg(p + x + 4);
+    }
+    q[0] = c0.x; q[1] = c0.y; q[2] = c0.z; q[3] = c0.w;
+    q[4] = c1.x; q[5] = c1.y; q[6] = c1.z; q[7] = c1.w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) o[i][e] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+  }
+  __device__ __forceinline__ static uint4 chunk(const uint4* base, long row, long step, int i) {
+    return row >= 0 ? __ldg(base + row * step + i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const DecodeArgs& a, int g, int rows, Data& d) const {
+    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    const long step = (long)a.c.Hkv * 8;      // 16-byte chunks a pool row
+    const uint4* k = reinterpret_cast<const uint4*>(a.c.k_pages) + g * 8;
+    const uint4* v = reinterpret_cast<const uint4*>(a.c.v_pages) + g * 8;
+    const int k0 = __shfl_sync(0xffffffffu, rows, r), k1 = __shfl_sync(0xffffffffu, rows, 8 + r);
+    d.k[0] = chunk(k, k0, step, x);
+    d.k[1] = chunk(k, k0, step, x + 4);
+    d.k[2] = chunk(k, k1, step, x);
+    d.k[3] = chunk(k, k1, step, x + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int vr = __shfl_sync(0xffffffffu, rows, (i >> 1) * 8 + 2 * x + (i & 1));
+      d.v[i] = chunk(v, vr, step, r);
+    }
+  }
+  __device__ __forceinline__ void compute(const DecodeArgs& a, int rows, const Data& d, int t, float* logits) {
+    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    float s[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) s[h][e] = 0.f;
+      const uint4 a0 = d.k[2 * h], a1 = d.k[2 * h + 1];
+      mma_16816(s[h], q[0], q[1], a0.x, a0.y);
+      mma_16816(s[h], q[2], q[3], a0.z, a0.w);
+      mma_16816(s[h], q[4], q[5], a1.x, a1.y);
+      mma_16816(s[h], q[6], q[7], a1.z, a1.w);
+    }
+    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
+    float y[4] = {s[0][0] * a.c.scale_log2, s[0][1] * a.c.scale_log2, s[1][0] * a.c.scale_log2,
+                  s[1][1] * a.c.scale_log2};
+    if ((have & 0xffffu) != 0xffffu) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!((have >> ((i >> 1) * 8 + 2 * x + (i & 1))) & 1u)) y[i] = -INFINITY;
+    }
+    if (logits && r < G) {
+      float* p = logits + (size_t)r * a.c.cap + t * kSlots + 2 * x;   // cap is a multiple of 16
+      *reinterpret_cast<float2*>(p) = make_float2(y[0], y[1]);
+      *reinterpret_cast<float2*>(p + 8) = make_float2(y[2], y[3]);
+    }
+    float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    if (__any_sync(0xffffffffu, mx > m)) {
+      const float top = fmaxf(m, mx);
+      const float f = top == -INFINITY ? 1.f : exp2f(m - top);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f;
+        o[i][1] *= f;
+      }
+    }
+    const float sub = m == -INFINITY ? 0.f : m;
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = exp2f(y[i] - sub);
+    l += (p[0] + p[1]) + (p[2] + p[3]);
+    const uint32_t p0 = pack_bf16x2(p[0], p[1]), p1 = pack_bf16x2(p[2], p[3]);
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(d.v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t pick = (i & 1) ? 0x7632u : 0x5410u;   // high or low halves: one dim of a token pair
+      mma_16816(o[i], p0, p1, __byte_perm(v[i >> 1], v[4 + (i >> 1)], pick),
+                __byte_perm(v[8 + (i >> 1)], v[12 + (i >> 1)], pick));
+    }
+  }
+  // The lane's row total; o[i][e] of row r is dim 16 x + 8 e + i.
+  __device__ __forceinline__ void finish() {
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+  }
+  __device__ __forceinline__ void store(Piece<G>* p) const {
+    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    if (r >= G) return;
+    if (x == 0) {
+      p->m[r] = m;
+      p->l[r] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p->o[r][16 * x + 8 * e + i] = o[i][e];
+  }
+};
+
+// ---- float ------------------------------------------------------------------------
+// Lane (u, x) = (lane / 16, lane % 16): of every pair of slots, slot u, and the
+// dims 4x .. 4x+3.  The two halves of a warp keep separate softmax states,
+// joined at the end of a piece.
+template <int G> struct Worker<float, G> {
+  // Pairs of slots of a step, half of which is in flight: fewer with many
+  // heads, whose queries and sums take the registers.
+  static constexpr int kPairs = G >= 4 ? 2 : 4, kSteps = 8 / kPairs;
+  struct Data {
+    float4 k[kPairs], v[kPairs];
+  };
+  float4 q[G], o[G];
+  float m[G], l[G];
+
+  __device__ __forceinline__ void begin(const DecodeArgs& a, int b, int g) {
+    const int x = threadIdx.x & 15;
+    const float4* p = reinterpret_cast<const float4*>((const float*)a.q + ((size_t)b * a.c.Hq + g * G) * kDh);
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float4 f = __ldg(p + h * 16 + x);
+      q[h] = f;
+      o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(const DecodeArgs& a, int g, int rows, int step_of, Data& d) const {
+    const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
+    const long step = (long)a.c.Hkv * 16;
+    const float4* k = reinterpret_cast<const float4*>(a.c.k_pages) + g * 16 + x;
+    const float4* v = reinterpret_cast<const float4*>(a.c.v_pages) + g * 16 + x;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int row = __shfl_sync(0xffffffffu, rows, 2 * (step_of * kPairs + i) + u);
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      d.k[i] = row >= 0 ? __ldg(k + (long)row * step) : zero;
+      d.v[i] = row >= 0 ? __ldg(v + (long)row * step) : zero;
+    }
+  }
+  __device__ __forceinline__ void compute(const DecodeArgs& a, int rows, int step_of, const Data& d, int t,
+                                          float* logits) {
+    const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
+    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float y[kPairs];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int slot = 2 * (step_of * kPairs + i) + u;
+        float s = fmaf(q[h].x, d.k[i].x, fmaf(q[h].y, d.k[i].y, fmaf(q[h].z, d.k[i].z, q[h].w * d.k[i].w)));
+#pragma unroll
+        for (int e = 8; e > 0; e >>= 1) s += __shfl_xor_sync(0xffffffffu, s, e);
+        y[i] = (have >> slot) & 1u ? s * a.c.scale_log2 : -INFINITY;
+        if (logits && x == 0) logits[(size_t)h * a.c.cap + t * kSlots + slot] = y[i];
+        mx = fmaxf(mx, y[i]);
+      }
+      if (mx > m[h]) {
+        const float f = exp2f(m[h] - mx);
+        m[h] = mx;
+        l[h] *= f;
+        o[h].x *= f;
+        o[h].y *= f;
+        o[h].z *= f;
+        o[h].w *= f;
+      }
+      const float sub = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float p = exp2f(y[i] - sub);
+        l[h] += p;
+        o[h].x = fmaf(p, d.v[i].x, o[h].x);
+        o[h].y = fmaf(p, d.v[i].y, o[h].y);
+        o[h].z = fmaf(p, d.v[i].z, o[h].z);
+        o[h].w = fmaf(p, d.v[i].w, o[h].w);
+      }
+    }
+  }
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m[h], 16);
+      const float top = fmaxf(m[h], mo);
+      const float f = m[h] == top ? 1.f : exp2f(m[h] - top);     // also for two empty halves
+      float* acc[5] = {&l[h], &o[h].x, &o[h].y, &o[h].z, &o[h].w};
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const float mine = *acc[i] * f;
+        *acc[i] = mine + __shfl_xor_sync(0xffffffffu, mine, 16);
+      }
+      m[h] = top;
+    }
+  }
+  __device__ __forceinline__ void store(Piece<G>* p) const {
+    const int lane = threadIdx.x & 31;
+    if (lane >= 16) return;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      if (lane == 0) {
+        p->m[h] = m[h];
+        p->l[h] = l[h];
+      }
+      *reinterpret_cast<float4*>(&p->o[h][4 * lane]) = o[h];
+    }
+  }
+};
+
+// Tiles [t0, t1) of one (sequence, key head): rows two tiles ahead, data one.
+template <int G>
+__device__ __forceinline__ void run_tiles(Worker<__nv_bfloat16, G>& k, const DecodeArgs& a, int b, int g,
+                                          const Seen& v, int t0, int t1, float* logits) {
+  const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
+  int rows = tile_rows(a.c, table, v, t0);
+  int next = t0 + 1 < t1 ? tile_rows(a.c, table, v, t0 + 1) : -1;
+  typename Worker<__nv_bfloat16, G>::Data d[2];
+  k.load(a, g, rows, d[0]);
+  for (int t = t0; t < t1; t += 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (t + i >= t1) break;
+      const int after = t + i + 2 < t1 ? tile_rows(a.c, table, v, t + i + 2) : -1;
+      if (t + i + 1 < t1) k.load(a, g, next, d[i ^ 1]);
+      k.compute(a, rows, d[i], t + i, logits);
+      rows = next;
+      next = after;
+    }
+  }
+}
+template <int G>
+__device__ __forceinline__ void run_tiles(Worker<float, G>& k, const DecodeArgs& a, int b, int g, const Seen& v,
+                                          int t0, int t1, float* logits) {
+  const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
+  int rows = tile_rows(a.c, table, v, t0);
+  constexpr int kSteps = Worker<float, G>::kSteps;      // even
+  typename Worker<float, G>::Data d[2];
+  k.load(a, g, rows, 0, d[0]);
+  for (int t = t0; t < t1; ++t) {
+    const int next = t + 1 < t1 ? tile_rows(a.c, table, v, t + 1) : -1;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i + 1 < kSteps) k.load(a, g, rows, i + 1, d[(i + 1) & 1]);
+      else if (t + 1 < t1) k.load(a, g, next, 0, d[(i + 1) & 1]);
+      k.compute(a, rows, i, d[i & 1], t, logits);
+    }
+    rows = next;
+  }
+}
+
+// Final values of head h: lane holds the dims 2 lane, 2 lane + 1 of the sum o.
+template <typename T>
+__device__ __forceinline__ void write_row(const DecodeArgs& a, int b, int h, float m, float l, float2 o) {
+  const size_t at = (size_t)b * a.c.Hq + h;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store2((T*)a.out + at * kDh, make_float2(o.x * inv, o.y * inv));
   if ((threadIdx.x & 31) == 0) {
-    if (lse) lse[at] = m + logf(l);
-    row_lse[at] = m + logf(l);
+    const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+    if (a.lse) a.lse[at] = lse2 * 0.69314718f;
+    if (a.row_lse2) a.row_lse2[at] = lse2;
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) cache_weights_row_kernel(const Cache c, const T* __restrict__ q,
-                                                                const float* __restrict__ row_lse, float* weights,
-                                                                int accumulate) {
+// Joins the pieces number first .. last of one (sequence, key head), in order,
+// of those that are in use: into `to`, or where to is null into the results.
+// One warp.
+template <typename T, int G>
+__device__ __forceinline__ void join_pieces(const DecodeArgs& a, int b, int g, const Piece<G>* p, const Span* used,
+                                            int first, int last, Piece<G>* to) {
+  const int lane = threadIdx.x & 31;
+  for (int h = 0; h < G; ++h) {
+    float top = -INFINITY;
+    for (int i = first; i <= last; ++i)
+      if (used[i].b >= 0) top = fmaxf(top, p[i].m[h]);
+    float l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+    for (int i = first; i <= last; ++i) {
+      if (used[i].b < 0) continue;
+      const float f = p[i].m[h] == top ? 1.f : exp2f(p[i].m[h] - top);
+      const float2 x = *reinterpret_cast<const float2*>(&p[i].o[h][2 * lane]);
+      l = fmaf(p[i].l[h], f, l);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+    }
+    if (to) {
+      if (lane == 0) {
+        to->m[h] = top;
+        to->l[h] = l;
+      }
+      *reinterpret_cast<float2*>(&to->o[h][2 * lane]) = o;
+    } else {
+      write_row<T>(a, b, g * G + h, top, l, o);
+    }
+  }
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArgs a) {
+  __shared__ Piece<G> pieces[2 * kWarps];    // two a warp: its run's first and last are the ones that may not be whole
+  __shared__ Span spans[2 * kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Cache& c = a.c;
+  if (threadIdx.x < 2 * kWarps) spans[threadIdx.x].b = -1;
+  // This warp's run of units and where it begins.
+  Unit at;
+  long begin, end;
+  if (a.split) {
+    const long total = find_unit(c, -1, &at);
+    const long per = run_units(total, gridDim.x);
+    const long first = min(total, blockIdx.x * per), past = min(total, first + per);
+    begin = first + (past - first) * warp / kWarps;
+    end = first + (past - first) * (warp + 1) / kWarps;
+    if (begin < end) find_unit(c, begin, &at);
+  } else {
+    at.b = blockIdx.x / c.Hkv;
+    at.g = blockIdx.x % c.Hkv;
+    at.tiles = units_of(c, at.b);
+    begin = (long)at.tiles * warp / kWarps;
+    end = (long)at.tiles * (warp + 1) / kWarps;
+    at.t = (int)begin;
+    if (at.tiles == 0) {     // nothing cached: zeros, for every head of the group
+      if (warp < G) write_row<T>(a, at.b, at.g * G + warp, -INFINITY, 0.f, make_float2(0.f, 0.f));
+      return;
+    }
+  }
+  __syncthreads();
+  int used = 0;              // pieces this warp left in shared memory
+  Worker<T, G> k;
+  for (long u = begin; u < end;) {
+    const Seen v = seen(c, cached(c, at.b));
+    const int t1 = (int)min((long)at.tiles, at.t + (end - u));
+    float* logits = a.logits ? a.logits + ((size_t)at.b * c.Hq + at.g * G) * c.cap : nullptr;
+    k.begin(a, at.b, at.g);
+    run_tiles(k, a, at.b, at.g, v, at.t, t1, logits);
+    k.finish();
+    const int slot = 2 * warp + used;
+    k.store(&pieces[slot]);
+    if (lane == 0) spans[slot] = Span{at.b, at.g, at.t, t1};
+    __syncwarp();
+    if (at.t == 0 && t1 == at.tiles) {       // whole: the slot is free again
+      join_pieces<T, G>(a, at.b, at.g, pieces, spans, slot, slot, nullptr);
+      __syncwarp();
+      if (lane == 0) spans[slot].b = -1;
+    } else {
+      ++used;
+    }
+    u += t1 - at.t;
+    // The next (sequence, key head) with units.
+    if (u < end) {
+      at.t = 0;
+      if (++at.g == c.Hkv) {
+        at.g = 0;
+        do at.tiles = units_of(c, ++at.b);
+        while (at.tiles == 0 && at.b + 1 < c.B);
+      }
+    }
+  }
+  __syncthreads();
+  // Pieces of one (sequence, key head) lie behind one another: the warp of the
+  // first one's slot joins them.  What is still not whole goes to the
+  // workspace: slot 1 of the CTA if it begins its (sequence, key head), slot 0
+  // if it continues one.
+  for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
+    const Span me = spans[i];
+    if (me.b < 0) continue;
+    bool mine = true;
+    for (int j = 0; j < i; ++j) mine &= !(spans[j].b == me.b && spans[j].g == me.g);
+    if (!mine) continue;
+    int last = i;
+    for (int j = i + 1; j < 2 * kWarps; ++j)
+      if (spans[j].b == me.b && spans[j].g == me.g) last = j;
+    const bool whole = me.t0 == 0 && spans[last].t1 == units_of(c, me.b);
+    Piece<G>* to = whole ? nullptr : (Piece<G>*)a.part + 2 * (size_t)blockIdx.x + (me.t0 == 0 ? 1 : 0);
+    join_pieces<T, G>(a, me.b, me.g, pieces, spans, i, last, to);
+  }
+}
+
+// Joins the CTAs' parts of one (sequence, head) in the order of the cache: 16
+// groups of 16 threads each add every 16th part, a thread four dims.
+template <typename T, int G>
+__global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int ctas) {
+  __shared__ long s_first, s_total;
+  __shared__ float s_top[8];
+  __shared__ float4 s_o[16][16];
+  __shared__ float s_l[16];
+  const Cache& c = a.c;
+  const int b = blockIdx.x / c.Hq, hq = blockIdx.x % c.Hq, g = hq / G, h = hq % G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = units_of(c, b);
+  if (warp == 0) {
+    long before = 0, total = 0;
+    for (int i = lane; i < c.B; i += 32) {
+      const long n = (long)units_of(c, i) * c.Hkv;
+      total += n;
+      if (i < b) before += n;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, d);
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+    }
+    if (lane == 0) {
+      s_first = before + (long)g * tiles;
+      s_total = total;
+    }
+    if (tiles == 0) write_row<T>(a, b, hq, -INFINITY, 0.f, make_float2(0.f, 0.f));
+  }
+  if (tiles == 0) return;
+  __syncthreads();
+  const long per = run_units(s_total, ctas);
+  const int c0 = (int)(s_first / per), n = (int)((s_first + tiles - 1) / per) - c0 + 1;
+  if (n == 1) return;       // one CTA had all of it and wrote the results
+  const Piece<G>* part = (const Piece<G>*)a.part + 2 * (size_t)c0;
+  auto piece = [&](int i) { return part + 2 * i + (i == 0 ? 1 : 0); };
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += 256) top = fmaxf(top, piece(i)->m[h]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, s_top[i]);
+  const int part_of = threadIdx.x >> 4, x = threadIdx.x & 15;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = part_of; i < n; i += 16) {
+    const Piece<G>* p = piece(i);
+    const float f = p->m[h] == top ? 1.f : exp2f(p->m[h] - top);
+    const float4 y = *reinterpret_cast<const float4*>(&p->o[h][4 * x]);
+    l = fmaf(p->l[h], f, l);
+    o.x = fmaf(y.x, f, o.x);
+    o.y = fmaf(y.y, f, o.y);
+    o.z = fmaf(y.z, f, o.z);
+    o.w = fmaf(y.w, f, o.w);
+  }
+  s_o[part_of][x] = o;
+  if (x == 0) s_l[part_of] = l;
+  __syncthreads();
+  if (warp > 0) return;
+  float2 sum = make_float2(0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 y = reinterpret_cast<const float2*>(s_o[i])[lane];
+    sum.x += y.x;
+    sum.y += y.y;
+    l += s_l[i];
+  }
+  write_row<T>(a, b, hq, top, l, sum);
+}
+
+// The token's weight of every slot: softmax weights from the kept scores and
+// the rows' denominators, summed over the heads.
+__global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const float* __restrict__ logits,
+                                                            const float* __restrict__ row_lse2,
+                                                            float* __restrict__ weights, int accumulate) {
   const int b = blockIdx.y;
-  const int n = cached(c, b), low = c.window > 0 ? max(0, n - c.window) : 0;
-  const size_t step = (size_t)c.Hkv * kDh;
-  const int32_t* row = c.table + (size_t)b * c.max_pages;
-  for (int j = blockIdx.x * 4 + (threadIdx.x >> 5); j < n; j += gridDim.x * 4) {
+  const int n = cached(c, b);
+  const Seen v = seen(c, n);
+  for (int j = blockIdx.x * 256 + threadIdx.x; j < n; j += gridDim.x * 256) {
+    const int i = j < v.s0 ? j : (j >= v.lo ? j - v.lo + v.s0 : -1);
     float total = 0.f;
-    if (j < c.sinks || j >= low) {
-      const long src = pool_row(c, row, j);
-      if (src >= 0)
-        for (int h = 0; h < c.Hq; ++h) {
-          const size_t at = (size_t)b * c.Hq + h;
-          const float x = dot2(load2(q + at * kDh), load2((const T*)c.k_pages + src * step + (h / c.G) * kDh));
-          total += expf(x * c.scale - row_lse[at]);
-        }
-    }
-    if ((threadIdx.x & 31) == 0) {
-      float* dst = weights + (size_t)b * c.cap + j;
-      *dst = accumulate ? *dst + total : total;
-    }
+    if (i >= 0)
+      for (int h = 0; h < c.Hq; ++h) {
+        const size_t at = (size_t)b * c.Hq + h;
+        total += exp2f(__ldg(logits + at * c.cap + i) - __ldg(row_lse2 + at));
+      }
+    float* dst = weights + (size_t)b * c.cap + j;
+    *dst = accumulate ? *dst + total : total;
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const Cache& c, const void* q, void* out, float* lse, float* weights, bool accumulate,
-                     void* workspace, cudaStream_t st) {
-  float* row_lse = (float*)workspace;
-  cache_attn_row_kernel<T><<<dim3(c.B, c.Hq), 32, 0, st>>>(c, (const T*)q, (T*)out, lse, row_lse);
-  if (weights)
-    cache_weights_row_kernel<T><<<dim3((c.cap + 63) / 64, c.B), 128, 0, st>>>(c, (const T*)q, row_lse, weights,
-                                                                              accumulate);
+// ---- host side ------------------------------------------------------------------
+
+int sm_count() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 148;
+}
+
+// One CTA per (sequence, key head) where a cache of at most 64 units (eight a
+// warp) or a batch of at least 4,096 such pairs leaves nothing to split for.
+bool is_split(int B, int Hkv, int cap) { return cap > 64 * kSlots && (long)B * Hkv < 4096; }
+
+// CTAs of a split call: two an SM, fewer where the capacity has fewer runs.
+// The workspace has room for the most there can be on any GPU.
+constexpr int kMaxCtas = 512;
+int split_ctas(int B, int Hkv, int cap) {
+  const long runs = ((long)B * Hkv * (cap / kSlots) + kWarps - 1) / kWarps;
+  return (int)min((long)min(2 * sm_count(), kMaxCtas), max(1L, runs));
+}
+
+size_t up1k(size_t n) { return (n + 1023) / 1024 * 1024; }
+
+template <typename T, int G>
+cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
+  const Cache& c = a.c;
+  if (!a.split) {
+    cache_attn_kernel<T, G><<<c.B * c.Hkv, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  const int ctas = split_ctas(c.B, c.Hkv, c.cap);
+  cache_attn_kernel<T, G><<<ctas, kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cache_join_kernel<T, G><<<c.B * c.Hq, 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(DecodeArgs& a, cudaStream_t st) {
+  switch (a.c.G) {
+    case 1: return launch_g<T, 1>(a, st);
+    case 2: return launch_g<T, 2>(a, st);
+    case 4: return launch_g<T, 4>(a, st);
+    default: return launch_g<T, 8>(a, st);
+  }
 }
 
 }  // namespace
 
+// The split's parts, then with weights the rows' denominators and the scores.
 size_t cache_attn_workspace(int B, int Hq, int Hkv, int cap, bool weights) {
-  return ((size_t)B * Hq * 4 + 1023) / 1024 * 1024;
+  size_t n = 1024;
+  if (is_split(B, Hkv, cap)) n = up1k((size_t)2 * kMaxCtas * (((size_t)(Hq / Hkv) * (2 + kDh) * sizeof(float) + 15) / 16 * 16));
+  if (weights) n += up1k((size_t)B * Hq * 4) + (size_t)B * Hq * cap * 4;
+  return n;
 }
 
 cudaError_t launch_cache_attn(const Cache& c, int dtype, const void* q, void* out, float* lse, float* weights,
                               bool accumulate, void* workspace, cudaStream_t st) {
-  if (dtype == PACK3D_BF16) return launch_t<__nv_bfloat16>(c, q, out, lse, weights, accumulate, workspace, st);
-  return launch_t<float>(c, q, out, lse, weights, accumulate, workspace, st);
+  DecodeArgs a;
+  a.c = c;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.split = is_split(c.B, c.Hkv, c.cap);
+  a.part = workspace;
+  a.row_lse2 = nullptr;
+  a.logits = nullptr;
+  if (weights) {
+    char* p = (char*)workspace + cache_attn_workspace(c.B, c.Hq, c.Hkv, c.cap, false);
+    a.row_lse2 = (float*)p;
+    a.logits = (float*)(p + up1k((size_t)c.B * c.Hq * 4));
+  }
+  cudaError_t e = dtype == PACK3D_BF16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
+  if (e != cudaSuccess || !weights || c.cap == 0) return e;
+  const dim3 grid((unsigned)((c.cap + 255) / 256), c.B);
+  cache_weights_kernel<<<grid, 256, 0, st>>>(c, a.logits, a.row_lse2, weights, accumulate);
+  return cudaGetLastError();
 }
 
 }  // namespace seq
