@@ -620,12 +620,6 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const
 
 // ---- host side ------------------------------------------------------------------
 
-int sm_count() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
-}
-
 // One CTA per (sequence, key head) where a cache of at most 64 units (eight a
 // warp) or a batch of at least 4,096 such pairs leaves nothing to split for.
 bool is_split(int B, int Hkv, int cap) { return cap > 64 * kSlots && (long)B * Hkv < 4096; }

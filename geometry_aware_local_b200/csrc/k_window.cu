@@ -16,16 +16,18 @@ __device__ __forceinline__ void no_query_tile(const Win& w, const Tiles& all, vo
   if (all.bad) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
   } else if (w.zero_outside && blockIdx.y == 0) {
-    fill_outside(w, w.cu_q, w.Tq, rows, w.Hq * kDh * (int)sizeof(T) / 4, 0u, blockIdx.x, gridDim.x, all);
-    if (lse) fill_outside(w, w.cu_q, w.Tq, lse, w.Hq, 0xff800000u, blockIdx.x, gridDim.x, all);
+    const int part = (blockIdx.x - all.total) * kWarps + (threadIdx.x >> 5), parts = (gridDim.x - all.total) * kWarps;
+    fill_outside(w, w.cu_q, w.Tq, rows, w.Hq * kDh * (int)sizeof(T) / 4, 0u, part, parts);
+    if (lse) fill_outside(w, w.cu_q, w.Tq, lse, w.Hq, 0xff800000u, part, parts);
   }
 }
 template <typename T>
 __device__ __forceinline__ void no_key_tile(const Win& w, const Tiles& all) {
   if (all.bad || !w.zero_outside || blockIdx.y != 0) return;
   const int words = w.Hkv * kDh * (int)sizeof(T) / 4;
-  fill_outside(w, w.cu_k, w.Tk, w.dk, words, 0u, blockIdx.x, gridDim.x, all);
-  fill_outside(w, w.cu_k, w.Tk, w.dv, words, 0u, blockIdx.x, gridDim.x, all);
+  const int part = (blockIdx.x - all.total) * kWarps + (threadIdx.x >> 5), parts = (gridDim.x - all.total) * kWarps;
+  fill_outside(w, w.cu_k, w.Tk, w.dk, words, 0u, part, parts);
+  fill_outside(w, w.cu_k, w.Tk, w.dv, words, 0u, part, parts);
 }
 
 template <typename T>

@@ -123,7 +123,9 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     if (all.bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
     } else if (w.zero_outside && blockIdx.y == 0) {
-      fill_outside(w, w.cu_q, w.Tq, w.dq, w.Hq * kDh / 2, 0u, blockIdx.x, gridDim.x, all);
+      constexpr int kWarps = kThreads / 32;
+      fill_outside(w, w.cu_q, w.Tq, w.dq, w.Hq * kDh / 2, 0u, (blockIdx.x - all.total) * kWarps + warp,
+                   (gridDim.x - all.total) * kWarps);
     }
     return;
   }
@@ -459,8 +461,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   if (!*found_slot) {
     const Tiles all = *tiles_slot;
     if (!far && !all.bad && w.zero_outside && blockIdx.y == 0) {
-      fill_outside(w, w.cu_k, w.Tk, w.dk, w.Hkv * kDh / 2, 0u, x, key_grid, all);
-      fill_outside(w, w.cu_k, w.Tk, w.dv, w.Hkv * kDh / 2, 0u, x, key_grid, all);
+      constexpr int kWarps = kThreads / 32;
+      const int part = (x - all.total) * kWarps + warp, parts = (key_grid - all.total) * kWarps;
+      fill_outside(w, w.cu_k, w.Tk, w.dk, w.Hkv * kDh / 2, 0u, part, parts);
+      fill_outside(w, w.cu_k, w.Tk, w.dv, w.Hkv * kDh / 2, 0u, part, parts);
     }
     return;
   }

@@ -31,22 +31,31 @@ namespace pack3d {
 namespace seq {
 namespace {
 
-constexpr int kBM = kRowsPerTile, kBN = 128;
+constexpr int kBM = kRowsPerTile, kBN = 96;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kThreads = 192;
-constexpr int kColS = 0, kColP = kBN, kColO = kBN + kBN / 2, kTmemCols = 256;
+constexpr int kColS = 0, kColP = kBN, kColO = 2 * kBN, kTmemCols = 256;   // P buffer b at kColP + b * kBN / 2
+static_assert(kColO + kDh <= kTmemCols, "tensor memory plan");
 constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2;
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;     // K at +0, V at +kTileBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, s_full, s_free, p_full, p_free, o_final, drain
-constexpr int kNumBars = 2 * kStages + 7;
+// barriers: full[S], empty[S], qfull, s_full, s_free, p_full[2], p_free[2], o_final, drain
+constexpr int kNumBars = 2 * kStages + 9;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
-constexpr int kTileOff = kCtlOff + 32;                               // Tile, Tiles and the answer of find_tile
-constexpr int kSmemBytes = kTileOff + 64 + 1024;
+constexpr int kPlanOff = kCtlOff + 32;
+constexpr int kSmemBytes = kPlanOff + 64 + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(sizeof(Tile) + sizeof(Tiles) + 4 <= 64, "tile slot");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kDh, true);   // V MN-major
+
+// What the softmax warps need of the CTA's tile at its edges and its end: kept
+// in shared memory, so that it takes no registers in the loop over key tiles.
+struct Plan {
+  Tile s;
+  KeyTiles<kBN> kt;
+  int r0, r1;       // query rows
+};
+static_assert(sizeof(Plan) <= 64, "plan slot");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -66,27 +75,20 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
   const uint32_t qfull = bar0 + 8 * (2 * kStages);
-  const uint32_t s_full = qfull + 8, s_free = qfull + 16, p_full = qfull + 24, p_free = qfull + 32,
-                 o_final = qfull + 40, drain = qfull + 48;
+  const uint32_t s_full = qfull + 8, s_free = qfull + 16, o_final = qfull + 24, drain = qfull + 32;
+  auto p_full = [&](int b) { return qfull + 40 + 8 * b; };
+  auto p_free = [&](int b) { return qfull + 56 + 8 * b; };
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
-  Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
-  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
-  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
   auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
   const int tokens = kBM >> w.gshift;     // per tile
 
-  if (warp == 0) {
-    Tile s;
-    Tiles all;
-    const bool found = find_tile(w, blockIdx.x, tokens, false, &s, &all);
-    if (lane == 0) {
-      *tile_slot = s;
-      *tiles_slot = all;
-      *found_slot = found;
-    }
-  }
-  if (threadIdx.x == 32) {
+  // The producer sets the barriers up, and every warp finds the tile for
+  // itself, so that the first loads are under way before the CTA meets.
+  if (warp == kTmaWarp && lane == 0) {
+    ptx::tma_prefetch(&tmQ);
+    ptx::tma_prefetch(&tmK);
+    ptx::tma_prefetch(&tmV);
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), 1);
@@ -94,8 +96,10 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     ptx::mbar_init(qfull, 1);
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(s_free, 4);
-    ptx::mbar_init(p_full, 4);
-    ptx::mbar_init(p_free, 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(p_full(b), 4);
+      ptx::mbar_init(p_free(b), 1);
+    }
     ptx::mbar_init(o_final, 1);
     ptx::mbar_init(drain, 1);
     ctl->abort = 0;
@@ -103,17 +107,45 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     ctl->limit_ns = w.wait_ns;
     ptx::fence_mbar_init();
   }
-  __syncthreads();
-  if (!*found_slot) {
-    const Tiles all = *tiles_slot;
+  __syncwarp();
+  Tile s;
+  Tiles all;
+  if (!find_tile(w, blockIdx.x, tokens, false, &s, &all)) {
     if (all.bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
     } else if (w.zero_outside && blockIdx.y == 0) {
-      fill_outside(w, w.cu_q, w.Tq, w.out, w.Hq * kDh / 2, 0u, blockIdx.x, gridDim.x, all);
-      if (w.lse) fill_outside(w, w.cu_q, w.Tq, w.lse, w.Hq, 0xff800000u, blockIdx.x, gridDim.x, all);
+      constexpr int kWarps = kThreads / 32;
+      const int part = (blockIdx.x - all.total) * kWarps + warp, parts = (gridDim.x - all.total) * kWarps;
+      fill_outside(w, w.cu_q, w.Tq, w.out, w.Hq * kDh / 2, 0u, part, parts);
+      if (w.lse) fill_outside(w, w.cu_q, w.Tq, w.lse, w.Hq, 0xff800000u, part, parts);
     }
     return;
   }
+  s.t = s.n - 1 - s.t;      // the tiles with most keys first
+  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
+  const int p0 = position(s, r0), p1 = position(s, r1);
+  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
+  const int T = kt.n, T_load = w.stall ? T - 1 : T;
+  volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + kPlanOff);
+  auto load_tile = [&](int j) {
+    const int st = j % kStages;
+    const uint32_t dst = sbase + kStageOff + st * kStageBytes;
+    const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
+    ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
+#pragma unroll 1
+    for (int c = 0; c < cols / 32; ++c) ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
+#pragma unroll 1
+    for (int c = 0; c < cols / 32; ++c)
+      ptx::tma_load_3d(dst + kTileBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
+  };
+  if (warp == kTmaWarp && lane == 0 && T > 0) {
+    ptx::mbar_expect_tx(qfull, kQBytes);
+    ptx::tma_load_4d(sbase, &tmQ, 0, 0, g, s.q0 + r0, qfull);
+#pragma unroll 1
+    for (int j = 0; j < min(T_load, kStages); ++j) load_tile(j);
+    ctl->issued = min(T_load, kStages);
+  }
+  if (threadIdx.x == 0) *const_cast<Plan*>(plan) = Plan{s, kt, r0, r1};
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
@@ -122,32 +154,15 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Tile s = *tile_slot;
-  s.t = s.n - 1 - s.t;      // the tiles with most keys first
-  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
-  const int p0 = position(s, r0), p1 = position(s, r1);
-  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
-  const int T = kt.n;
 
   if (warp == kTmaWarp) {
     // ---------------- TMA producer ----------------
-    if (lane == 0 && T > 0) {
-      ptx::tma_prefetch(&tmQ);
-      ptx::tma_prefetch(&tmK);
-      ptx::tma_prefetch(&tmV);
-      ptx::mbar_expect_tx(qfull, kQBytes);
-      ptx::tma_load_4d(sbase, &tmQ, 0, 0, g, s.q0 + r0, qfull);
-      const int T_load = w.stall ? T - 1 : T;
-      int issued = 0;
-      for (int j = 0; j < T_load; ++j) {
-        const int st = j % kStages;
-        if (j >= kStages && !wait(empty(st), ((j / kStages) - 1) & 1)) break;
-        const uint32_t dst = sbase + kStageOff + st * kStageBytes;
-        const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
-        ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
-        for (int c = 0; c < cols / 32; ++c) ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
-        for (int c = 0; c < cols / 32; ++c)
-          ptx::tma_load_3d(dst + kTileBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
+    if (lane == 0) {
+      int issued = min(T_load, kStages);
+#pragma unroll 1
+      for (int j = issued; j < T_load; ++j) {
+        if (!wait(empty(j % kStages), ((j / kStages) - 1) & 1)) break;
+        load_tile(j);
         issued = j + 1;
       }
       ctl->issued = issued;
@@ -168,11 +183,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       };
       auto issue_pv = [&](int j) {
         const uint32_t vaddr = sbase + kStageOff + (j % kStages) * kStageBytes + kTileBytes;
-        const int steps = kt.cols(j) / 16;
-        for (int kk = 0; kk < steps; ++kk)
-          ptx::mma_ts(tO, tP + kk * 8, ptx::smem_desc_sw128(vaddr + kk * 2048, 8192, 1024), kIdescPV,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-        ptx::tc_commit(p_free);
+        const int cols = kt.cols(j);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          if (kk * 16 < cols)
+            ptx::mma_ts(tO, tP + (j & 1) * (kBN / 2) + kk * 8, ptx::smem_desc_sw128(vaddr + kk * 2048, 8192, 1024),
+                        kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(p_free(j & 1));
         ptx::tc_commit(empty(j % kStages));
         if (j == T - 1) ptx::tc_commit(o_final);
       };
@@ -187,7 +204,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           ptx::tc_fence_after();
           issue_s(j + 1);
         }
-        if (!(ok = wait(p_full, j & 1))) break;
+        if (!(ok = wait(p_full(j & 1), (j >> 1) & 1))) break;
         ptx::tc_fence_after();
         issue_pv(j);
       }
@@ -197,14 +214,12 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     // ---------------- softmax warps: thread = row = tensor-memory lane ----------------
     const int lane_base = warp * 32;
     const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
-    const uint32_t tP = trow + kColP, tO = trow + kColO;
+    const uint32_t tO = trow + kColO;
     const float c = w.scale_log2;
-    const int row = lane_base + lane;
-    const int r = r0 + (row >> w.gshift);               // this row's token in its sequence
-    const bool valid = r <= r1;
-    const int p = valid ? position(s, r) : -1;          // rows past the sequence see nothing
-    const int low = window_low(w, p);
-    const int low_last = window_low(w, p1);             // the tile's last window start
+    // A 32-key chunk is seen in full by every row if it lies in [full_lo,
+    // full_hi]: behind the last row's window start and not past the first row's
+    // own key (and every row is one of the sequence).
+    const int full_lo = window_low(w, p1), full_hi = r0 + tokens > s.lq ? -1 : p0;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     auto warp_arrive = [&](uint32_t bar) {
@@ -212,40 +227,38 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar);
     };
+#pragma unroll 1
     for (int j = 0; j < T; ++j) {
+      const int k0 = kt.begin(j), cols = kt.cols(j);
       if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
       ptx::tc_fence_after();
-      const int k0 = kt.begin(j), cols = kt.cols(j);
       uint32_t sv[kBN];
-#pragma unroll
-      for (int q = 0; q < kBN / 64; ++q)
-        if (64 * q < cols) {
-          if (64 * q + 32 < cols) ptx::tmem_ld64_sync(trow + kColS + 64 * q, sv + 64 * q);
-          else ptx::tmem_ld32_sync(trow + kColS + 64 * q, sv + 64 * q);
-        }
+      if (cols > 32) ptx::tmem_ld64_sync(trow + kColS, sv);
+      else ptx::tmem_ld32_sync(trow + kColS, sv);
+      if (cols > 64) ptx::tmem_ld32_sync(trow + kColS + 64, sv + 64);
       warp_arrive(s_free);
       float mx = -INFINITY;
 #pragma unroll
       for (int q = 0; q < kBN / 32; ++q) {
         if (32 * q >= cols) break;
-        const int c0 = k0 + 32 * q;                     // the chunk's first key
-        // Seen in full by every row of the tile: behind the last row's window
-        // start and not past the first row's own key (and every row valid).
-        if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {
-          const uint32_t see = visible_bits(w, p, low, c0);
+        const int c0 = k0 + 32 * q;
+        if (c0 < full_lo || c0 + 31 > full_hi) {
+          const int r = plan->r0 + ((lane_base + lane) >> w.gshift);        // this row's token in its sequence
+          const int p = r <= plan->r1 ? plan->s.lk - plan->s.lq + r : -1;   // rows past the sequence see nothing
+          const uint32_t see = visible_bits(w, p, window_low(w, p), c0);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (!((see >> k) & 1u)) sv[32 * q + k] = __float_as_uint(-INFINITY);
         }
         float m4[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m4[i] = fmaxf(__uint_as_float(sv[32 * q + 2 * i]), __uint_as_float(sv[32 * q + 2 * i + 1]));
+        for (int e = 0; e < 4; ++e)
+          m4[e] = fmaxf(__uint_as_float(sv[32 * q + 2 * e]), __uint_as_float(sv[32 * q + 2 * e + 1]));
 #pragma unroll
         for (int k = 8; k < 32; k += 8)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m4[i] = max3(m4[i], __uint_as_float(sv[32 * q + k + 2 * i]), __uint_as_float(sv[32 * q + k + 2 * i + 1]));
+          for (int e = 0; e < 4; ++e)
+            m4[e] = max3(m4[e], __uint_as_float(sv[32 * q + k + 2 * e]), __uint_as_float(sv[32 * q + k + 2 * e + 1]));
         mx = max3(mx, max3(m4[0], m4[1], m4[2]), m4[3]);
       }
       const float mxs = mx * c;
@@ -256,9 +269,9 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         m_used = mxs;
       }
       const bool rescale = j > 0 && __any_sync(0xffffffffu, f != 1.f);
-      if (j > 0) {
-        // P of the previous tile has been read by its O += P V.
-        if (!(ok = __all_sync(0xffffffffu, wait(p_free, (j - 1) & 1)))) break;
+      if (j > 1) {
+        // This P buffer's last tile has been read by its O += P V.
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free(j & 1), ((j >> 1) - 1) & 1)))) break;
         ptx::tc_fence_after();
       }
       // A row that has seen no key yet (maximum -infinity) has only scores of
@@ -266,6 +279,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       const float shift = m_used == -INFINITY ? 0.f : -m_used;
       const float2 c2 = make_float2(c, c), nm2 = make_float2(shift, shift);
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const uint32_t tP = trow + kColP + (j & 1) * (kBN / 2);
 #pragma unroll
       for (int q = 0; q < kBN / 32; ++q) {
         if (32 * q >= cols) break;
@@ -273,14 +287,17 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int e = 32 * q + 2 * k;
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nm2);
-          const float2 pr = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nm2);
+          const float2 pr = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
           rs[k & 1] = __fadd2_rn(rs[k & 1], pr);
           pk[k] = pack_bf16x2(pr.x, pr.y);
         }
         ptx::tmem_st16(tP + 16 * q, pk);
       }
       if (rescale) {
+        // After the last tile's O += P V and before this one's.
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free((j - 1) & 1), ((j - 1) >> 1) & 1)))) break;
+        ptx::tc_fence_after();
         uint32_t o[16];
 #pragma unroll
         for (int q = 0; q < kDh / 16; ++q) {
@@ -291,12 +308,15 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         }
       }
       ptx::tmem_wait_st();
-      warp_arrive(p_full);
+      warp_arrive(p_full(j & 1));
       l = l * f + ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y));
     }
     if (T == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
+      const Tile at = *const_cast<const Tile*>(&plan->s);
+      const int row = lane_base + lane, r0 = plan->r0, r = r0 + (row >> w.gshift);
+      const bool valid = r <= plan->r1;
       const int h = (g << w.gshift) + (row & (w.G - 1));
-      const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
+      const size_t orow = (size_t)(at.q0 + r) * w.Hq + h;
       uint32_t o[kDh];
       if (T > 0) {
         ptx::tc_fence_after();
@@ -328,7 +348,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       __syncwarp();
       for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
         const int rr = lane_base + __ffs(todo) - 1;
-        out_row<__nv_bfloat16>(w, s, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+        out_row<__nv_bfloat16>(w, at, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
       }
     }
   }

@@ -72,6 +72,7 @@ __device__ __forceinline__ bool find_piece(const Win& w, int x, Count count, Til
   const int lane = threadIdx.x & 31;
   int base = 0;
   bool found = false, wrong = false;
+#pragma unroll 1
   for (int b0 = 0; b0 < w.B; b0 += 32) {
     const int b = b0 + lane;
     const bool in = b < w.B;
@@ -126,16 +127,31 @@ __device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool ove
 // one CTA without a tile: sum over b of ceil(n_b / per) <= rows / per + B.
 inline long tile_grid(long rows, int per, int batch) { return rows / per + batch + 1; }
 
-// The CTAs without a tile (number x of the grid's `grid`) set the rows outside
-// [cu[0], cu[B]) of a tensor of T rows of `words` 32-bit words to `value`.
+// Warp number part of `parts` sets its share of the rows outside [cu[0], cu[B])
+// of a tensor of T rows of `words` 32-bit words to `value`.
 __device__ __forceinline__ void fill_outside(const Win& w, const int32_t* cu, int T, void* base, int words,
-                                             uint32_t value, int x, int grid, const Tiles& all) {
+                                             uint32_t value, int part, int parts) {
   const long c0 = __ldg(cu), c1 = __ldg(cu + w.B);
   const long before = c0 * words, total = before + (T - c1) * words;
   uint32_t* p = (uint32_t*)base;
-  for (long i = (long)(x - all.total) * blockDim.x + threadIdx.x; i < total;
-       i += (long)(grid - all.total) * blockDim.x)
+#pragma unroll 1
+  for (long i = part * 32L + (threadIdx.x & 31); i < total; i += parts * 32L)
     p[i < before ? i : c1 * words + (i - before)] = value;
+}
+
+// Compile-time answers passed to generic lambdas.
+struct TrueType {
+  static constexpr bool value = true;
+};
+struct FalseType {
+  static constexpr bool value = false;
+};
+
+// SMs of the current device.
+inline int sm_count() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 148;
 }
 
 // ---- row by row -----------------------------------------------------------------
@@ -170,7 +186,9 @@ __device__ __forceinline__ float dot2(float2 a, float2 b) {
 template <typename F>
 __device__ __forceinline__ void for_visible(const Win& w, int p, F f) {
   const int low = window_low(w, p);
+#pragma unroll 1
   for (int j = 0; j < min(w.sinks, low); ++j) f(j);
+#pragma unroll 1
   for (int j = low; j <= p; ++j) f(j);
 }
 

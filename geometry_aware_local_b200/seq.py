@@ -26,7 +26,7 @@ import ctypes
 import math
 from typing import Optional
 
-from . import BF16, F32, Pack3DError, _check, check_status, lib
+from . import BF16, F32, Pack3DError, check_status, lib
 
 DH = 64
 
@@ -82,27 +82,38 @@ def validate_seq(cfg: SeqConfig) -> int:
 
 
 # ---- checks ------------------------------------------------------------------
+# The checks run before every launch, so the common case is one expression per
+# tensor; what is wrong is looked up only where something is.
 
-def _require(what, name, t, dtype, shape, device):
-    """Refuses, before anything runs, a tensor that is not what the kernels will take it for."""
+def _refuse(what, cfg, name, t, dtype, shape, device):
+    st = validate_seq(cfg)
+    if st != 0:
+        raise Pack3DError(st, what)
     if t.dtype != dtype:
         raise ValueError(f"{what}: {name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: {name} must have the shape {shape}, got {tuple(t.shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what}: {name} must be a CUDA tensor")
     if t.device != device:
         raise ValueError(f"{what}: {name} is on {t.device}, other tensors on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be contiguous")
+    raise ValueError(f"{what}: {name} must be contiguous")
 
 
-def _start(what, cfg):
-    import torch
-    st = validate_seq(cfg)
-    if st != 0:
-        raise Pack3DError(st, what)
-    return torch, (torch.bfloat16 if cfg.dtype == BF16 else torch.float32)
+def _require(what, cfg, name, t, dtype, shape, device):
+    """Refuses, before anything runs, a tensor that is not what the kernels will take it for."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous() or not t.is_cuda:
+        _refuse(what, cfg, name, t, dtype, shape, device)
+
+
+_modules = []
+
+
+def _torch():
+    if not _modules:       # torch is imported with the first call, not with the package
+        import torch
+        _modules.append((torch, {BF16: torch.bfloat16, F32: torch.float32}))
+    return _modules[0]
 
 
 def _check_err_word(what, err, device, torch):
@@ -110,8 +121,13 @@ def _check_err_word(what, err, device, torch):
         raise ValueError(f"{what}: the error word must be an int32 tensor of at least one element on {device}")
 
 
-def _owned(what, stream, *tensors):
-    if stream is not None and any(t is None for t in tensors):
+def _check_workspace(what, workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{what}: the workspace must be a contiguous tensor on {device}")
+
+
+def _owned(what, *tensors):
+    if any(t is None for t in tensors):
         raise ValueError(f"{what}: with an explicit stream, give every output and the workspace too")
 
 
@@ -119,30 +135,39 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(device):
+    """The device's current stream as the handle the C ABI takes.  (torch.cuda.current_stream builds an object for
+    it, which takes longer than the launch itself of a small call.)"""
+    return _modules[0][0]._C._cuda_getCurrentRawStream(device.index)
+
+
 def _call(torch, what, fn, device, stream, *args):
     """Runs a C entry point on `stream` (the device's current one by default) with the tensors' device current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream), what)
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream), what)
+            st = fn(*args, stream)
+    if st != 0:
+        raise Pack3DError(st, what)
 
 
 def _window_args(what, cfg, q, k, v, cu_q, cu_k):
-    torch, T = _start(what, cfg)
+    torch, types = _torch()
     if q.dim() != 3 or k.dim() != 3 or cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError(f"{what}: q and k are [rows, heads, {DH}], cu_q is [batch + 1]")
-    dev = q.device
-    _require(what, "q", q, T, (q.shape[0], cfg.Hq, DH), dev)
-    _require(what, "k", k, T, (k.shape[0], cfg.Hkv, DH), dev)
-    _require(what, "v", v, T, (k.shape[0], cfg.Hkv, DH), dev)
-    _require(what, "cu_q", cu_q, torch.int32, (cu_q.shape[0],), dev)
+    T, dev = types.get(cfg.dtype), q.device
+    keys = (k.shape[0], cfg.Hkv, DH)
+    _require(what, cfg, "q", q, T, (q.shape[0], cfg.Hq, DH), dev)
+    _require(what, cfg, "k", k, T, keys, dev)
+    _require(what, cfg, "v", v, T, keys, dev)
+    _require(what, cfg, "cu_q", cu_q, torch.int32, cu_q.shape, dev)
     if cu_k is not cu_q:
-        _require(what, "cu_k", cu_k, torch.int32, (cu_q.shape[0],), dev)
+        _require(what, cfg, "cu_k", cu_k, torch.int32, cu_q.shape, dev)
     return torch, T, dev
 
 
@@ -155,7 +180,8 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
     what = "pack3d_window_attn"
     cu_k = cu_q if cu_k is None else cu_k
     torch, T, dev = _window_args(what, cfg, q, k, v, cu_q, cu_k)
-    _owned(what, stream, out, lse)
+    if stream is not None:
+        _owned(what, out, lse)
     if (out is None) != (lse is None):
         raise ValueError(f"{what}: give both out and lse or none of them")
     new = out is None
@@ -165,8 +191,8 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
             return out.zero_(), lse.fill_(-math.inf)
     else:
-        _require(what, "out", out, T, tuple(q.shape), dev)
-        _require(what, "lse", lse, torch.float32, tuple(q.shape[:2]), dev)
+        _require(what, cfg, "out", out, T, tuple(q.shape), dev)
+        _require(what, cfg, "lse", lse, torch.float32, tuple(q.shape[:2]), dev)
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_window_attn, dev, stream, ctypes.byref(cfg), cu_q.shape[0] - 1, q.shape[0],
           k.shape[0], cu_q.data_ptr(), cu_k.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -185,10 +211,11 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     what = "pack3d_window_attn_bwd"
     cu_k = cu_q if cu_k is None else cu_k
     torch, T, dev = _window_args(what, cfg, q, k, v, cu_q, cu_k)
-    _owned(what, stream, dq, dk, dv, workspace)
+    if stream is not None:
+        _owned(what, dq, dk, dv, workspace)
     for name, t in (("out", out), ("dout", dout)):
-        _require(what, name, t, T, tuple(q.shape), dev)
-    _require(what, "lse", lse, torch.float32, tuple(q.shape[:2]), dev)
+        _require(what, cfg, name, t, T, tuple(q.shape), dev)
+    _require(what, cfg, "lse", lse, torch.float32, tuple(q.shape[:2]), dev)
     new = dq is None
     if (dk is None) != new or (dv is None) != new:
         raise ValueError(f"{what}: give all of dq, dk and dv or none of them")
@@ -197,12 +224,12 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
         return tuple(t.zero_() for t in grads)
     if not new:
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            _require(what, name, t, T, tuple(like.shape), dev)
+            _require(what, cfg, name, t, T, tuple(like.shape), dev)
     if workspace is None:
         n = window_attn_bwd_workspace_bytes(cfg, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"{what}: the workspace must be a contiguous tensor on {dev}")
+    else:
+        _check_workspace(what, workspace, dev)
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), cu_q.shape[0] - 1, q.shape[0],
           k.shape[0], cu_q.data_ptr(), cu_k.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -250,15 +277,15 @@ def _autograd():
 # ---- the paged cache ------------------------------------------------------------------
 
 def _cache_args(what, cfg, k_pages, v_pages, table, lengths):
-    torch, T = _start(what, cfg)
+    torch, types = _torch()
     if k_pages.dim() != 4 or table.dim() != 2:
         raise ValueError(f"{what}: the pages are [num_pages, page, Hkv, {DH}], the table is [batch, max_pages]")
-    dev = k_pages.device
+    T, dev = types.get(cfg.dtype), k_pages.device
     shape = (k_pages.shape[0], cfg.page, cfg.Hkv, DH)
-    _require(what, "k_pages", k_pages, T, shape, dev)
-    _require(what, "v_pages", v_pages, T, shape, dev)
-    _require(what, "table", table, torch.int32, tuple(table.shape), dev)
-    _require(what, "lengths", lengths, torch.int32, (table.shape[0],), dev)
+    _require(what, cfg, "k_pages", k_pages, T, shape, dev)
+    _require(what, cfg, "v_pages", v_pages, T, shape, dev)
+    _require(what, cfg, "table", table, torch.int32, table.shape, dev)
+    _require(what, cfg, "lengths", lengths, torch.int32, (table.shape[0],), dev)
     return torch, T, dev
 
 
@@ -268,10 +295,10 @@ def cache_append(cfg: SeqConfig, k, v, k_pages, v_pages, table, lengths, cu=None
     what = "pack3d_cache_append"
     torch, T, dev = _cache_args(what, cfg, k_pages, v_pages, table, lengths)
     rows = k.shape[0]
-    _require(what, "k", k, T, (rows, cfg.Hkv, DH), dev)
-    _require(what, "v", v, T, (rows, cfg.Hkv, DH), dev)
+    _require(what, cfg, "k", k, T, (rows, cfg.Hkv, DH), dev)
+    _require(what, cfg, "v", v, T, (rows, cfg.Hkv, DH), dev)
     if cu is not None:
-        _require(what, "cu", cu, torch.int32, (table.shape[0] + 1,), dev)
+        _require(what, cfg, "cu", cu, torch.int32, (table.shape[0] + 1,), dev)
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_cache_append, dev, stream, ctypes.byref(cfg), table.shape[0], rows, _p(cu),
           lengths.data_ptr(), table.data_ptr(), table.shape[1], k_pages.shape[0], k.data_ptr(), v.data_ptr(),
@@ -290,23 +317,24 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     what = "pack3d_cache_attn"
     torch, T, dev = _cache_args(what, cfg, k_pages, v_pages, table, lengths)
     batch, max_pages = table.shape
-    _require(what, "q", q, T, (batch, cfg.Hq, DH), dev)
-    _owned(what, stream, out, lse, workspace)
+    _require(what, cfg, "q", q, T, (batch, cfg.Hq, DH), dev)
+    if stream is not None:
+        _owned(what, out, lse, workspace)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _require(what, "out", out, T, tuple(q.shape), dev)
+        _require(what, cfg, "out", out, T, tuple(q.shape), dev)
     if lse is None:
         lse = torch.empty((batch, cfg.Hq), dtype=torch.float32, device=dev)
     else:
-        _require(what, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
+        _require(what, cfg, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
     if weights is not None:
-        _require(what, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
+        _require(what, cfg, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
     if workspace is None:
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"{what}: the workspace must be a contiguous tensor on {dev}")
+    else:
+        _check_workspace(what, workspace, dev)
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_cache_attn, dev, stream, ctypes.byref(cfg), batch, q.data_ptr(),
           k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), max_pages, k_pages.shape[0], lengths.data_ptr(),
@@ -323,11 +351,12 @@ def cache_evict(cfg: SeqConfig, k_pages, v_pages, table, lengths, weights, new_t
     what = "pack3d_cache_evict"
     torch, T, dev = _cache_args(what, cfg, k_pages, v_pages, table, lengths)
     batch, max_pages = table.shape
-    _require(what, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
+    _require(what, cfg, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
     if new_table.dim() != 2:
         raise ValueError(f"{what}: new_table is [batch, new_max_pages]")
-    _require(what, "new_table", new_table, torch.int32, (batch, new_table.shape[1]), dev)
-    _owned(what, stream, kept, new_weights, new_lengths)
+    _require(what, cfg, "new_table", new_table, torch.int32, (batch, new_table.shape[1]), dev)
+    if stream is not None:
+        _owned(what, kept, new_weights, new_lengths)
     shapes = ((batch, max(int(budget), 0)), (batch, new_table.shape[1] * cfg.page), (batch,))
     outs = []
     for name, t, dt, shape in (("kept", kept, torch.int32, shapes[0]), ("new_weights", new_weights, torch.float32,
@@ -335,7 +364,7 @@ def cache_evict(cfg: SeqConfig, k_pages, v_pages, table, lengths, weights, new_t
         if t is None:
             t = torch.empty(shape, dtype=dt, device=dev)
         else:
-            _require(what, name, t, dt, shape, dev)
+            _require(what, cfg, name, t, dt, shape, dev)
         outs.append(t)
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_cache_evict, dev, stream, ctypes.byref(cfg), batch, k_pages.data_ptr(),
@@ -353,7 +382,11 @@ class PagedCache:
     ones.  Nothing here waits for the device; check() does."""
 
     def __init__(self, cfg: SeqConfig, batch: int, capacity: int, budget: int = 0, device="cuda"):
-        torch, T = _start("PagedCache", cfg)
+        st = validate_seq(cfg)
+        if st != 0:
+            raise Pack3DError(st, "PagedCache")
+        torch, types = _torch()
+        T = types[cfg.dtype]
         if batch < 1 or capacity < 1 or budget < 0 or budget > capacity:
             raise ValueError("PagedCache: batch and capacity are at least 1, the budget is at most the capacity")
         self.cfg, self.budget = cfg, budget
@@ -397,8 +430,7 @@ class PagedCache:
         return kept
 
     def check(self):
-        import torch
-        with torch.cuda.device(self.err.device):
+        with _torch()[0].cuda.device(self.err.device):
             st = check_status(self.err)
         if st != 0:
             raise Pack3DError(st, "PagedCache")
