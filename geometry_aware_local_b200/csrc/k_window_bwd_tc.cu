@@ -62,10 +62,8 @@ constexpr int kBarOff = kStageOff + kStages * kStageBytes;
 // barriers: full[S], empty[S], qfull, s_full, s_free, p_full, p_free, o_final, drain
 constexpr int kNumBars = 2 * kStages + 7;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
-constexpr int kTileOff = kCtlOff + 32;
-constexpr int kSmemBytes = kTileOff + 64 + 1024;
+constexpr int kSmemBytes = kCtlOff + 32 + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(sizeof(Tile) + sizeof(Tiles) + 4 <= 64 && kBarOff % 8 == 0, "tile slot");
 constexpr uint32_t kIdescDQ = ptx::idesc_bf16_f32(kRowsPerTile, kDh, true);  // dQ: N = 64 dims, K MN-major
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -84,23 +82,16 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                  o_final = qfull + 40, drain = qfull + 48;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
-  Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
-  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
-  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
-  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kRowsPerTile >> w.gshift;
 
-  if (warp == 0) {
-    Tile s;
-    Tiles all;
-    const bool found = find_tile(w, blockIdx.x, tokens, false, &s, &all);
-    if (lane == 0) {
-      *tile_slot = s;
-      *tiles_slot = all;
-      *found_slot = found;
-    }
-  }
-  if (threadIdx.x == 32) {
+  // The producer sets the barriers up, and every warp finds the tile for
+  // itself, so that the first loads are under way before the CTA meets.
+  if (warp == kTmaWarp && lane == 0) {
+    ptx::tma_prefetch(&tmQ);
+    ptx::tma_prefetch(&tmO);
+    ptx::tma_prefetch(&tmK);
+    ptx::tma_prefetch(&tmV);
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), 1);
@@ -117,9 +108,10 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     ctl->limit_ns = w.wait_ns;
     ptx::fence_mbar_init();
   }
-  __syncthreads();
-  if (!*found_slot) {
-    const Tiles all = *tiles_slot;
+  __syncwarp();
+  Tile s;
+  Tiles all;
+  if (!find_tile(w, blockIdx.x, tokens, false, &s, &all)) {
     if (all.bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
     } else if (w.zero_outside && blockIdx.y == 0) {
@@ -129,6 +121,30 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
     return;
   }
+  s.t = s.n - 1 - s.t;      // the tiles with most keys first
+  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
+  const int p0 = position(s, r0), p1 = position(s, r1);
+  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
+  const int T = kt.n, T_load = w.stall ? T - 1 : T;
+  auto load_tile = [&](int j) {
+    const int st = j % kStages;
+    const uint32_t dst = sbase + kStageOff + st * kStageBytes;
+    const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
+    ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
+#pragma unroll 1
+    for (int c = 0; c < cols / 32; ++c) {
+      ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
+      ptx::tma_load_3d(dst + kKVBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
+    }
+  };
+  if (warp == kTmaWarp && lane == 0 && T > 0) {
+    ptx::mbar_expect_tx(qfull, 2 * kQTileBytes);
+    ptx::tma_load_4d(sbase + kQOff, &tmQ, 0, 0, g, s.q0 + r0, qfull);
+    ptx::tma_load_4d(sbase + kDOOff, &tmO, 0, 0, g, s.q0 + r0, qfull);
+#pragma unroll 1
+    for (int j = 0; j < min(T_load, kStages); ++j) load_tile(j);
+    ctl->issued = min(T_load, kStages);
+  }
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
@@ -137,41 +153,21 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Tile s = *tile_slot;
-  s.t = s.n - 1 - s.t;      // the tiles with most keys first
-  const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
-  const int p0 = position(s, r0), p1 = position(s, r1);
-  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
-  const int T = kt.n;
 
   if (warp == kTmaWarp) {
-    if (lane == 0 && T > 0) {
-      ptx::tma_prefetch(&tmQ);
-      ptx::tma_prefetch(&tmO);
-      ptx::tma_prefetch(&tmK);
-      ptx::tma_prefetch(&tmV);
-      ptx::mbar_expect_tx(qfull, 2 * kQTileBytes);
-      ptx::tma_load_4d(sbase + kQOff, &tmQ, 0, 0, g, s.q0 + r0, qfull);
-      ptx::tma_load_4d(sbase + kDOOff, &tmO, 0, 0, g, s.q0 + r0, qfull);
-      const int T_load = w.stall ? T - 1 : T;
-      int issued = 0;
-      for (int j = 0; j < T_load; ++j) {
-        const int st = j % kStages;
-        if (j >= kStages && !wait(empty(st), ((j / kStages) - 1) & 1)) break;
-        const uint32_t dst = sbase + kStageOff + st * kStageBytes;
-        const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
-        ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
-        for (int c = 0; c < cols / 32; ++c) {
-          ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
-          ptx::tma_load_3d(dst + kKVBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
-        }
+    if (lane == 0) {
+      int issued = min(T_load, kStages);
+#pragma unroll 1
+      for (int j = issued; j < T_load; ++j) {
+        if (!wait(empty(j % kStages), ((j / kStages) - 1) & 1)) break;
+        load_tile(j);
         issued = j + 1;
       }
       ctl->issued = issued;
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && T > 0) {
+    if (T > 0 && ptx::elect_one()) {
       const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDS = tmem + kColDS, tDQ = tmem + kColDQ;
       auto issue_sdp = [&](int j) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
@@ -189,9 +185,11 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       };
       auto issue_dq = [&](int j) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
-        const int steps = kt.cols(j) / 16;
-        for (int kk = 0; kk < steps; ++kk)
-          ptx::mma_ts(tDQ, tDS + kk * 8, ptx::smem_desc_sw128(kaddr + kk * 2048, 8192, 1024), kIdescDQ,
+        const int cols = kt.cols(j);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          if (kk * 16 < cols)
+            ptx::mma_ts(tDQ, tDS + kk * 8, ptx::smem_desc_sw128(kaddr + kk * 2048, 8192, 1024), kIdescDQ,
                       (j > 0 || kk > 0) ? 1u : 0u);
         ptx::tc_commit(p_free);
         ptx::tc_commit(empty(j % kStages));
@@ -202,6 +200,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ptx::tc_fence_after();
         issue_sdp(0);
       }
+#pragma unroll 1
       for (int j = 0; ok && j < T; ++j) {
         if (j + 1 < T) {
           if (!(ok = wait(s_free, j & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
@@ -246,6 +245,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const float2 c2 = make_float2(w.scale_log2, w.scale_log2), nl2 = make_float2(-lse2, -lse2);
     const float2 nd2 = make_float2(-delta, -delta);
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < T; ++j) {
       if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
       ptx::tc_fence_after();
@@ -422,7 +422,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
   int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
   volatile uint8_t* redo = smem + kRedoOff;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kRowsPerTile >> w.gshift;
   const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
   const int x = far ? blockIdx.x - key_grid : blockIdx.x;
@@ -504,6 +504,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::tma_load_3d(sbase + kVOff, &tmV, 0, g, s.k0 + j0, kvfull);
       const int nsteps_load = w.stall ? nsteps - 1 : nsteps;
       int issued = 0;
+#pragma unroll 1
       for (int t = 0; t < nsteps_load; ++t) {
         const int st = t % kStages;
         if (t >= kStages && !wait(empty(st), ((t / kStages) - 1) & 1)) break;
@@ -518,7 +519,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     }
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
-    if (lane == 0 && nsteps > 0) {
+    if (nsteps > 0 && ptx::elect_one()) {
       const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDK = tmem + kColDK, tDV = tmem + kColDV;
       auto issue_sdp = [&](int t) {
         const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
@@ -552,6 +553,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       bool ok = true;
       if (warp == kMmaWarp) {
         ok = wait(kvfull, 0);
+#pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
           if (!(ok = wait(full(t % kStages), (t / kStages) & 1))) break;
           if (t > 0 && !(ok = wait(s_free, (t - 1) & 1))) break;
@@ -559,6 +561,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           issue_sdp(t);
         }
       } else {
+#pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
           if (!(ok = wait(p_full, t & 1))) break;
           ptx::tc_fence_after();
@@ -577,6 +580,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const int h = (g << w.gshift) + (rl & (w.G - 1));
     const int c0 = j0 + 32 * c;                  // the chunk's first key
     bool ok = true;
+#pragma unroll 1
     for (int t = 0; t < nsteps; ++t) {
       const int rs = ra + t * tokens;            // the step's first row
       const int r = rs + (rl >> w.gshift);

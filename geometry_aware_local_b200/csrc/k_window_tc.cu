@@ -8,19 +8,33 @@
 // heads that share keys share every key tile.  The tile's visible keys are one
 // range [lo, hi] (the first token's window to the last token) and, where the
 // window has moved past them, the sinks as one short tile in front.  Keys come
-// in tiles of 128 from lo on; the last tile, and the sinks' one, are cut to a
+// in tiles of 96 from lo on; the last tile, and the sinks' one, are cut to a
 // multiple of 32 columns, so the work follows the range in steps of 32 keys.
 // Masks are evaluated only in the 32-column chunks that some row sees in part.
 //   * the last warp loads the Q tile and a ring of K / V tiles by TMA (boxes of
-//     32 keys x 64 dims, 128-byte swizzle);
+//     32 keys x 64 dims, 128-byte swizzle); the first loads are under way
+//     before the CTA first meets;
 //   * one warp issues tcgen05.mma: S = Q K^T (M=128, N = the tile's columns,
 //     K=64) into tensor memory and O += P V (N=64) with P from tensor memory;
 //   * four softmax warps (thread = row = TMEM lane) run the online softmax in
 //     base 2 with a lazily moved maximum: O is rescaled only when a row maximum
 //     grows by more than 2^8.
-// Two CTAs per SM (256 tensor-memory columns each: S 128, P 64, O 64) hide each
-// other's hand-offs.  At d_h = 64 an exponential pairs with only 256 MMA flops,
-// so the softmax warps set the pace.
+// Tensor memory of a CTA, 256 columns (two CTAs per SM): two regions of 96 and
+// O (64).  Tile j's S and then, over it, its P (packed bf16) are in region
+// j % 2: a warp has its rows of S in registers before it writes P.  S of tile
+// j + 1 is under way while tile j is exponentiated, and S of tile j + 2 follows
+// the product with P of tile j.  (S and two P buffers apart, one S region: 0.298
+// against 0.288 ms at the size below.)
+//
+// At d_h = 64 an exponential pairs with only 256 MMA flops, so the bound is the
+// exponentials' rate (16 a clock and SM: 0.12 ms at that size); what paces the
+// kernel is the softmax warps' chain of a tile (wait, load, maximum,
+// exponentials, store, arrive), of which two CTAs overlap, and a CTA's start
+// and end, which a window of 1,024 keys pays every 11 tiles.  The code is kept
+// small on purpose: the roles' loops evict one another from the instruction
+// cache, and a second copy of the softmax body for tiles without masks made the
+// kernel a quarter slower.  Persistent CTAs that walk the tiles measured 0.320 ms.
+// 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.288 ms, 475 TFLOP/s.
 //
 // A key that a row does not see has P = 0 exactly; where its value row holds a
 // NaN or an infinity, 0 times it is a NaN.  A row whose result is not finite is
@@ -33,13 +47,13 @@ namespace {
 
 constexpr int kBM = kRowsPerTile, kBN = 96;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kThreads = 192;
-constexpr int kColS = 0, kColP = kBN, kColO = 2 * kBN, kTmemCols = 256;   // P buffer b at kColP + b * kBN / 2
+constexpr int kColO = 2 * kBN, kTmemCols = 256;   // tile j: S, then P over it, at (j & 1) * kBN
 static_assert(kColO + kDh <= kTmemCols, "tensor memory plan");
 constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2;
 constexpr int kStages = 3;
 constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;     // K at +0, V at +kTileBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, s_full, s_free, p_full[2], p_free[2], o_final, drain
+// barriers: full[S], empty[S], qfull, s_full[2], p_full[2], pv_done[2], o_final, drain
 constexpr int kNumBars = 2 * kStages + 9;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kPlanOff = kCtlOff + 32;
@@ -75,12 +89,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
   const uint32_t qfull = bar0 + 8 * (2 * kStages);
-  const uint32_t s_full = qfull + 8, s_free = qfull + 16, o_final = qfull + 24, drain = qfull + 32;
+  const uint32_t o_final = qfull + 8, drain = qfull + 16;
+  auto s_full = [&](int b) { return qfull + 24 + 8 * b; };
   auto p_full = [&](int b) { return qfull + 40 + 8 * b; };
-  auto p_free = [&](int b) { return qfull + 56 + 8 * b; };
+  auto pv_done = [&](int b) { return qfull + 56 + 8 * b; };
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
-  auto wait = [&](uint32_t bar, uint32_t parity) { return ptx::mbar_wait(bar, parity, ctl); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kBM >> w.gshift;     // per tile
 
   // The producer sets the barriers up, and every warp finds the tile for
@@ -94,11 +109,10 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       ptx::mbar_init(empty(s), 1);
     }
     ptx::mbar_init(qfull, 1);
-    ptx::mbar_init(s_full, 1);
-    ptx::mbar_init(s_free, 4);
     for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(s_full(b), 1);
       ptx::mbar_init(p_full(b), 4);
-      ptx::mbar_init(p_free(b), 1);
+      ptx::mbar_init(pv_done(b), 1);
     }
     ptx::mbar_init(o_final, 1);
     ptx::mbar_init(drain, 1);
@@ -170,16 +184,16 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0 && T > 0) {
-      const uint32_t tS = tmem + kColS, tP = tmem + kColP, tO = tmem + kColO;
+    if (T > 0 && ptx::elect_one()) {
+      const uint32_t tO = tmem + kColO;
       auto issue_s = [&](int j) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
         const uint32_t idesc = ptx::idesc_bf16_f32(kBM, kt.cols(j), false);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kk * 32, 16, 1024),
+          ptx::mma_ss(tmem + (j & 1) * kBN, ptx::smem_desc_sw128(sbase + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(kaddr + kk * 32, 16, 1024), idesc, kk > 0);
-        ptx::tc_commit(s_full);
+        ptx::tc_commit(s_full(j & 1));
       };
       auto issue_pv = [&](int j) {
         const uint32_t vaddr = sbase + kStageOff + (j % kStages) * kStageBytes + kTileBytes;
@@ -187,26 +201,27 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           if (kk * 16 < cols)
-            ptx::mma_ts(tO, tP + (j & 1) * (kBN / 2) + kk * 8, ptx::smem_desc_sw128(vaddr + kk * 2048, 8192, 1024),
+            ptx::mma_ts(tO, tmem + (j & 1) * kBN + kk * 8, ptx::smem_desc_sw128(vaddr + kk * 2048, 8192, 1024),
                         kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
-        ptx::tc_commit(p_free(j & 1));
+        ptx::tc_commit(pv_done(j & 1));
         ptx::tc_commit(empty(j % kStages));
         if (j == T - 1) ptx::tc_commit(o_final);
       };
-      bool ok = wait(qfull, 0) && wait(full(0), 0);
-      if (ok) {
-        ptx::tc_fence_after();
-        issue_s(0);
-      }
-      for (int j = 0; ok && j < T; ++j) {
-        if (j + 1 < T) {
-          if (!(ok = wait(s_free, j & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
+      bool ok = wait(qfull, 0);
+#pragma unroll 1
+      for (int j = -2; ok && j < T; ++j) {
+        if (j >= 0) {
+          if (!(ok = wait(p_full(j & 1), (j >> 1) & 1))) break;
           ptx::tc_fence_after();
-          issue_s(j + 1);
+          issue_pv(j);
         }
-        if (!(ok = wait(p_full(j & 1), (j >> 1) & 1))) break;
-        ptx::tc_fence_after();
-        issue_pv(j);
+        if (j + 2 < T) {
+          // S of tile j + 2 goes where P of tile j is: once its product is done.
+          if (!(ok = (j < 0 || wait(pv_done(j & 1), (j >> 1) & 1)) && wait(full((j + 2) % kStages), ((j + 2) / kStages) & 1)))
+            break;
+          ptx::tc_fence_after();
+          issue_s(j + 2);
+        }
       }
     }
     __syncwarp();
@@ -230,13 +245,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 #pragma unroll 1
     for (int j = 0; j < T; ++j) {
       const int k0 = kt.begin(j), cols = kt.cols(j);
-      if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full(j & 1), (j >> 1) & 1)))) break;
       ptx::tc_fence_after();
+      const uint32_t tS = trow + (j & 1) * kBN;
       uint32_t sv[kBN];
-      if (cols > 32) ptx::tmem_ld64_sync(trow + kColS, sv);
-      else ptx::tmem_ld32_sync(trow + kColS, sv);
-      if (cols > 64) ptx::tmem_ld32_sync(trow + kColS + 64, sv + 64);
-      warp_arrive(s_free);
+      if (cols > 32) ptx::tmem_ld64_sync(tS, sv);
+      else ptx::tmem_ld32_sync(tS, sv);
+      if (cols > 64) ptx::tmem_ld32_sync(tS + 64, sv + 64);
       float mx = -INFINITY;
 #pragma unroll
       for (int q = 0; q < kBN / 32; ++q) {
@@ -269,17 +284,11 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         m_used = mxs;
       }
       const bool rescale = j > 0 && __any_sync(0xffffffffu, f != 1.f);
-      if (j > 1) {
-        // This P buffer's last tile has been read by its O += P V.
-        if (!(ok = __all_sync(0xffffffffu, wait(p_free(j & 1), ((j >> 1) - 1) & 1)))) break;
-        ptx::tc_fence_after();
-      }
       // A row that has seen no key yet (maximum -infinity) has only scores of
       // -infinity here: any finite shift gives their weight 0.
       const float shift = m_used == -INFINITY ? 0.f : -m_used;
       const float2 c2 = make_float2(c, c), nm2 = make_float2(shift, shift);
       float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const uint32_t tP = trow + kColP + (j & 1) * (kBN / 2);
 #pragma unroll
       for (int q = 0; q < kBN / 32; ++q) {
         if (32 * q >= cols) break;
@@ -292,11 +301,11 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           rs[k & 1] = __fadd2_rn(rs[k & 1], pr);
           pk[k] = pack_bf16x2(pr.x, pr.y);
         }
-        ptx::tmem_st16(tP + 16 * q, pk);
+        ptx::tmem_st16(tS + 16 * q, pk);
       }
       if (rescale) {
         // After the last tile's O += P V and before this one's.
-        if (!(ok = __all_sync(0xffffffffu, wait(p_free((j - 1) & 1), ((j - 1) >> 1) & 1)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait(pv_done((j - 1) & 1), ((j - 1) >> 1) & 1)))) break;
         ptx::tc_fence_after();
         uint32_t o[16];
 #pragma unroll

@@ -139,14 +139,6 @@ __device__ __forceinline__ void fill_outside(const Win& w, const int32_t* cu, in
     p[i < before ? i : c1 * words + (i - before)] = value;
 }
 
-// Compile-time answers passed to generic lambdas.
-struct TrueType {
-  static constexpr bool value = true;
-};
-struct FalseType {
-  static constexpr bool value = false;
-};
-
 // SMs of the current device.
 inline int sm_count() {
   int dev = 0, n = 148;

@@ -15,6 +15,14 @@ namespace seq {
 constexpr int kRowsPerTile = 128;                     // (token, query head) rows of a query tile
 constexpr int kChunkBytes = 32 * kDh * 2;             // 32 keys of one head
 
+// mbar_wait with its slow half out of line: the roles' loops stay short.
+__device__ __noinline__ inline bool wait_on(uint32_t bar, uint32_t parity, volatile ptx::WaitCtl* ctl) {
+  return ptx::mbar_wait(bar, parity, ctl);
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile ptx::WaitCtl* ctl) {
+  return ptx::mbar_try_wait(bar, parity) || wait_on(bar, parity, ctl);
+}
+
 // The key tiles of a query tile: number j starts at key begin(j) of the
 // sequence and has cols(j) columns, a multiple of 32, BN at most.
 template <int BN>
