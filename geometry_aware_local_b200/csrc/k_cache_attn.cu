@@ -2,8 +2,10 @@
 //
 // Every visible key and value row is read once and serves the G query heads of
 // its key head; there is no reuse beyond that, so HBM bounds the work and the
-// kernels read straight into registers, one tile of 16 slots ahead, without
-// shared memory.
+// kernels are built to keep enough reads in flight.  Each lane copies (cp.async)
+// the 16-byte chunks that it will use itself into a queue of its own in shared
+// memory, two 4 KiB stages a warp ahead: no lane waits for another, and the
+// reads in flight (16 warps an SM) take no registers.
 //
 // Split and join.  The work is one line of units - (sequence, key head, tile of
 // 16 visible slots), sequences of very different lengths behind one another -
@@ -11,7 +13,7 @@
 // warp: every processor reads the same number of rows whatever the lengths
 // are.  A warp keeps the online softmax (maximum, sum, weighted values) of the
 // piece of a (sequence, key head) it is in.  A piece that is whole is written
-// out; the others of a CTA are joined in shared memory, and what is still part
+// out; the others of a CTA are joined in shared memory, a warp a head, and what is still part
 // of a longer one goes to the workspace (two slots a CTA at most: the run's
 // first and last), where cache_join_kernel adds the parts in order.  Short
 // caches, and batches that fill the GPU by themselves, take one CTA per
@@ -25,6 +27,7 @@
 // slots free for the loads.  P is rounded to bf16 for the product.
 // float: 16 lanes share a row, two rows at a time, on CUDA cores.
 #include "seq.cuh"
+#include "tc_ptx.cuh"
 
 namespace pack3d {
 namespace seq {
@@ -64,6 +67,8 @@ __device__ __forceinline__ Seen seen(const Cache& c, int n) {
   v.count = v.s0 + n - v.lo;
   return v;
 }
+
+
 __device__ __forceinline__ int units_of(const Cache& c, int b) {
   return (seen(c, cached(c, b)).count + kSlots - 1) / kSlots;
 }
@@ -72,30 +77,32 @@ __device__ __forceinline__ int units_of(const Cache& c, int b) {
 struct Unit {
   int b, g, t, tiles;
 };
-// Tiles [t0, t1) of a (sequence, key head), in shared memory; b < 0: none.
+// The tiles [t0, t1) of a (sequence, key head) that a piece covers; b < 0: none.
 struct Span {
   int b, g, t0, t1;
 };
 
-// All sequences' units (one warp), and with `u` >= 0 where unit u lies.
-__device__ __forceinline__ long find_unit(const Cache& c, long u, Unit* at) {
+// All sequences' units (one warp), and with `u` >= 0 where unit u lies.  A
+// split call has fewer than 2^31 (is_split).
+__device__ __noinline__ int find_unit(const Cache& c, int u, Unit* at) {
   const int lane = threadIdx.x & 31;
-  long base = 0;
+  int base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int tiles = b0 + lane < c.B ? units_of(c, b0 + lane) : 0;
-    long incl = (long)tiles * c.Hkv;
+    const int tiles = b0 + lane < c.B ? units_of(c, b0 + lane) : 0, own = tiles * c.Hkv;
+    int incl = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long up = __shfl_up_sync(0xffffffffu, incl, d);
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += up;
     }
-    const long first = base + incl - (long)tiles * c.Hkv;
-    const uint32_t hit = __ballot_sync(0xffffffffu, u >= first && u < first + (long)tiles * c.Hkv);
+    const int first = base + incl - own;
+    const uint32_t hit = __ballot_sync(0xffffffffu, u >= first && u < first + own);
     if (hit) {
       const int src = __ffs(hit) - 1;
       at->b = b0 + src;
       at->tiles = __shfl_sync(0xffffffffu, tiles, src);
-      const int in = (int)(u - __shfl_sync(0xffffffffu, first, src));
+      const int in = u - __shfl_sync(0xffffffffu, first, src);
       at->g = in / at->tiles;
       at->t = in - at->g * at->tiles;
     }
@@ -105,7 +112,7 @@ __device__ __forceinline__ long find_unit(const Cache& c, long u, Unit* at) {
 }
 
 // Units of one CTA's run: at least one per warp.
-__device__ __forceinline__ long run_units(long total, int ctas) { return max((total + ctas - 1) / ctas, (long)kWarps); }
+__device__ __forceinline__ int run_units(int total, int ctas) { return max((int)(((unsigned)total + ctas - 1) / ctas), kWarps); }
 
 // d += A B for the rows 0-7 of A (8-15 are zero, and so is what they give).
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
@@ -124,16 +131,18 @@ __device__ __forceinline__ int tile_rows(const Cache& c, const int32_t* table, c
   return i < v.count ? (int)pool_row(c, table, v.slot(i)) : -1;
 }
 
+// A stage of a warp's queue: eight 16-byte chunks a lane, chunk i of lane l at
+// 512 i + 16 l.
+constexpr int kStageBytes = 8 * 512, kDepth = 3;
+
 template <typename T, int G> struct Worker;
 
-// ---- bf16 -------------------------------------------------------------------------
+// ---- bf16: a stage is a unit -------------------------------------------------------
 // Lane (r, x) = (lane / 4, lane % 4): head row r; of the keys, token r (and
 // 8 + r) and the 16-byte chunks x and x + 4; of the values, the tokens 2x, 2x+1,
 // 8+2x, 8+2x+1 and the chunk r.
 template <int G> struct Worker<__nv_bfloat16, G> {
-  struct Data {
-    uint4 k[4], v[4];
-  };
+  static constexpr int kStages = 1;      // per unit
   uint32_t q[8];
   float o[8][2];
   float m, l;
@@ -149,51 +158,47 @@ template <int G> struct Worker<__nv_bfloat16, G> {
     q[0] = c0.x; q[1] = c0.y; q[2] = c0.z; q[3] = c0.w;
     q[4] = c1.x; q[5] = c1.y; q[6] = c1.z; q[7] = c1.w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) o[i][e] = 0.f;
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = 0.f;
     m = -INFINITY;
     l = 0.f;
   }
-  __device__ __forceinline__ static uint4 chunk(const uint4* base, long row, long step, int i) {
-    return row >= 0 ? __ldg(base + row * step + i) : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void load(const DecodeArgs& a, int g, int rows, Data& d) const {
+  // Copies of one unit whose pool rows are `rows`; a row that is not there gives zeros.
+  __device__ __forceinline__ static void issue(const DecodeArgs& a, int g, int rows, int, uint32_t stage) {
     const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
     const long step = (long)a.c.Hkv * 8;      // 16-byte chunks a pool row
     const uint4* k = reinterpret_cast<const uint4*>(a.c.k_pages) + g * 8;
     const uint4* v = reinterpret_cast<const uint4*>(a.c.v_pages) + g * 8;
-    const int k0 = __shfl_sync(0xffffffffu, rows, r), k1 = __shfl_sync(0xffffffffu, rows, 8 + r);
-    d.k[0] = chunk(k, k0, step, x);
-    d.k[1] = chunk(k, k0, step, x + 4);
-    d.k[2] = chunk(k, k1, step, x);
-    d.k[3] = chunk(k, k1, step, x + 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = __shfl_sync(0xffffffffu, rows, 8 * h + r);
+      const uint4* p = k + max(row, 0) * step + x;
+      ptx::cp_async16(stage + 1024 * h, p, row >= 0 ? 16 : 0);
+      ptx::cp_async16(stage + 1024 * h + 512, p + 4, row >= 0 ? 16 : 0);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int vr = __shfl_sync(0xffffffffu, rows, (i >> 1) * 8 + 2 * x + (i & 1));
-      d.v[i] = chunk(v, vr, step, r);
+      const int row = __shfl_sync(0xffffffffu, rows, (i >> 1) * 8 + 2 * x + (i & 1));
+      ptx::cp_async16(stage + 2048 + 512 * i, v + max(row, 0) * step + r, row >= 0 ? 16 : 0);
     }
   }
-  __device__ __forceinline__ void compute(const DecodeArgs& a, int rows, const Data& d, int t, float* logits) {
+  __device__ __forceinline__ void compute(const DecodeArgs& a, int count, uint32_t stage, int t, int, float* logits) {
     const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
     float s[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s[h][e] = 0.f;
-      const uint4 a0 = d.k[2 * h], a1 = d.k[2 * h + 1];
+      s[h][0] = s[h][1] = 0.f;
+      const uint4 a0 = ptx::ld_shared_v4(stage + 1024 * h), a1 = ptx::ld_shared_v4(stage + 1024 * h + 512);
       mma_16816(s[h], q[0], q[1], a0.x, a0.y);
       mma_16816(s[h], q[2], q[3], a0.z, a0.w);
       mma_16816(s[h], q[4], q[5], a1.x, a1.y);
       mma_16816(s[h], q[6], q[7], a1.z, a1.w);
     }
-    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
     float y[4] = {s[0][0] * a.c.scale_log2, s[0][1] * a.c.scale_log2, s[1][0] * a.c.scale_log2,
                   s[1][1] * a.c.scale_log2};
-    if ((have & 0xffffu) != 0xffffu) {
+    if (count < kSlots) {       // slots past the end
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (!((have >> ((i >> 1) * 8 + 2 * x + (i & 1))) & 1u)) y[i] = -INFINITY;
+        if ((i >> 1) * 8 + 2 * x + (i & 1) >= count) y[i] = -INFINITY;
     }
     if (logits && r < G) {
       float* p = logits + (size_t)r * a.c.cap + t * kSlots + 2 * x;   // cap is a multiple of 16
@@ -205,7 +210,7 @@ template <int G> struct Worker<__nv_bfloat16, G> {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     if (__any_sync(0xffffffffu, mx > m)) {
       const float top = fmaxf(m, mx);
-      const float f = top == -INFINITY ? 1.f : exp2f(m - top);
+      const float f = top == -INFINITY ? 1.f : ptx::ex2(m - top);
       m = top;
       l *= f;
 #pragma unroll
@@ -217,10 +222,15 @@ template <int G> struct Worker<__nv_bfloat16, G> {
     const float sub = m == -INFINITY ? 0.f : m;
     float p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = exp2f(y[i] - sub);
+    for (int i = 0; i < 4; ++i) p[i] = ptx::ex2(y[i] - sub);
     l += (p[0] + p[1]) + (p[2] + p[3]);
     const uint32_t p0 = pack_bf16x2(p[0], p[1]), p1 = pack_bf16x2(p[2], p[3]);
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(d.v);
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 y4 = ptx::ld_shared_v4(stage + 2048 + 512 * i);
+      v[4 * i] = y4.x; v[4 * i + 1] = y4.y; v[4 * i + 2] = y4.z; v[4 * i + 3] = y4.w;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t pick = (i & 1) ? 0x7632u : 0x5410u;   // high or low halves: one dim of a token pair
@@ -243,21 +253,18 @@ template <int G> struct Worker<__nv_bfloat16, G> {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p->o[r][16 * x + 8 * e + i] = o[i][e];
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4*>(&p->o[r][16 * x + 8 * e + i]) =
+            make_float4(o[i][e], o[i + 1][e], o[i + 2][e], o[i + 3][e]);
   }
 };
 
-// ---- float ------------------------------------------------------------------------
+// ---- float: a stage is half a unit ---------------------------------------------------
 // Lane (u, x) = (lane / 16, lane % 16): of every pair of slots, slot u, and the
 // dims 4x .. 4x+3.  The two halves of a warp keep separate softmax states,
 // joined at the end of a piece.
 template <int G> struct Worker<float, G> {
-  // Pairs of slots of a step, half of which is in flight: fewer with many
-  // heads, whose queries and sums take the registers.
-  static constexpr int kPairs = G >= 4 ? 2 : 4, kSteps = 8 / kPairs;
-  struct Data {
-    float4 k[kPairs], v[kPairs];
-  };
+  static constexpr int kStages = 2;
   float4 q[G], o[G];
   float m[G], l[G];
 
@@ -266,62 +273,68 @@ template <int G> struct Worker<float, G> {
     const float4* p = reinterpret_cast<const float4*>((const float*)a.q + ((size_t)b * a.c.Hq + g * G) * kDh);
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      float4 f = __ldg(p + h * 16 + x);
-      q[h] = f;
+      q[h] = __ldg(p + h * 16 + x);
       o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
   }
-  __device__ __forceinline__ void load(const DecodeArgs& a, int g, int rows, int step_of, Data& d) const {
+  __device__ __forceinline__ static void issue(const DecodeArgs& a, int g, int rows, int half, uint32_t stage) {
     const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
     const long step = (long)a.c.Hkv * 16;
     const float4* k = reinterpret_cast<const float4*>(a.c.k_pages) + g * 16 + x;
     const float4* v = reinterpret_cast<const float4*>(a.c.v_pages) + g * 16 + x;
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int row = __shfl_sync(0xffffffffu, rows, 2 * (step_of * kPairs + i) + u);
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-      d.k[i] = row >= 0 ? __ldg(k + (long)row * step) : zero;
-      d.v[i] = row >= 0 ? __ldg(v + (long)row * step) : zero;
+    for (int i = 0; i < 4; ++i) {
+      const int row = __shfl_sync(0xffffffffu, rows, 8 * half + 2 * i + u);
+      ptx::cp_async16(stage + 512 * i, k + max(row, 0) * step, row >= 0 ? 16 : 0);
+      ptx::cp_async16(stage + 2048 + 512 * i, v + max(row, 0) * step, row >= 0 ? 16 : 0);
     }
   }
-  __device__ __forceinline__ void compute(const DecodeArgs& a, int rows, int step_of, const Data& d, int t,
+  __device__ __forceinline__ static float4 chunk(uint32_t at) {
+    const uint4 u = ptx::ld_shared_v4(at);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  __device__ __forceinline__ void compute(const DecodeArgs& a, int count, uint32_t stage, int t, int half,
                                           float* logits) {
     const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
-    const uint32_t have = __ballot_sync(0xffffffffu, rows >= 0);
+    float y[G][4];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      float y[kPairs];
-      float mx = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      const float4 k = chunk(stage + 512 * i);
+      const int slot = 8 * half + 2 * i + u;
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const int slot = 2 * (step_of * kPairs + i) + u;
-        float s = fmaf(q[h].x, d.k[i].x, fmaf(q[h].y, d.k[i].y, fmaf(q[h].z, d.k[i].z, q[h].w * d.k[i].w)));
+      for (int h = 0; h < G; ++h) {
+        float s = fmaf(q[h].x, k.x, fmaf(q[h].y, k.y, fmaf(q[h].z, k.z, q[h].w * k.w)));
 #pragma unroll
         for (int e = 8; e > 0; e >>= 1) s += __shfl_xor_sync(0xffffffffu, s, e);
-        y[i] = (have >> slot) & 1u ? s * a.c.scale_log2 : -INFINITY;
-        if (logits && x == 0) logits[(size_t)h * a.c.cap + t * kSlots + slot] = y[i];
-        mx = fmaxf(mx, y[i]);
+        y[h][i] = slot < count ? s * a.c.scale_log2 : -INFINITY;
+        if (logits && x == 0) logits[(size_t)h * a.c.cap + t * kSlots + slot] = y[h][i];
       }
-      if (mx > m[h]) {
-        const float f = exp2f(m[h] - mx);
-        m[h] = mx;
-        l[h] *= f;
-        o[h].x *= f;
-        o[h].y *= f;
-        o[h].z *= f;
-        o[h].w *= f;
-      }
-      const float sub = m[h] == -INFINITY ? 0.f : m[h];
+    }
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const float p = exp2f(y[i] - sub);
-        l[h] += p;
-        o[h].x = fmaf(p, d.v[i].x, o[h].x);
-        o[h].y = fmaf(p, d.v[i].y, o[h].y);
-        o[h].z = fmaf(p, d.v[i].z, o[h].z);
-        o[h].w = fmaf(p, d.v[i].w, o[h].w);
+    for (int h = 0; h < G; ++h) {
+      const float top = fmaxf(fmaxf(fmaxf(y[h][0], y[h][1]), fmaxf(y[h][2], y[h][3])), m[h]);
+      const float f = m[h] == top ? 1.f : ptx::ex2(m[h] - top);
+      const float sub = top == -INFINITY ? 0.f : top;
+      m[h] = top;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[h][i] = ptx::ex2(y[h][i] - sub);
+      l[h] = fmaf(l[h], f, (y[h][0] + y[h][1]) + (y[h][2] + y[h][3]));
+      o[h].x *= f;
+      o[h].y *= f;
+      o[h].z *= f;
+      o[h].w *= f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = chunk(stage + 2048 + 512 * i);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        o[h].x = fmaf(y[h][i], v.x, o[h].x);
+        o[h].y = fmaf(y[h][i], v.y, o[h].y);
+        o[h].z = fmaf(y[h][i], v.z, o[h].z);
+        o[h].w = fmaf(y[h][i], v.w, o[h].w);
       }
     }
   }
@@ -330,7 +343,7 @@ template <int G> struct Worker<float, G> {
     for (int h = 0; h < G; ++h) {
       const float mo = __shfl_xor_sync(0xffffffffu, m[h], 16);
       const float top = fmaxf(m[h], mo);
-      const float f = m[h] == top ? 1.f : exp2f(m[h] - top);     // also for two empty halves
+      const float f = m[h] == top ? 1.f : ptx::ex2(m[h] - top);     // also for two empty halves
       float* acc[5] = {&l[h], &o[h].x, &o[h].y, &o[h].z, &o[h].w};
 #pragma unroll
       for (int i = 0; i < 5; ++i) {
@@ -354,44 +367,33 @@ template <int G> struct Worker<float, G> {
   }
 };
 
-// Tiles [t0, t1) of one (sequence, key head): rows two tiles ahead, data one.
-template <int G>
-__device__ __forceinline__ void run_tiles(Worker<__nv_bfloat16, G>& k, const DecodeArgs& a, int b, int g,
-                                          const Seen& v, int t0, int t1, float* logits) {
+// Tiles [t0, t1) of one (sequence, key head) through the warp's queue: copies
+// kDepth - 1 stages ahead of their use, the pool rows one tile ahead of that.
+template <typename T, int G>
+__device__ __forceinline__ void run_tiles(Worker<T, G>& k, const DecodeArgs& a, int b, int g, const Seen& v, int t0,
+                                          int t1, float* logits, uint32_t queue) {
+  constexpr int S = Worker<T, G>::kStages;
   const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
+  const int end = t1 * S;
   int rows = tile_rows(a.c, table, v, t0);
   int next = t0 + 1 < t1 ? tile_rows(a.c, table, v, t0 + 1) : -1;
-  typename Worker<__nv_bfloat16, G>::Data d[2];
-  k.load(a, g, rows, d[0]);
-  for (int t = t0; t < t1; t += 2) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (t + i >= t1) break;
-      const int after = t + i + 2 < t1 ? tile_rows(a.c, table, v, t + i + 2) : -1;
-      if (t + i + 1 < t1) k.load(a, g, next, d[i ^ 1]);
-      k.compute(a, rows, d[i], t + i, logits);
-      rows = next;
-      next = after;
+  int in = t0 * S, in_slot = 0, out_slot = 0;      // the next stage to copy; ring slots
+#pragma unroll 1
+  for (int s = t0 * S - (kDepth - 1); s < end; ++s) {
+    if (s >= t0 * S) {
+      ptx::cp_async_wait_one();                    // all but the newest group: stage s is here
+      k.compute(a, v.count - (s / S) * kSlots, queue + out_slot * kStageBytes, s / S, s % S, logits);
+      out_slot = out_slot + 1 == kDepth ? 0 : out_slot + 1;
     }
-  }
-}
-template <int G>
-__device__ __forceinline__ void run_tiles(Worker<float, G>& k, const DecodeArgs& a, int b, int g, const Seen& v,
-                                          int t0, int t1, float* logits) {
-  const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
-  int rows = tile_rows(a.c, table, v, t0);
-  constexpr int kSteps = Worker<float, G>::kSteps;      // even
-  typename Worker<float, G>::Data d[2];
-  k.load(a, g, rows, 0, d[0]);
-  for (int t = t0; t < t1; ++t) {
-    const int next = t + 1 < t1 ? tile_rows(a.c, table, v, t + 1) : -1;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (i + 1 < kSteps) k.load(a, g, rows, i + 1, d[(i + 1) & 1]);
-      else if (t + 1 < t1) k.load(a, g, next, 0, d[(i + 1) & 1]);
-      k.compute(a, rows, i, d[i & 1], t, logits);
+    if (in < end) {
+      Worker<T, G>::issue(a, g, rows, in % S, queue + in_slot * kStageBytes);
+      in_slot = in_slot + 1 == kDepth ? 0 : in_slot + 1;
+      if (++in % S == 0) {
+        rows = next;
+        next = in / S + 1 < t1 ? tile_rows(a.c, table, v, in / S + 1) : -1;
+      }
     }
-    rows = next;
+    ptx::cp_async_commit();                        // a group a turn, empty or not
   }
 }
 
@@ -408,87 +410,108 @@ __device__ __forceinline__ void write_row(const DecodeArgs& a, int b, int h, flo
   }
 }
 
-// Joins the pieces number first .. last of one (sequence, key head), in order,
-// of those that are in use: into `to`, or where to is null into the results.
-// One warp.
+// A CTA's shared memory: per warp its queue and two pieces, the run's first and
+// last (the ones that may not be whole).  The second piece lies over the queue,
+// which is empty when it is written.
+template <int G>
+struct CtaSmem {
+  alignas(128) uint8_t queue[kWarps][kDepth * kStageBytes];
+  Piece<G> first[kWarps];
+  Span spans[2 * kWarps];
+  __device__ __forceinline__ Piece<G>* piece(int i) {
+    return i & 1 ? reinterpret_cast<Piece<G>*>(queue[i >> 1]) : &first[i >> 1];
+  }
+};
+
+// Joins head h of the pieces in `mask` (bit i: piece i), all of one (sequence,
+// key head), in order: into `to`, or where to is null into the results.  One
+// warp; lane i < 16 holds piece i's maximum and sum.
 template <typename T, int G>
-__device__ __forceinline__ void join_pieces(const DecodeArgs& a, int b, int g, const Piece<G>* p, const Span* used,
-                                            int first, int last, Piece<G>* to) {
+__device__ __forceinline__ void join_head(const DecodeArgs& a, CtaSmem<G>* sm, int b, int g, int h, uint32_t mask,
+                                          Piece<G>* to) {
   const int lane = threadIdx.x & 31;
-  for (int h = 0; h < G; ++h) {
-    float top = -INFINITY;
-    for (int i = first; i <= last; ++i)
-      if (used[i].b >= 0) top = fmaxf(top, p[i].m[h]);
-    float l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-    for (int i = first; i <= last; ++i) {
-      if (used[i].b < 0) continue;
-      const float f = p[i].m[h] == top ? 1.f : exp2f(p[i].m[h] - top);
-      const float2 x = *reinterpret_cast<const float2*>(&p[i].o[h][2 * lane]);
-      l = fmaf(p[i].l[h], f, l);
-      o.x = fmaf(x.x, f, o.x);
-      o.y = fmaf(x.y, f, o.y);
+  const bool in = (mask >> lane) & 1u;
+  const float m = in ? sm->piece(lane)->m[h] : -INFINITY;
+  float top = m;
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  top = __shfl_sync(0xffffffffu, top, 0);
+  const float f = m == top ? 1.f : ptx::ex2(m - top);
+  float l = in ? sm->piece(lane)->l[h] * f : 0.f;
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  l = __shfl_sync(0xffffffffu, l, 0);
+  float2 o = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (uint32_t left = mask; left; left &= left - 1) {
+    const int i = __ffs(left) - 1;
+    const float fi = __shfl_sync(0xffffffffu, f, i);
+    const float2 x = *reinterpret_cast<const float2*>(&sm->piece(i)->o[h][2 * lane]);
+    o.x = fmaf(x.x, fi, o.x);
+    o.y = fmaf(x.y, fi, o.y);
+  }
+  if (to) {
+    if (lane == 0) {
+      to->m[h] = top;
+      to->l[h] = l;
     }
-    if (to) {
-      if (lane == 0) {
-        to->m[h] = top;
-        to->l[h] = l;
-      }
-      *reinterpret_cast<float2*>(&to->o[h][2 * lane]) = o;
-    } else {
-      write_row<T>(a, b, g * G + h, top, l, o);
-    }
+    *reinterpret_cast<float2*>(&to->o[h][2 * lane]) = o;
+  } else {
+    write_row<T>(a, b, g * G + h, top, l, o);
   }
 }
 
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArgs a) {
-  __shared__ Piece<G> pieces[2 * kWarps];    // two a warp: its run's first and last are the ones that may not be whole
-  __shared__ Span spans[2 * kWarps];
+  extern __shared__ __align__(128) uint8_t smem[];
+  CtaSmem<G>* sm = reinterpret_cast<CtaSmem<G>*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Cache& c = a.c;
-  if (threadIdx.x < 2 * kWarps) spans[threadIdx.x].b = -1;
+  if (threadIdx.x < 2 * kWarps) sm->spans[threadIdx.x].b = -1;
   // This warp's run of units and where it begins.
   Unit at;
-  long begin, end;
+  int begin, end;
   if (a.split) {
-    const long total = find_unit(c, -1, &at);
-    const long per = run_units(total, gridDim.x);
-    const long first = min(total, blockIdx.x * per), past = min(total, first + per);
-    begin = first + (past - first) * warp / kWarps;
-    end = first + (past - first) * (warp + 1) / kWarps;
+    const int total = find_unit(c, -1, &at);
+    const int per = run_units(total, gridDim.x);
+    const int first = (int)min((unsigned)total, blockIdx.x * (unsigned)per), past = (int)min((unsigned)total, (unsigned)first + per);
+    begin = first + (unsigned)(past - first) * warp / kWarps;
+    end = first + (unsigned)(past - first) * (warp + 1) / kWarps;
     if (begin < end) find_unit(c, begin, &at);
   } else {
     at.b = blockIdx.x / c.Hkv;
     at.g = blockIdx.x % c.Hkv;
     at.tiles = units_of(c, at.b);
-    begin = (long)at.tiles * warp / kWarps;
-    end = (long)at.tiles * (warp + 1) / kWarps;
-    at.t = (int)begin;
+    begin = (int)((long)at.tiles * warp / kWarps);
+    end = (int)((long)at.tiles * (warp + 1) / kWarps);
+    at.t = begin;
     if (at.tiles == 0) {     // nothing cached: zeros, for every head of the group
       if (warp < G) write_row<T>(a, at.b, at.g * G + warp, -INFINITY, 0.f, make_float2(0.f, 0.f));
       return;
     }
   }
   __syncthreads();
+  const uint32_t queue = ptx::smem_u32(sm->queue[warp]) + 16 * lane;
   int used = 0;              // pieces this warp left in shared memory
   Worker<T, G> k;
-  for (long u = begin; u < end;) {
+#pragma unroll 1
+  for (int u = begin; u < end;) {
     const Seen v = seen(c, cached(c, at.b));
-    const int t1 = (int)min((long)at.tiles, at.t + (end - u));
+    const int t1 = min(at.tiles, at.t + (end - u));
     float* logits = a.logits ? a.logits + ((size_t)at.b * c.Hq + at.g * G) * c.cap : nullptr;
     k.begin(a, at.b, at.g);
-    run_tiles(k, a, at.b, at.g, v, at.t, t1, logits);
+    run_tiles(k, a, at.b, at.g, v, at.t, t1, logits, queue);
     k.finish();
     const int slot = 2 * warp + used;
-    k.store(&pieces[slot]);
-    if (lane == 0) spans[slot] = Span{at.b, at.g, at.t, t1};
+    __syncwarp();            // the queue's last stage has been read by every lane
+    k.store(sm->piece(slot));
     __syncwarp();
     if (at.t == 0 && t1 == at.tiles) {       // whole: the slot is free again
-      join_pieces<T, G>(a, at.b, at.g, pieces, spans, slot, slot, nullptr);
+#pragma unroll 1
+      for (int h = 0; h < G; ++h) join_head<T, G>(a, sm, at.b, at.g, h, 1u << slot, nullptr);
       __syncwarp();
-      if (lane == 0) spans[slot].b = -1;
     } else {
+      if (lane == 0) sm->spans[slot] = Span{at.b, at.g, at.t, t1};
       ++used;
     }
     u += t1 - at.t;
@@ -503,22 +526,23 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArg
     }
   }
   __syncthreads();
-  // Pieces of one (sequence, key head) lie behind one another: the warp of the
-  // first one's slot joins them.  What is still not whole goes to the
-  // workspace: slot 1 of the CTA if it begins its (sequence, key head), slot 0
-  // if it continues one.
-  for (int i = 2 * warp; i < 2 * warp + 2; ++i) {
-    const Span me = spans[i];
-    if (me.b < 0) continue;
-    bool mine = true;
-    for (int j = 0; j < i; ++j) mine &= !(spans[j].b == me.b && spans[j].g == me.g);
-    if (!mine) continue;
-    int last = i;
-    for (int j = i + 1; j < 2 * kWarps; ++j)
-      if (spans[j].b == me.b && spans[j].g == me.g) last = j;
-    const bool whole = me.t0 == 0 && spans[last].t1 == units_of(c, me.b);
-    Piece<G>* to = whole ? nullptr : (Piece<G>*)a.part + 2 * (size_t)blockIdx.x + (me.t0 == 0 ? 1 : 0);
-    join_pieces<T, G>(a, me.b, me.g, pieces, spans, i, last, to);
+  // Pieces of one (sequence, key head) lie behind one another.  Every warp looks
+  // at the groups (lane i < 16: piece i) and joins every eighth head of each.
+  // What is still not whole goes to the workspace: slot 1 of the CTA if it
+  // begins its (sequence, key head), slot 0 if it continues one.
+  const Span me = lane < 2 * kWarps ? sm->spans[lane] : Span{-1, 0, 0, 0};
+  const int key = me.b < 0 ? -1 - lane : me.b * c.Hkv + me.g;
+  const uint32_t mask = __match_any_sync(0xffffffffu, key);
+  uint32_t groups = __ballot_sync(0xffffffffu, me.b >= 0 && __ffs(mask) - 1 == lane);
+  for (int n = 0; groups; groups &= groups - 1, n += G) {
+    const int i = __ffs(groups) - 1;
+    const uint32_t of = __shfl_sync(0xffffffffu, mask, i);
+    const int b = __shfl_sync(0xffffffffu, me.b, i), g = __shfl_sync(0xffffffffu, me.g, i);
+    const int t0 = __shfl_sync(0xffffffffu, me.t0, i), t1 = __shfl_sync(0xffffffffu, me.t1, 31 - __clz(of));
+    const bool whole = t0 == 0 && t1 == units_of(c, b);
+    Piece<G>* to = whole ? nullptr : (Piece<G>*)a.part + 2 * (size_t)blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll 1
+    for (int h = (warp - n) & (kWarps - 1); h < G; h += kWarps) join_head<T, G>(a, sm, b, g, h, of, to);
   }
 }
 
@@ -526,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArg
 // groups of 16 threads each add every 16th part, a thread four dims.
 template <typename T, int G>
 __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int ctas) {
-  __shared__ long s_first, s_total;
+  __shared__ int s_first, s_total;
   __shared__ float s_top[8];
   __shared__ float4 s_o[16][16];
   __shared__ float s_l[16];
@@ -535,9 +559,10 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tiles = units_of(c, b);
   if (warp == 0) {
-    long before = 0, total = 0;
+    int before = 0, total = 0;
+#pragma unroll 1
     for (int i = lane; i < c.B; i += 32) {
-      const long n = (long)units_of(c, i) * c.Hkv;
+      const int n = units_of(c, i) * c.Hkv;
       total += n;
       if (i < b) before += n;
     }
@@ -547,15 +572,15 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int
       total += __shfl_xor_sync(0xffffffffu, total, d);
     }
     if (lane == 0) {
-      s_first = before + (long)g * tiles;
+      s_first = before + g * tiles;
       s_total = total;
     }
     if (tiles == 0) write_row<T>(a, b, hq, -INFINITY, 0.f, make_float2(0.f, 0.f));
   }
   if (tiles == 0) return;
   __syncthreads();
-  const long per = run_units(s_total, ctas);
-  const int c0 = (int)(s_first / per), n = (int)((s_first + tiles - 1) / per) - c0 + 1;
+  const int per = run_units(s_total, ctas);
+  const int c0 = s_first / per, n = (s_first + tiles - 1) / per - c0 + 1;
   if (n == 1) return;       // one CTA had all of it and wrote the results
   const Piece<G>* part = (const Piece<G>*)a.part + 2 * (size_t)c0;
   auto piece = [&](int i) { return part + 2 * i + (i == 0 ? 1 : 0); };
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int
 #pragma unroll 4
   for (int i = part_of; i < n; i += 16) {
     const Piece<G>* p = piece(i);
-    const float f = p->m[h] == top ? 1.f : exp2f(p->m[h] - top);
+    const float f = p->m[h] == top ? 1.f : ptx::ex2(p->m[h] - top);
     const float4 y = *reinterpret_cast<const float4*>(&p->o[h][4 * x]);
     l = fmaf(p->l[h], f, l);
     o.x = fmaf(y.x, f, o.x);
@@ -611,7 +636,7 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const
     if (i >= 0)
       for (int h = 0; h < c.Hq; ++h) {
         const size_t at = (size_t)b * c.Hq + h;
-        total += exp2f(__ldg(logits + at * c.cap + i) - __ldg(row_lse2 + at));
+        total += ptx::ex2(__ldg(logits + at * c.cap + i) - __ldg(row_lse2 + at));
       }
     float* dst = weights + (size_t)b * c.cap + j;
     *dst = accumulate ? *dst + total : total;
@@ -622,7 +647,10 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const
 
 // One CTA per (sequence, key head) where a cache of at most 64 units (eight a
 // warp) or a batch of at least 4,096 such pairs leaves nothing to split for.
-bool is_split(int B, int Hkv, int cap) { return cap > 64 * kSlots && (long)B * Hkv < 4096; }
+// Also where the units would not fit 31 bits.
+bool is_split(int B, int Hkv, int cap) {
+  return cap > 64 * kSlots && (long)B * Hkv < 4096 && (long)B * Hkv * (cap / kSlots) < (1L << 31) - 4096;
+}
 
 // CTAs of a split call: two an SM, fewer where the capacity has fewer runs.
 // The workspace has room for the most there can be on any GPU.
@@ -637,14 +665,14 @@ size_t up1k(size_t n) { return (n + 1023) / 1024 * 1024; }
 template <typename T, int G>
 cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
   const Cache& c = a.c;
-  if (!a.split) {
-    cache_attn_kernel<T, G><<<c.B * c.Hkv, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  const int ctas = split_ctas(c.B, c.Hkv, c.cap);
-  cache_attn_kernel<T, G><<<ctas, kThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  constexpr int kSmem = sizeof(CtaSmem<G>);
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
+  const int ctas = a.split ? split_ctas(c.B, c.Hkv, c.cap) : c.B * c.Hkv;
+  cache_attn_kernel<T, G><<<ctas, kThreads, kSmem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.split) return e;
   cache_join_kernel<T, G><<<c.B * c.Hq, 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
