@@ -2,16 +2,16 @@
 //
 // Every visible key and value row is read once and serves the G query heads of
 // its key head; there is no reuse beyond that, so HBM bounds the work and the
-// kernels are built to keep enough reads in flight.  Each lane copies (cp.async)
-// the 16-byte chunks that it will use itself into a queue of its own in shared
-// memory, two 4 KiB stages a warp ahead: no lane waits for another, and the
-// reads in flight (16 warps an SM) take no registers.
+// kernels are built to keep enough reads in flight.  Each warp copies (cp.async)
+// whole rows into a queue of its own in shared memory, 4 KiB a stage, ahead of
+// their use: no warp waits for another, and the reads in flight (16 warps an
+// SM) take no registers.
 //
 // Split and join.  The work is one line of units - (sequence, key head, tile of
 // 16 visible slots), sequences of very different lengths behind one another -
-// cut into equal runs, one per CTA, and each CTA's run into eight, one per
-// warp: every processor reads the same number of rows whatever the lengths
-// are.  A warp keeps the online softmax (maximum, sum, weighted values) of the
+// cut into equal runs, one per CTA: every processor reads the same number of
+// rows whatever the lengths are.  The eight warps of a CTA take every eighth
+// tile, or an eighth of the run each where it holds many short sequences.  A warp keeps the online softmax (maximum, sum, weighted values) of the
 // piece of a (sequence, key head) it is in.  A piece that is whole is written
 // out; the others of a CTA are joined in shared memory, a warp a head, and what is still part
 // of a longer one goes to the workspace (two slots a CTA at most: the run's
@@ -52,6 +52,7 @@ struct DecodeArgs {
   float* row_lse2;   // with weights: log2 of each row's denominator
   float* logits;     // with weights: scaled log2 scores [B * Hq][cap], by visible slot
   void* part;        // Piece [CTAs][2]
+  int2* joins;       // [B * Hkv]: first CTA and number of CTAs that have a part
   int split;         // 0: one CTA per (sequence, key head)
 };
 
@@ -82,37 +83,63 @@ struct Span {
   int b, g, t0, t1;
 };
 
-// All sequences' units (one warp), and with `u` >= 0 where unit u lies.  A
-// split call has fewer than 2^31 (is_split).
-__device__ __noinline__ int find_unit(const Cache& c, int u, Unit* at) {
-  const int lane = threadIdx.x & 31;
-  int base = 0;
+// All sequences' units, and where unit number first(total) lies: found by the
+// whole CTA, kThreads sequences at a time.  A split call has fewer than 2^31
+// units (is_split).
+struct Scan {
+  int warp_sum[kWarps];
+  Unit at;
+  int start;        // first unit of at's (sequence, key head)
+};
+template <typename First>
+__device__ __forceinline__ int find_unit(const Cache& c, Scan* sc, First first) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int total = 0, tiles = 0, own = 0, before = 0;
+  // With more sequences than threads the sum comes first and the place in a
+  // second pass.
+  for (int pass = c.B > kThreads ? 0 : 1; pass < 2; ++pass) {
+    int base = 0, u = pass ? (c.B > kThreads ? first(total) : 0) : -1;
 #pragma unroll 1
-  for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int tiles = b0 + lane < c.B ? units_of(c, b0 + lane) : 0, own = tiles * c.Hkv;
-    int incl = own;
+    for (int b0 = 0; b0 < c.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      tiles = b < c.B ? units_of(c, b) : 0;
+      own = tiles * c.Hkv;
+      int incl = own;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += up;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      __syncthreads();
+      if (lane == 31) sc->warp_sum[warp] = incl;
+      __syncthreads();
+      before = base + incl - own;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const int n = sc->warp_sum[i];
+        if (i < warp) before += n;
+        base += n;
+      }
+      if (c.B <= kThreads) u = first(base);
+      if (u >= before && u < before + own) {
+        Unit at;
+        at.b = b;
+        at.tiles = tiles;
+        at.g = (u - before) / tiles;
+        at.t = (u - before) - at.g * tiles;
+        sc->at = at;
+      }
     }
-    const int first = base + incl - own;
-    const uint32_t hit = __ballot_sync(0xffffffffu, u >= first && u < first + own);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      at->b = b0 + src;
-      at->tiles = __shfl_sync(0xffffffffu, tiles, src);
-      const int in = u - __shfl_sync(0xffffffffu, first, src);
-      at->g = in / at->tiles;
-      at->t = in - at->g * at->tiles;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    total = base;
   }
-  return base;
+  __syncthreads();
+  return total;
 }
 
-// Units of one CTA's run: at least one per warp.
-__device__ __forceinline__ int run_units(int total, int ctas) { return max((int)(((unsigned)total + ctas - 1) / ctas), kWarps); }
+// Units of one CTA's run: at least four a warp.
+__device__ __forceinline__ int run_units(int total, int ctas) {
+  return max((int)(((unsigned)total + ctas - 1) / ctas), 4 * kWarps);
+}
 
 // d += A B for the rows 0-7 of A (8-15 are zero, and so is what they give).
 __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
@@ -124,16 +151,26 @@ __device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a2, ui
   (void)z1;
 }
 
-// Pool rows of the tile's 16 slots, lane i < 16 for slot i; -1 where there is
-// none (past the end, or a page outside the pool: reported and left out).
-__device__ __forceinline__ int tile_rows(const Cache& c, const int32_t* table, const Seen& v, int t) {
+// Pages and pool rows of a tile's 16 slots, lane i < 16 for slot i; -1 where
+// there is none (past the end, or a page outside the pool: reported and left
+// out).  The page is read a turn before the row is formed, so that no branch
+// waits for it.
+__device__ __forceinline__ int tile_pages(const Cache& c, const int32_t* table, const Seen& v, int t) {
   const int i = t * kSlots + (threadIdx.x & 15);
-  return i < v.count ? (int)pool_row(c, table, v.slot(i)) : -1;
+  return i < v.count ? __ldg(table + (v.slot(i) >> c.page_shift)) : 0;
+}
+__device__ __forceinline__ int tile_rows(const Cache& c, const Seen& v, int t, int page) {
+  const int i = t * kSlots + (threadIdx.x & 15);
+  if (i >= v.count) return -1;
+  if ((unsigned)page >= (unsigned)c.num_pages) {
+    set_err(c.err, PACK3D_DEVERR_PAGE);
+    return -1;
+  }
+  return (page << c.page_shift) + (v.slot(i) & (c.page - 1));
 }
 
-// A stage of a warp's queue: eight 16-byte chunks a lane, chunk i of lane l at
-// 512 i + 16 l.
-constexpr int kStageBytes = 8 * 512, kDepth = 3;
+// A stage of a warp's queue: 4 KiB, the keys in its first half.
+constexpr int kStageBytes = 4096, kDepth = 3;
 
 template <typename T, int G> struct Worker;
 
@@ -164,30 +201,32 @@ template <int G> struct Worker<__nv_bfloat16, G> {
   }
   // Copies of one unit whose pool rows are `rows`; a row that is not there gives zeros.
   __device__ __forceinline__ static void issue(const DecodeArgs& a, int g, int rows, int, uint32_t stage) {
-    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    const int lane = threadIdx.x & 31, r = lane >> 2, x = lane & 3;
     const long step = (long)a.c.Hkv * 8;      // 16-byte chunks a pool row
     const uint4* k = reinterpret_cast<const uint4*>(a.c.k_pages) + g * 8;
     const uint4* v = reinterpret_cast<const uint4*>(a.c.v_pages) + g * 8;
+    // Keys: four rows an instruction, chunk c of row i at 128 i + 16 (c ^ 4 (i & 1)).
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = __shfl_sync(0xffffffffu, rows, 8 * h + r);
-      const uint4* p = k + max(row, 0) * step + x;
-      ptx::cp_async16(stage + 1024 * h, p, row >= 0 ? 16 : 0);
-      ptx::cp_async16(stage + 1024 * h + 512, p + 4, row >= 0 ? 16 : 0);
+    for (int i = 0; i < 4; ++i) {
+      const int at = 4 * i + (lane >> 3), row = __shfl_sync(0xffffffffu, rows, at);
+      ptx::cp_async16(stage + 128 * at + 16 * ((lane & 7) ^ ((at & 1) << 2)), k + max(row, 0) * step + (lane & 7),
+                      row >= 0 ? 16 : 0);
     }
+    // Values: the lane's own chunks, chunk i of lane l at 2048 + 512 i + 16 l.
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = __shfl_sync(0xffffffffu, rows, (i >> 1) * 8 + 2 * x + (i & 1));
-      ptx::cp_async16(stage + 2048 + 512 * i, v + max(row, 0) * step + r, row >= 0 ? 16 : 0);
+      ptx::cp_async16(stage + 2048 + 512 * i + 16 * lane, v + max(row, 0) * step + r, row >= 0 ? 16 : 0);
     }
   }
   __device__ __forceinline__ void compute(const DecodeArgs& a, int count, uint32_t stage, int t, int, float* logits) {
-    const int r = (threadIdx.x & 31) >> 2, x = threadIdx.x & 3;
+    const int lane = threadIdx.x & 31, r = lane >> 2, x = lane & 3;
     float s[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       s[h][0] = s[h][1] = 0.f;
-      const uint4 a0 = ptx::ld_shared_v4(stage + 1024 * h), a1 = ptx::ld_shared_v4(stage + 1024 * h + 512);
+      const uint32_t at = stage + 128 * (8 * h + r), flip = (r & 1) << 2;
+      const uint4 a0 = ptx::ld_shared_v4(at + 16 * (x ^ flip)), a1 = ptx::ld_shared_v4(at + 16 * ((x + 4) ^ flip));
       mma_16816(s[h], q[0], q[1], a0.x, a0.y);
       mma_16816(s[h], q[2], q[3], a0.z, a0.w);
       mma_16816(s[h], q[4], q[5], a1.x, a1.y);
@@ -228,7 +267,7 @@ template <int G> struct Worker<__nv_bfloat16, G> {
     uint32_t v[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 y4 = ptx::ld_shared_v4(stage + 2048 + 512 * i);
+      const uint4 y4 = ptx::ld_shared_v4(stage + 2048 + 512 * i + 16 * lane);
       v[4 * i] = y4.x; v[4 * i + 1] = y4.y; v[4 * i + 2] = y4.z; v[4 * i + 3] = y4.w;
     }
 #pragma unroll
@@ -281,6 +320,7 @@ template <int G> struct Worker<float, G> {
   }
   __device__ __forceinline__ static void issue(const DecodeArgs& a, int g, int rows, int half, uint32_t stage) {
     const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
+    stage += 16 * (threadIdx.x & 31);         // chunk i of lane l at 512 i + 16 l
     const long step = (long)a.c.Hkv * 16;
     const float4* k = reinterpret_cast<const float4*>(a.c.k_pages) + g * 16 + x;
     const float4* v = reinterpret_cast<const float4*>(a.c.v_pages) + g * 16 + x;
@@ -298,6 +338,7 @@ template <int G> struct Worker<float, G> {
   __device__ __forceinline__ void compute(const DecodeArgs& a, int count, uint32_t stage, int t, int half,
                                           float* logits) {
     const int u = (threadIdx.x >> 4) & 1, x = threadIdx.x & 15;
+    stage += 16 * (threadIdx.x & 31);
     float y[G][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -367,30 +408,35 @@ template <int G> struct Worker<float, G> {
   }
 };
 
-// Tiles [t0, t1) of one (sequence, key head) through the warp's queue: copies
-// kDepth - 1 stages ahead of their use, the pool rows one tile ahead of that.
+// Tiles t0, t0 + step, .. below t1 of one (sequence, key head) through the warp's
+// queue: copies kDepth - 1 stages ahead of their use, the pages one tile ahead
+// of that.
 template <typename T, int G>
 __device__ __forceinline__ void run_tiles(Worker<T, G>& k, const DecodeArgs& a, int b, int g, const Seen& v, int t0,
-                                          int t1, float* logits, uint32_t queue) {
+                                          int t1, int step, float* logits, uint32_t queue) {
   constexpr int S = Worker<T, G>::kStages;
   const int32_t* table = a.c.table + (size_t)b * a.c.max_pages;
-  const int end = t1 * S;
-  int rows = tile_rows(a.c, table, v, t0);
-  int next = t0 + 1 < t1 ? tile_rows(a.c, table, v, t0 + 1) : -1;
-  int in = t0 * S, in_slot = 0, out_slot = 0;      // the next stage to copy; ring slots
+  const int end = (t1 - t0 + step - 1) / step * S;      // stages
+  int rows = tile_rows(a.c, v, t0, tile_pages(a.c, table, v, t0));
+  int next = tile_pages(a.c, table, v, t0 + step);
+  int in = 0, in_t = t0, t = t0, in_slot = 0, out_slot = 0;   // the next stage to copy; its tile, the tile in use; ring slots
 #pragma unroll 1
-  for (int s = t0 * S - (kDepth - 1); s < end; ++s) {
-    if (s >= t0 * S) {
-      ptx::cp_async_wait_one();                    // all but the newest group: stage s is here
-      k.compute(a, v.count - (s / S) * kSlots, queue + out_slot * kStageBytes, s / S, s % S, logits);
+  for (int s = 1 - kDepth; s < end; ++s) {
+    if (s >= 0) {
+      ptx::cp_async_wait_one();                    // all but the newest group: stage s is here,
+      __syncwarp();                                // every lane's part of it
+      k.compute(a, v.count - t * kSlots, queue + out_slot * kStageBytes, t, s % S, logits);
       out_slot = out_slot + 1 == kDepth ? 0 : out_slot + 1;
+      if ((s + 1) % S == 0) t += step;
     }
     if (in < end) {
+      __syncwarp();                                // the slot's last stage has been read by every lane
       Worker<T, G>::issue(a, g, rows, in % S, queue + in_slot * kStageBytes);
       in_slot = in_slot + 1 == kDepth ? 0 : in_slot + 1;
       if (++in % S == 0) {
-        rows = next;
-        next = in / S + 1 < t1 ? tile_rows(a.c, table, v, in / S + 1) : -1;
+        in_t += step;
+        rows = tile_rows(a.c, v, in_t, next);
+        next = tile_pages(a.c, table, v, in_t + step);
       }
     }
     ptx::cp_async_commit();                        // a group a turn, empty or not
@@ -418,6 +464,7 @@ struct CtaSmem {
   alignas(128) uint8_t queue[kWarps][kDepth * kStageBytes];
   Piece<G> first[kWarps];
   Span spans[2 * kWarps];
+  Scan scan;
   __device__ __forceinline__ Piece<G>* piece(int i) {
     return i & 1 ? reinterpret_cast<Piece<G>*>(queue[i >> 1]) : &first[i >> 1];
   }
@@ -468,62 +515,96 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Cache& c = a.c;
   if (threadIdx.x < 2 * kWarps) sm->spans[threadIdx.x].b = -1;
-  // This warp's run of units and where it begins.
+  // This CTA's run of units: where it begins, and how many.
   Unit at;
-  int begin, end;
+  int first = 0, count, per = 1;
   if (a.split) {
-    const int total = find_unit(c, -1, &at);
-    const int per = run_units(total, gridDim.x);
-    const int first = (int)min((unsigned)total, blockIdx.x * (unsigned)per), past = (int)min((unsigned)total, (unsigned)first + per);
-    begin = first + (unsigned)(past - first) * warp / kWarps;
-    end = first + (unsigned)(past - first) * (warp + 1) / kWarps;
-    if (begin < end) find_unit(c, begin, &at);
+    const int total = find_unit(c, &sm->scan, [&](int total) {
+      per = run_units(total, gridDim.x);
+      return (int)min((unsigned)total, blockIdx.x * (unsigned)per);
+    });
+    first = (int)min((unsigned)total, blockIdx.x * (unsigned)per);
+    count = min(total - first, per);
+    if (count == 0) return;
+    at = sm->scan.at;
   } else {
     at.b = blockIdx.x / c.Hkv;
     at.g = blockIdx.x % c.Hkv;
-    at.tiles = units_of(c, at.b);
-    begin = (int)((long)at.tiles * warp / kWarps);
-    end = (int)((long)at.tiles * (warp + 1) / kWarps);
-    at.t = begin;
-    if (at.tiles == 0) {     // nothing cached: zeros, for every head of the group
+    at.t = 0;
+    count = at.tiles = units_of(c, at.b);
+    if (count == 0) {        // nothing cached: zeros, for every head of the group
       if (warp < G) write_row<T>(a, at.b, at.g * G + warp, -INFINITY, 0.f, make_float2(0.f, 0.f));
       return;
     }
   }
   __syncthreads();
-  const uint32_t queue = ptx::smem_u32(sm->queue[warp]) + 16 * lane;
+  const uint32_t queue = ptx::smem_u32(sm->queue[warp]);
   int used = 0;              // pieces this warp left in shared memory
   Worker<T, G> k;
-#pragma unroll 1
-  for (int u = begin; u < end;) {
-    const Seen v = seen(c, cached(c, at.b));
-    const int t1 = min(at.tiles, at.t + (end - u));
+  // One piece: the tiles t0, t0 + step, .. of [t0, t1) of at's (sequence, key
+  // head), left in the warp's next slot as a part of its tiles [p0, p1).
+  auto piece = [&](int t0, int t1, int step, int p0, int p1) {
     float* logits = a.logits ? a.logits + ((size_t)at.b * c.Hq + at.g * G) * c.cap : nullptr;
     k.begin(a, at.b, at.g);
-    run_tiles(k, a, at.b, at.g, v, at.t, t1, logits, queue);
+    run_tiles(k, a, at.b, at.g, seen(c, cached(c, at.b)), t0, t1, step, logits, queue);
     k.finish();
-    const int slot = 2 * warp + used;
     __syncwarp();            // the queue's last stage has been read by every lane
-    k.store(sm->piece(slot));
+    k.store(sm->piece(2 * warp + used));
+    if (lane == 0) sm->spans[2 * warp + used] = Span{at.b, at.g, p0, p1};
     __syncwarp();
-    if (at.t == 0 && t1 == at.tiles) {       // whole: the slot is free again
-#pragma unroll 1
-      for (int h = 0; h < G; ++h) join_head<T, G>(a, sm, at.b, at.g, h, 1u << slot, nullptr);
-      __syncwarp();
-    } else {
-      if (lane == 0) sm->spans[slot] = Span{at.b, at.g, at.t, t1};
-      ++used;
+  };
+  // To the next (sequence, key head) with units.
+  auto advance = [&]() {
+    at.t = 0;
+    if (++at.g == c.Hkv) {
+      at.g = 0;
+      do at.tiles = units_of(c, ++at.b);
+      while (at.tiles == 0 && at.b + 1 < c.B);
     }
-    u += t1 - at.t;
-    // The next (sequence, key head) with units.
-    if (u < end) {
-      at.t = 0;
-      if (++at.g == c.Hkv) {
-        at.g = 0;
-        do at.tiles = units_of(c, ++at.b);
-        while (at.tiles == 0 && at.b + 1 < c.B);
+  };
+  const int part0 = min(at.tiles - at.t, count);
+  bool few = part0 == count;      // at most two (sequence, key head)s in the run
+  if (!few) {
+    const Unit was = at;
+    advance();
+    few = at.tiles >= count - part0;
+    at = was;
+  }
+  int u = few ? 0 : (int)((unsigned)count * warp / kWarps);
+  const int end = few ? count : (int)((unsigned)count * (warp + 1) / kWarps);
+  // Few: the warps take every eighth tile of each, so that the CTA reads one
+  // stretch of the cache at a time.  Many short ones: a stretch of the run each.
+  if (!few)
+    for (int skip = u; skip > 0;) {
+      const int n = min(skip, at.tiles - at.t);
+      at.t += n;
+      skip -= n;
+      if (at.t == at.tiles) advance();
+    }
+#pragma unroll 1
+  while (u < end) {
+    const int t0 = at.t, t1 = min(at.tiles, t0 + (end - u));
+    if (a.split && t0 == 0 && lane == 0 && (!few || warp == 0)) {
+      // The beginning of a (sequence, key head): which CTAs have parts of it.
+      const int start = first + u, c0 = start / per;
+      a.joins[at.b * c.Hkv + at.g] = make_int2(c0, (start + at.tiles - 1) / per - c0 + 1);
+    }
+    if (few) {
+      if (t0 + warp < t1) piece(t0 + warp, t1, kWarps, t0, t1);
+      ++used;
+    } else {
+      piece(t0, t1, 1, t0, t1);
+      if (t0 == 0 && t1 == at.tiles) {       // whole: the slot is free again
+#pragma unroll 1
+        for (int h = 0; h < G; ++h) join_head<T, G>(a, sm, at.b, at.g, h, 1u << (2 * warp + used), nullptr);
+        __syncwarp();
+        if (lane == 0) sm->spans[2 * warp + used].b = -1;
+      } else {
+        ++used;
       }
     }
+    u += t1 - t0;
+    if (u < end) advance();
   }
   __syncthreads();
   // Pieces of one (sequence, key head) lie behind one another.  Every warp looks
@@ -549,38 +630,19 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArg
 // Joins the CTAs' parts of one (sequence, head) in the order of the cache: 16
 // groups of 16 threads each add every 16th part, a thread four dims.
 template <typename T, int G>
-__global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a, int ctas) {
-  __shared__ int s_first, s_total;
+__global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a) {
   __shared__ float s_top[8];
   __shared__ float4 s_o[16][16];
   __shared__ float s_l[16];
   const Cache& c = a.c;
   const int b = blockIdx.x / c.Hq, hq = blockIdx.x % c.Hq, g = hq / G, h = hq % G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tiles = units_of(c, b);
-  if (warp == 0) {
-    int before = 0, total = 0;
-#pragma unroll 1
-    for (int i = lane; i < c.B; i += 32) {
-      const int n = units_of(c, i) * c.Hkv;
-      total += n;
-      if (i < b) before += n;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, d);
-      total += __shfl_xor_sync(0xffffffffu, total, d);
-    }
-    if (lane == 0) {
-      s_first = before + g * tiles;
-      s_total = total;
-    }
-    if (tiles == 0) write_row<T>(a, b, hq, -INFINITY, 0.f, make_float2(0.f, 0.f));
+  const int2 from = a.joins[b * c.Hkv + g];
+  if (units_of(c, b) == 0) {          // nothing cached: no CTA had it
+    if (warp == 0) write_row<T>(a, b, hq, -INFINITY, 0.f, make_float2(0.f, 0.f));
+    return;
   }
-  if (tiles == 0) return;
-  __syncthreads();
-  const int per = run_units(s_total, ctas);
-  const int c0 = s_first / per, n = (s_first + tiles - 1) / per - c0 + 1;
+  const int c0 = from.x, n = from.y;
   if (n == 1) return;       // one CTA had all of it and wrote the results
   const Piece<G>* part = (const Piece<G>*)a.part + 2 * (size_t)c0;
   auto piece = [&](int i) { return part + 2 * i + (i == 0 ? 1 : 0); };
@@ -652,15 +714,18 @@ bool is_split(int B, int Hkv, int cap) {
   return cap > 64 * kSlots && (long)B * Hkv < 4096 && (long)B * Hkv * (cap / kSlots) < (1L << 31) - 4096;
 }
 
-// CTAs of a split call: two an SM, fewer where the capacity has fewer runs.
-// The workspace has room for the most there can be on any GPU.
-constexpr int kMaxCtas = 512;
+// CTAs of a split call: two turns of two an SM (the SMs do not all get the same
+// share of the memory's bandwidth, so the second turn goes where there is time:
+// @@), fewer where the capacity has fewer runs.  The workspace has room for
+// the most there can be on any GPU.
+constexpr int kMaxCtas = 1024;
 int split_ctas(int B, int Hkv, int cap) {
-  const long runs = ((long)B * Hkv * (cap / kSlots) + kWarps - 1) / kWarps;
-  return (int)min((long)min(2 * sm_count(), kMaxCtas), max(1L, runs));
+  const long runs = ((long)B * Hkv * (cap / kSlots) + 4 * kWarps - 1) / (4 * kWarps);
+  return (int)min((long)min(4 * sm_count(), kMaxCtas), max(1L, runs));
 }
 
 size_t up1k(size_t n) { return (n + 1023) / 1024 * 1024; }
+size_t parts_bytes(int G) { return up1k((size_t)2 * kMaxCtas * (((size_t)G * (2 + kDh) * sizeof(float) + 15) / 16 * 16)); }
 
 template <typename T, int G>
 cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
@@ -673,7 +738,7 @@ cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
   cache_attn_kernel<T, G><<<ctas, kThreads, kSmem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
-  cache_join_kernel<T, G><<<c.B * c.Hq, 256, 0, st>>>(a, ctas);
+  cache_join_kernel<T, G><<<c.B * c.Hq, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -689,10 +754,10 @@ cudaError_t launch_t(DecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// The split's parts, then with weights the rows' denominators and the scores.
+// The split's parts and the table for their join, then with weights the rows' denominators and the scores.
 size_t cache_attn_workspace(int B, int Hq, int Hkv, int cap, bool weights) {
   size_t n = 1024;
-  if (is_split(B, Hkv, cap)) n = up1k((size_t)2 * kMaxCtas * (((size_t)(Hq / Hkv) * (2 + kDh) * sizeof(float) + 15) / 16 * 16));
+  if (is_split(B, Hkv, cap)) n = parts_bytes(Hq / Hkv) + up1k((size_t)B * Hkv * sizeof(int2));
   if (weights) n += up1k((size_t)B * Hq * 4) + (size_t)B * Hq * cap * 4;
   return n;
 }
@@ -706,6 +771,7 @@ cudaError_t launch_cache_attn(const Cache& c, int dtype, const void* q, void* ou
   a.lse = lse;
   a.split = is_split(c.B, c.Hkv, c.cap);
   a.part = workspace;
+  a.joins = (int2*)((char*)workspace + parts_bytes(c.G));
   a.row_lse2 = nullptr;
   a.logits = nullptr;
   if (weights) {
