@@ -1,6 +1,8 @@
-// Causal windowed attention of packed sequences and its gradients, row by row:
-// one warp owns one query row of one head (forward, dq) or one key row of one
-// key head (dk, dv).
+// Dispatch of the causal windowed attention of packed sequences: bf16 to the
+// tensor-core kernels, float to the CUDA-core ones, and bf16 calls without a
+// single key row (or, backwards, query row), which have no tensor a TMA map
+// could describe, row by row: one warp owns one query row of one head or one
+// key row of one key head.
 #include "seq.cuh"
 
 namespace pack3d {
@@ -63,23 +65,19 @@ __global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win 
 }  // namespace
 
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st) {
-  if (dtype == PACK3D_BF16 && w.Tk > 0) return launch_window_attn_tc(w, st);   // Tq > 0: checked by the caller
+  if (dtype != PACK3D_BF16) return launch_window_attn_f32(w, st);
+  if (w.Tk > 0) return launch_window_attn_tc(w, st);
   const dim3 grid((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq);
-  if (dtype == PACK3D_BF16) window_rows_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(w);
-  else window_rows_kernel<float><<<grid, 32 * kWarps, 0, st>>>(w);
+  window_rows_kernel<__nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(w);
   return cudaGetLastError();
 }
 
 cudaError_t launch_window_bwd(const Win& w, int dtype, cudaStream_t st) {
-  if (dtype == PACK3D_BF16 && w.Tq > 0 && w.Tk > 0) return launch_window_bwd_tc(w, st);
+  if (dtype != PACK3D_BF16) return launch_window_bwd_f32(w, st);
+  if (w.Tq > 0 && w.Tk > 0) return launch_window_bwd_tc(w, st);
   const dim3 gq((unsigned)tile_grid(w.Tq, kWarps, w.B), w.Hq), gk((unsigned)tile_grid(w.Tk, kWarps, w.B), w.Hkv);
-  if (dtype == PACK3D_BF16) {
-    window_dq_rows_kernel<__nv_bfloat16><<<gq, 32 * kWarps, 0, st>>>(w);
-    window_dkv_rows_kernel<__nv_bfloat16><<<gk, 32 * kWarps, 0, st>>>(w);
-  } else {
-    window_dq_rows_kernel<float><<<gq, 32 * kWarps, 0, st>>>(w);
-    window_dkv_rows_kernel<float><<<gk, 32 * kWarps, 0, st>>>(w);
-  }
+  window_dq_rows_kernel<__nv_bfloat16><<<gq, 32 * kWarps, 0, st>>>(w);
+  window_dkv_rows_kernel<__nv_bfloat16><<<gk, 32 * kWarps, 0, st>>>(w);
   return cudaGetLastError();
 }
 

@@ -22,14 +22,15 @@
 //
 // The first key tile of a sequence holds its sinks, which every later query
 // sees.  Their gradients from the queries beyond the tile's window are formed
-// by further CTAs of the same kernel, kFarSteps query tiles each, which like
-// the tile itself leave float partial sums of the sink rows; window_sink_kernel
+// by further CTAs of the same kernel, far_steps query tiles each, which like
+// the tile itself leave float partial sums of the sink rows; window_sinks_kernel
 // adds them in a fixed order.  No atomics: the same inputs give the same bits.
 //
 // A gradient row that is not finite may be spoilt by 0 times a NaN or an
 // infinity of a row it does not depend on; it is computed again from its
 // visible pairs alone (dq_row, dkv_row).
 #include "seq_tc.cuh"
+#include "window_sinks.cuh"
 
 namespace pack3d {
 namespace seq {
@@ -383,23 +384,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRowsPerTile, kKeys, false);      // S, dP: N = 128 keys
 constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32_ab(kKeys, kDh, true, true);      // dK, dV: A, B MN-major
 
-// Query tiles a CTA of the sinks' far queries takes: long enough that its
-// partial sums (at most 64 rows x 128 floats) are small beside what it reads.
-constexpr int kFarSteps = 16;
-
-// First query row of a sequence beyond the windows of its first key tile: from
-// there on only the sinks of that tile are seen.  lq where there is none.
-__device__ __forceinline__ int far_begin(const Win& w, int lq, int lk) {
-  if (w.sinks == 0 || w.window == 0) return lq;
-  const long r = (long)min(kKeys, lk) - 1 + w.window - (lk - lq);     // past the last position that sees the last key
-  return (int)min((long)lq, max(0L, r));
-}
-__device__ __forceinline__ int far_chunks(const Win& w, int lq, int lk) {
-  if (lk == 0) return 0;
-  const int per = kFarSteps * (kRowsPerTile >> w.gshift);
-  return (lq - far_begin(w, lq, lk) + per - 1) / per;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Win w,
@@ -430,7 +414,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   if (warp == 0) {
     Tile s;
     Tiles all;
-    const bool found = far ? find_piece(w, x, [&](int lq, int lk) { return far_chunks(w, lq, lk); }, &s, &all)
+    const bool found = far ? find_piece(w, x, [&](int lq, int lk) { return far_pieces<kKeys, kRowsPerTile>(w, lq, lk); }, &s, &all)
                            : find_tile(w, x, kKeys, true, &s, &all);
     if (lane == 0) {
       *tile_slot = s;
@@ -482,8 +466,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const int j0 = far ? 0 : s.t * kKeys, j1 = min(s.lk, j0 + kKeys) - 1;
   int ra, rb;
   if (far) {
-    ra = far_begin(w, s.lq, s.lk) + s.t * kFarSteps * tokens;
-    rb = min(s.lq, ra + kFarSteps * tokens) - 1;
+    ra = far_begin<kKeys>(w, s.lq, s.lk) + s.t * far_steps<kRowsPerTile> * tokens;
+    rb = min(s.lq, ra + far_steps<kRowsPerTile> * tokens) - 1;
   } else {
     ra = max(0, j0 - shift);
     rb = s.lq - 1;
@@ -491,7 +475,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   }
   const int nsteps = rb >= ra ? (rb - ra) / tokens + 1 : 0;
   // Rows below `split_rows` of this tile leave float partial sums.
-  const int split_rows = far || (j0 == 0 && far_chunks(w, s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
+  const int split_rows = far || (j0 == 0 && far_pieces<kKeys, kRowsPerTile>(w, s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
 
   if (warp == kTmaWarp) {
     if (lane == 0 && nsteps > 0) {
@@ -668,9 +652,9 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       // the next ones its far CTAs' (x counts the far CTAs of all sequences).
       int slot = x + s.b + 1;
       if (split_rows > 0 && !far)
-        slot = pieces_before(w, s.b, [&](int lq, int lk) { return far_chunks(w, lq, lk); }) + s.b;
+        slot = pieces_before(w, s.b, [&](int lq, int lk) { return far_pieces<kKeys, kRowsPerTile>(w, lq, lk); }) + s.b;
       if (rl < split_rows) {
-        float4* dst = reinterpret_cast<float4*>(w.part + (((size_t)slot * w.Hkv + g) * w.sinks + rl) * 2 * kDh + col0);
+        float4* dst = reinterpret_cast<float4*>(part_row(w, slot, g, rl) + col0);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
@@ -720,59 +704,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     if (redo[rl]) dkv_row<__nv_bfloat16>(w, s, j0 + rl, g);
 }
 
-// dK and dV of the sink rows of sequences with far queries: the tile's partial
-// sums and the far CTAs', added in order.  One CTA per (sequence, key head),
-// one warp per sink row.
-__global__ void __launch_bounds__(256) window_sink_kernel(const Win w) {
-  const int b = blockIdx.x, g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Tile s;
-  Tiles all;
-  find_tile(w, 0, 1, false, &s, &all);        // checks the offsets
-  if (all.bad) return;
-  s.b = b;
-  s.q0 = __ldg(w.cu_q + b);
-  s.lq = __ldg(w.cu_q + b + 1) - s.q0;
-  s.k0 = __ldg(w.cu_k + b);
-  s.lk = __ldg(w.cu_k + b + 1) - s.k0;
-  s.t = 0;
-  s.n = far_chunks(w, s.lq, s.lk);
-  if (s.n == 0) return;
-  const int before = pieces_before(w, b, [&](int lq, int lk) { return far_chunks(w, lq, lk); });
-  for (int j = warp; j < min(w.sinks, s.lk); j += 8) {
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i <= s.n; ++i) {
-      const float4 y = *reinterpret_cast<const float4*>(
-          w.part + (((size_t)(before + b + i) * w.Hkv + g) * w.sinks + j) * 2 * kDh + 4 * lane);
-      sum.x += y.x;
-      sum.y += y.y;
-      sum.z += y.z;
-      sum.w += y.w;
-    }
-    // Lanes 0-15 hold dK's 64 dims, 16-31 dV's.
-    const size_t at = ((size_t)(s.k0 + j) * w.Hkv + g) * kDh;
-    __nv_bfloat16* base = (__nv_bfloat16*)(lane < 16 ? w.dk : w.dv) + at + 4 * (lane & 15);
-    *reinterpret_cast<uint2*>(base) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-    const float zero = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
-    const bool again = __any_sync(0xffffffffu, !(zero == 0.f));
-    __syncwarp();
-    if (again) dkv_row<__nv_bfloat16>(w, s, j, g);
-  }
-}
-
-// CTAs of the sinks' far queries, whatever the offsets are.
-long far_grid(const Win& w) {
-  if (w.sinks == 0 || w.window == 0) return 0;
-  return w.Tq / ((long)kFarSteps * (kRowsPerTile >> w.gshift)) + w.B;
-}
-
 }  // namespace k_side
 }  // namespace
-
-size_t window_bwd_part_bytes(const Win& w, int dtype) {
-  if (dtype != PACK3D_BF16 || w.sinks == 0 || w.window == 0) return 0;
-  // A slot for every sequence's first tile and one for every far CTA.
-  return (size_t)(k_side::far_grid(w) + w.B) * w.Hkv * w.sinks * 2 * kDh * sizeof(float);
-}
 
 cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   // First, so that a thread that has made no CUDA call yet (autograd's) has the
@@ -793,12 +726,11 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int key_grid = (int)tile_grid(w.Tk, k_side::kKeys, w.B);
-  const dim3 gk((unsigned)(key_grid + k_side::far_grid(w)), w.Hkv);
+  const dim3 gk((unsigned)(key_grid + far_grid<kRowsPerTile>(w)), w.Hkv);
   k_side::window_dkv_tc_kernel<<<gk, k_side::kThreads, k_side::kSmemBytes, st>>>(tq, to, tk128, tv128, w, key_grid);
   e = cudaGetLastError();
-  if (e != cudaSuccess || w.sinks == 0 || w.window == 0) return e;
-  k_side::window_sink_kernel<<<dim3(w.B, w.Hkv), 256, 0, st>>>(w);
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_window_sinks<__nv_bfloat16, k_side::kKeys, kRowsPerTile>(w, st);
 }
 
 }  // namespace seq

@@ -276,6 +276,9 @@ __device__ __forceinline__ void delta_row(const Win& w, size_t at) {
 // The tensor-core kernels (bf16; at least one key row and one query row).
 cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st);
 cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st);
+// The float kernels.
+cudaError_t launch_window_attn_f32(const Win& w, cudaStream_t st);
+cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st);
 // Bytes of Win::part for a call of this size.
 size_t window_bwd_part_bytes(const Win& w, int dtype);
 cudaError_t launch_window_attn(const Win& w, int dtype, cudaStream_t st);
