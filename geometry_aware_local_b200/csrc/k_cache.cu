@@ -48,13 +48,16 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const Cache c, const 
 
 // ---- eviction -----------------------------------------------------------------
 // Select: one CTA per sequence.  The weights become 32-bit keys whose unsigned
-// order is the weights' order; the key of the last slot that stays is found by
-// a radix search from the top byte down (four histograms of 256 bins).  Then
-// every warp counts, over its own run of slots, those that stay for sure and
-// those that equal that key, one scan over the warps turns the counts into
-// places, and a second walk writes the kept slots in order: of the equal ones
-// the first few stay.
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+// order is the weights' order (kept in shared memory as far as they fit); the
+// key of the last slot that stays is found by a radix search from the top
+// digit down (11, 11 and 10 bits: 11 bits of a float's top tell close weights
+// apart, so the bins' counters are not all one, and three histograms are
+// enough).  Then every warp counts, over its own run of slots, those that stay
+// for sure and those that equal that key, one scan over the warps turns the
+// counts into places, and a second walk writes the kept slots in order: of the
+// equal ones the first few stay.
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kBins = 2048;
+constexpr int kSelKeys = 40 * 1024;      // keys held in shared memory, at most
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;                                 // NaN: below every number
@@ -62,12 +65,25 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Sum of x over the lanes before this one, and of all lanes.
+__device__ __forceinline__ int lanes_before(int x, int* total) {
+  int incl = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, d);
+    if ((int)(threadIdx.x & 31) >= d) incl += up;
+  }
+  *total = __shfl_sync(0xffffffffu, incl, 31);
+  return incl - x;
+}
+
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c, const float* __restrict__ weights,
-                                                                   int budget, int recent, int new_cap,
+                                                                   int budget, int recent, int new_cap, int held,
                                                                    int32_t* __restrict__ kept,
                                                                    float* __restrict__ new_weights,
                                                                    int32_t* __restrict__ new_lengths) {
-  __shared__ uint32_t hist[256];
+  extern __shared__ uint32_t keys[];                     // `held` of them
+  __shared__ uint32_t hist[kBins];
   __shared__ int s_need;
   __shared__ uint32_t s_prefix;
   __shared__ int2 warp_count[kSelWarps];
@@ -87,36 +103,50 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
     }
     return;
   }
-  // n > budget >= sinks + recent: the slots [lo, hi) compete for `need` places.
-  const int lo = c.sinks, hi = n - recent;
+  // n > budget >= sinks + recent: the slots [lo, hi) compete for `places`.
+  const int lo = c.sinks, hi = n - recent, places = budget - c.sinks - recent;
+  for (int i = tid; i < min(n, held); i += kSelThreads) keys[i] = weight_key(__ldg(w + i));
+  auto key_of = [&](int i) { return i < held ? keys[i] : weight_key(__ldg(w + i)); };
   if (tid == 0) {
-    s_need = budget - c.sinks - recent;
+    s_need = places;
     s_prefix = 0;
   }
-  __syncthreads();
-  const bool any = s_need > 0;
-  if (any) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+  if (places > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+      hist[tid] = 0;
+      hist[tid + kSelThreads] = 0;
       __syncthreads();
-      const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+      const uint32_t prefix = s_prefix, mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+      const int need = s_need;
       for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t key = weight_key(w[i]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
+        const uint32_t key = key_of(i);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
       }
       __syncthreads();
-      if (tid == 0) {
-        int left = s_need;
-        int d = 255;
-        while (d > 0 && (int)hist[d] < left) left -= hist[d--];
-        s_need = left;                                   // places among the keys with this prefix
-        s_prefix = prefix | ((uint32_t)d << shift);
+      // From the largest digit down: thread t has the digits top, top - 1.
+      const int top = kBins - 1 - 2 * tid, a = hist[top], d = hist[top - 1];
+      int all;
+      int before = lanes_before(a + d, &all);
+      if (lane == 31) warp_count[warp].x = all;
+      __syncthreads();
+      int others;
+      const int mine = lanes_before(warp_count[lane].x, &others);
+      before += __shfl_sync(0xffffffffu, mine, warp);
+      // The digit at which the places run out.
+      if (before < need && before + a + d >= need) {
+        const bool second = before + a < need;
+        s_need = need - before - (second ? a : 0);
+        s_prefix = prefix | ((uint32_t)(second ? top - 1 : top) << shift);
       }
       __syncthreads();
     }
+  } else {
+    __syncthreads();
   }
   const uint32_t last = s_prefix;
-  const int equal_places = any ? s_need : 0;
+  const int equal_places = places > 0 ? s_need : 0;
   // Warp `warp` walks the slots [begin, end), 32 at a time.
   const int per = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int begin = min(n, warp * per), end = min(n, begin + per);
@@ -124,8 +154,8 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
     *sure = *equal = false;
     if (i >= end) return;
     if (i < lo || i >= hi) *sure = true;
-    else if (any) {
-      const uint32_t key = weight_key(w[i]);
+    else if (places > 0) {
+      const uint32_t key = key_of(i);
       *sure = key > last;
       *equal = key == last;
     }
@@ -139,11 +169,9 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
   }
   if (lane == 0) warp_count[warp] = make_int2(sure_n, equal_n);
   __syncthreads();
-  int sure_at = 0, equal_at = 0;
-  for (int i = 0; i < warp; ++i) {
-    sure_at += warp_count[i].x;
-    equal_at += warp_count[i].y;
-  }
+  int total;
+  int sure_at = __shfl_sync(0xffffffffu, lanes_before(warp_count[lane].x, &total), warp);
+  int equal_at = __shfl_sync(0xffffffffu, lanes_before(warp_count[lane].y, &total), warp);
   for (int i0 = begin; i0 < end; i0 += 32) {
     const int i = i0 + lane;
     bool sure, equal;
@@ -154,7 +182,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
     const int at = sure_at + __popc(sb & below) + min(e, equal_places);
     if (sure || (equal && e < equal_places)) {
       kb[at] = i;
-      nw[at] = w[i];
+      nw[at] = __ldg(w + i);
     }
     sure_at += __popc(sb);
     equal_at += __popc(eb);
@@ -199,9 +227,12 @@ cudaError_t launch_cache_append(const Cache& c, const int32_t* cu, long rows, co
 cudaError_t launch_cache_evict(const Cache& c, const float* weights, int budget, int recent,
                                const int32_t* new_table, int new_max_pages, int32_t* kept, float* new_weights,
                                int32_t* new_lengths, cudaStream_t st) {
-  cache_select_kernel<<<c.B, kSelThreads, 0, st>>>(c, weights, budget, recent, new_max_pages * c.page, kept,
-                                                   new_weights, new_lengths);
-  cudaError_t e = cudaGetLastError();
+  const int held = min(c.cap, kSelKeys);
+  cudaError_t e = cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+  if (e != cudaSuccess) return e;
+  cache_select_kernel<<<c.B, kSelThreads, held * 4, st>>>(c, weights, budget, recent, new_max_pages * c.page, held,
+                                                          kept, new_weights, new_lengths);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int chunks = c.Hkv * kDh * c.elem_bytes / 16;
   const long want = ((long)budget * chunks + 255) / 256;
