@@ -36,9 +36,15 @@
 // kernel a quarter slower.  Persistent CTAs that walk the tiles measured 0.320 ms.
 // 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.288 ms, 475 TFLOP/s.
 //
+// Few query tiles before many keys (a piece of a long prompt) would leave most
+// SMs idle: then the CTAs of a cluster (2, 4 or 8) share a tile's key tiles and
+// join their rows' maxima, sums and O through each other's shared memory.
+//
 // A key that a row does not see has P = 0 exactly; where its value row holds a
 // NaN or an infinity, 0 times it is a NaN.  A row whose result is not finite is
 // therefore computed again from its visible keys alone (out_row).
+#include <cooperative_groups.h>
+
 #include "seq_tc.cuh"
 
 namespace pack3d {
@@ -66,10 +72,17 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kDh, true);   // V MN-maj
 // in shared memory, so that it takes no registers in the loop over key tiles.
 struct Plan {
   Tile s;
-  KeyTiles<kBN> kt;
   int r0, r1;       // query rows
 };
 static_assert(sizeof(Plan) <= 64, "plan slot");
+
+// A CTA's share of a tile that a cluster splits, over its K / V ring (which is
+// idle by then): each row's O, maximum and sum.
+struct Share {
+  float o[kBM][kDh + 4];
+  float m[kBM], l[kBM];
+};
+static_assert(sizeof(Share) <= kStages * kStageBytes, "share slot");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -77,6 +90,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// kSplit: the CTAs of a cluster along z share the tile's key tiles.
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2)
 window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Win w) {
@@ -127,7 +142,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   if (!find_tile(w, blockIdx.x, tokens, false, &s, &all)) {
     if (all.bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
-    } else if (w.zero_outside && blockIdx.y == 0) {
+    } else if (w.zero_outside && blockIdx.y == 0 && blockIdx.z == 0) {
       constexpr int kWarps = kThreads / 32;
       const int part = (blockIdx.x - all.total) * kWarps + warp, parts = (gridDim.x - all.total) * kWarps;
       fill_outside(w, w.cu_q, w.Tq, w.out, w.Hq * kDh / 2, 0u, part, parts);
@@ -139,12 +154,15 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const int p0 = position(s, r0), p1 = position(s, r1);
   const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
-  const int T = kt.n, T_load = w.stall ? T - 1 : T;
+  // This CTA's key tiles: [jo, jo + T).
+  const int jo = kSplit ? (int)((long)kt.n * blockIdx.z / gridDim.z) : 0;
+  const int T = kSplit ? (int)((long)kt.n * (blockIdx.z + 1) / gridDim.z) - jo : kt.n;
+  const int T_load = w.stall ? max(T - 1, 0) : T;
   volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + kPlanOff);
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
-    const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
+    const int cols = kt.cols(jo + j), row = s.k0 + kt.begin(jo + j);
     ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
 #pragma unroll 1
     for (int c = 0; c < cols / 32; ++c) ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
@@ -159,7 +177,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     for (int j = 0; j < min(T_load, kStages); ++j) load_tile(j);
     ctl->issued = min(T_load, kStages);
   }
-  if (threadIdx.x == 0) *const_cast<Plan*>(plan) = Plan{s, kt, r0, r1};
+  if (threadIdx.x == 0) *const_cast<Plan*>(plan) = Plan{s, r0, r1};
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
     ptx::tmem_relinquish();
@@ -188,7 +206,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       const uint32_t tO = tmem + kColO;
       auto issue_s = [&](int j) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
-        const uint32_t idesc = ptx::idesc_bf16_f32(kBM, kt.cols(j), false);
+        const uint32_t idesc = ptx::idesc_bf16_f32(kBM, kt.cols(jo + j), false);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
           ptx::mma_ss(tmem + (j & 1) * kBN, ptx::smem_desc_sw128(sbase + kk * 32, 16, 1024),
@@ -197,7 +215,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       };
       auto issue_pv = [&](int j) {
         const uint32_t vaddr = sbase + kStageOff + (j % kStages) * kStageBytes + kTileBytes;
-        const int cols = kt.cols(j);
+        const int cols = kt.cols(jo + j);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           if (kk * 16 < cols)
@@ -244,7 +262,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     };
 #pragma unroll 1
     for (int j = 0; j < T; ++j) {
-      const int k0 = kt.begin(j), cols = kt.cols(j);
+      const int k0 = kt.begin(jo + j), cols = kt.cols(jo + j);
       if (!(ok = __all_sync(0xffffffffu, wait(s_full(j & 1), (j >> 1) & 1)))) break;
       ptx::tc_fence_after();
       const uint32_t tS = trow + (j & 1) * kBN;
@@ -334,30 +352,39 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 #pragma unroll
         for (int e = 0; e < kDh; ++e) o[e] = 0u;
       }
-      // l == 0: the row sees no key (its O is 0, or a NaN from a hidden value).
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      float sum = 0.f;                                 // not finite where any element is not
+      if constexpr (kSplit) {
+        Share* mine = reinterpret_cast<Share*>(smem + kStageOff);
 #pragma unroll
-      for (int e = 0; e < kDh; ++e) {
-        const float x = __uint_as_float(o[e]) * inv;
-        sum = fmaf(x, 0.f, sum);
-        o[e] = __float_as_uint(x);
-      }
-      const bool again = valid && !(sum == 0.f);
-      if (valid) {
-        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.out + orow * kDh);
+        for (int e = 0; e < kDh; e += 4)
+          *reinterpret_cast<uint4*>(&mine->o[row][e]) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        mine->m[row] = m_used;
+        mine->l[row] = l;
+      } else {
+        // l == 0: the row sees no key (its O is 0, or a NaN from a hidden value).
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float sum = 0.f;                                 // not finite where any element is not
 #pragma unroll
-        for (int q = 0; q < kDh / 8; ++q) {
-          const float* x = reinterpret_cast<const float*>(o + 8 * q);
-          dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                              pack_bf16x2(x[6], x[7]));
+        for (int e = 0; e < kDh; ++e) {
+          const float x = __uint_as_float(o[e]) * inv;
+          sum = fmaf(x, 0.f, sum);
+          o[e] = __float_as_uint(x);
         }
-        if (w.lse) w.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718f;
-      }
-      __syncwarp();
-      for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
-        const int rr = lane_base + __ffs(todo) - 1;
-        out_row<__nv_bfloat16>(w, at, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+        const bool again = valid && !(sum == 0.f);
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.out + orow * kDh);
+#pragma unroll
+          for (int q = 0; q < kDh / 8; ++q) {
+            const float* x = reinterpret_cast<const float*>(o + 8 * q);
+            dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                pack_bf16x2(x[6], x[7]));
+          }
+          if (w.lse) w.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718f;
+        }
+        __syncwarp();
+        for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
+          const int rr = lane_base + __ffs(todo) - 1;
+          out_row<__nv_bfloat16>(w, at, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+        }
       }
     }
   }
@@ -385,22 +412,90 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
   if (threadIdx.x == 0 && ctl->abort) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+  if constexpr (kSplit) {
+    // Every CTA of the cluster comes here, whatever its waits did.  CTA z joins
+    // the rows z * 128 / S .., a warp a row, the shares in the keys' order.
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    Share* mine = reinterpret_cast<Share*>(smem + kStageOff);
+    const Tile at = *const_cast<const Tile*>(&plan->s);
+    const int S = gridDim.z, rows = kBM / S, r0 = plan->r0, r1 = plan->r1;
+#pragma unroll 1
+    for (int row = blockIdx.z * rows + warp; row < (int)(blockIdx.z + 1) * rows; row += kThreads / 32) {
+      const int r = r0 + (row >> w.gshift), h = (g << w.gshift) + (row & (w.G - 1));
+      if (r > r1) continue;
+      const Share* other = cluster.map_shared_rank(mine, min(lane, S - 1));
+      const float m = lane < S ? other->m[row] : -INFINITY;
+      float top = m;
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = __shfl_sync(0xffffffffu, top, 0);
+      const float f = m == top ? 1.f : ptx::ex2(m - top);
+      const float part = lane < S ? other->l[row] * f : 0.f;
+      float l = 0.f;
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int z = 0; z < S; ++z) {
+        const float fz = __shfl_sync(0xffffffffu, f, z);
+        l += __shfl_sync(0xffffffffu, part, z);
+        const float2 x = *reinterpret_cast<const float2*>(&cluster.map_shared_rank(mine, z)->o[row][2 * lane]);
+        o.x = fmaf(x.x, fz, o.x);
+        o.y = fmaf(x.y, fz, o.y);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      o.x *= inv;
+      o.y *= inv;
+      const size_t orow = (size_t)(at.q0 + r) * w.Hq + h;
+      store2((__nv_bfloat16*)w.out + orow * kDh, o);
+      if (w.lse && lane == 0) w.lse[orow] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718f;
+      const bool again = __any_sync(0xffffffffu, !(fmaf(o.x, 0.f, o.y * 0.f) == 0.f));
+      if (again) out_row<__nv_bfloat16>(w, at, r, h);
+    }
+    cluster.sync();           // no CTA ends while another reads its share
+  }
 }
 
 }  // namespace
+
+// CTAs of a cluster per query tile: as many as keep two CTAs an SM busy and
+// leave each at least four key tiles (2,048 queries before 16,384 keys, 8 heads
+// to one key head: 0.238 ms with 1, 0.131 with 2).
+int split_of(const Win& w, long tiles) {
+  const long keys = w.window > 0 ? min((long)w.Tk, (long)w.window + 2 * kBN) : w.Tk;
+  int S = 1;
+  while (S < 8 && tiles * w.Hkv * S * 2 <= 2L * sm_count() && keys / kBN >= 8L * S) S *= 2;
+  return S;
+}
 
 cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st) {
   // First, so that a thread that has made no CUDA call yet (autograd's) has the
   // device's context when the tensor maps are encoded.
   cudaError_t e =
-      cudaFuncSetAttribute(window_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      cudaFuncSetAttribute(window_attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
   if (!map_query_rows(&tq, w, w.q) || !map_key_rows(&tk, w, w.k, 32) || !map_key_rows(&tv, w, w.v, 32))
     return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)tile_grid(w.Tq, kBM >> w.gshift, w.B), w.Hkv);
-  window_attn_tc_kernel<<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, w);
-  return cudaGetLastError();
+  const long tiles = tile_grid(w.Tq, kBM >> w.gshift, w.B);
+  const int S = split_of(w, tiles - 1);
+  if (S == 1) {
+    window_attn_tc_kernel<false><<<dim3((unsigned)tiles, w.Hkv), kThreads, kSmemBytes, st>>>(tq, tk, tv, w);
+    return cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(window_attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = cluster.val.clusterDim.y = 1;
+  cluster.val.clusterDim.z = S;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)tiles, w.Hkv, S);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_attn_tc_kernel<true>, tq, tk, tv, w);
 }
 
 }  // namespace seq
