@@ -251,25 +251,20 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
       ptx::tc_fence_after();
       const int k0 = kt.begin(j), cols = kt.cols(j);
-      uint32_t sv[64], dv[64];
-      if (cols == 64) {
-        ptx::tmem_ld64_sync(trow + kColS, sv);
-        ptx::tmem_ld64_sync(trow + kColDP, dv);
-      } else {
-        ptx::tmem_ld32_sync(trow + kColS, sv);
-        ptx::tmem_ld32_sync(trow + kColDP, dv);
-      }
-      warp_arrive(s_free);
+      // 32 columns of S and dP at a time: the next step's go to tensor memory
+      // once the last are read.
       uint32_t pk[32];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (32 * q >= cols) break;
+        uint32_t sv[32], dv[32];
+        ptx::tmem_ld32x2_sync(trow + kColS + 32 * q, trow + kColDP + 32 * q, sv, dv);
+        if (32 * q + 32 >= cols) warp_arrive(s_free);
         const int c0 = k0 + 32 * q;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int e = 32 * q + 2 * k;
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2);
-          const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd2);
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), c2, nl2);
+          const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])), nd2);
           const float2 ds = __fmul2_rn(make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), t);
           pk[16 * q + k] = pack_bf16x2(ds.x, ds.y);
         }

@@ -240,7 +240,9 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
 
 def window_attention(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, err=None):
     """pack3d_window_attn as a differentiable PyTorch op: returns out, with gradients of q, k and v by
-    pack3d_window_attn_bwd.  Neither direction synchronises; both can be captured into a CUDA graph."""
+    pack3d_window_attn_bwd.  Neither direction synchronises; both can be captured into a CUDA graph, as long as no
+    eager autograd graph of the same leaves is alive then (PyTorch's gradient accumulation would wait for that
+    graph's stream, which ends the capture with an error; detached copies of the leaves have none)."""
     return _autograd().apply(cfg, q, k, v, cu_q, cu_q if cu_k is None else cu_k, err)
 
 

@@ -316,6 +316,34 @@ def test_decode_is_window_attention_of_one_query(p3, cuda_device):
         ref.close(l, r["lse"], r["lse_tol"], "lse")
 
 
+def test_pool_beyond_32_bit_offsets(p3, cuda_device):
+    """Pages whose elements and bytes lie beyond 2^31 and 2^32: written, read and moved there.  (Keys and values in
+    one pool of 10.5 GB: append writes equal rows to both.)"""
+    dev = cuda_device
+    page, Hkv, pages, n = 256, 8, 40000, 700
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("less than 16 GB free")
+    pool = torch.empty(pages, page, Hkv, 64, dtype=torch.bfloat16, device=dev)
+    table = torch.tensor([[39999, 33000, 17]], dtype=torch.int32, device=dev)
+    new_table = torch.tensor([[39001, 39000]], dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(5)
+    k = torch.randn(n, Hkv, 64, generator=g, device=dev).bfloat16()
+    q = torch.randn(1, Hkv, 64, generator=g, device=dev).bfloat16()
+    cfg = p3.make_seq_config(Hq=Hkv, Hkv=Hkv, page=page)
+    zero, used = (torch.tensor([x], dtype=torch.int32, device=dev) for x in (0, n))
+    p3.cache_append(cfg, k, k, pool, pool, table, zero, offsets([n], dev))
+    assert torch.equal(pool[table[0].long()].view(-1, Hkv, 64)[:n], k)
+    weights = torch.zeros(1, 3 * page, device=dev)
+    out, lse = p3.cache_attn(cfg, q, pool, pool, table, used, weights=weights)
+    r = ref.window(q, k, k, [1], [n], 0, 0, cfg.softmax_scale)
+    ref.close(out, r["out"], r["out_tol"], "out")
+    ref.close(lse, r["lse"], r["lse_tol"], "lse")
+    kept, _, lengths = p3.cache_evict(cfg, pool, pool, table, used, weights, new_table, 300, 10)
+    want = ref.evict(used, weights.cpu(), 300, 0, 10)[0]
+    assert kept[0].tolist() == want and int(lengths) == 300
+    assert torch.equal(pool[new_table[0].long()].view(-1, Hkv, 64)[:300], k[torch.tensor(want, device=dev)])
+
+
 def test_decode_reports_bad_pages_and_lengths(p3, cuda_device):
     """A page outside the pool or a length outside the capacity: reported, and no address outside the pool is read
     (the kernel checks every page number before it is used)."""
