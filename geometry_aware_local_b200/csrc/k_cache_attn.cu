@@ -756,7 +756,7 @@ cudaError_t launch_t(DecodeArgs& a, cudaStream_t st) {
 
 // The split's parts and the table for their join, then with weights the rows' denominators and the scores.
 size_t cache_attn_workspace(int B, int Hq, int Hkv, int cap, bool weights) {
-  size_t n = 1024;
+  size_t n = 0;
   if (is_split(B, Hkv, cap)) n = parts_bytes(Hq / Hkv) + up1k((size_t)B * Hkv * sizeof(int2));
   if (weights) n += up1k((size_t)B * Hq * 4) + (size_t)B * Hq * cap * 4;
   return n;

@@ -229,9 +229,8 @@ pack3d_status pack3d_cache_attn(const pack3d_seq_config* cfg, int32_t batch, con
   if (batch == 0) return PACK3D_OK;
   if (!q || !lengths || !out) return PACK3D_ERR_INVALID_ARG;
   if (max_pages > 0 && (!k_pages || !v_pages || !table)) return PACK3D_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < pack3d_cache_attn_workspace_bytes(cfg, batch, max_pages, weights != nullptr))
-    return PACK3D_ERR_WORKSPACE;
+  const size_t need = seq::cache_attn_workspace(batch, cfg->Hq, cfg->Hkv, max_pages * cfg->page, weights != nullptr);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return PACK3D_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(lse, 4) ||
       !aligned(weights, 4) || !aligned(lengths, 4) || !aligned(table, 4))
     return PACK3D_ERR_ALIGNMENT;

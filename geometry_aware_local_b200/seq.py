@@ -102,7 +102,7 @@ def _refuse(what, cfg, name, t, dtype, shape, device):
 
 def _require(what, cfg, name, t, dtype, shape, device):
     """Refuses, before anything runs, a tensor that is not what the kernels will take it for."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         _refuse(what, cfg, name, t, dtype, shape, device)
 
 
@@ -162,6 +162,8 @@ def _window_args(what, cfg, q, k, v, cu_q, cu_k):
         raise ValueError(f"{what}: q and k are [rows, heads, {DH}], cu_q is [batch + 1]")
     T, dev = types.get(cfg.dtype), q.device
     keys = (k.shape[0], cfg.Hkv, DH)
+    if not q.is_cuda:
+        _refuse(what, cfg, "q", q, T, (q.shape[0], cfg.Hq, DH), dev)
     _require(what, cfg, "q", q, T, (q.shape[0], cfg.Hq, DH), dev)
     _require(what, cfg, "k", k, T, keys, dev)
     _require(what, cfg, "v", v, T, keys, dev)
@@ -187,7 +189,7 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
     new = out is None
     if new:
         out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
             return out.zero_(), lse.fill_(-math.inf)
     else:
@@ -284,6 +286,8 @@ def _cache_args(what, cfg, k_pages, v_pages, table, lengths):
         raise ValueError(f"{what}: the pages are [num_pages, page, Hkv, {DH}], the table is [batch, max_pages]")
     T, dev = types.get(cfg.dtype), k_pages.device
     shape = (k_pages.shape[0], cfg.page, cfg.Hkv, DH)
+    if not k_pages.is_cuda:
+        _refuse(what, cfg, "k_pages", k_pages, T, shape, dev)
     _require(what, cfg, "k_pages", k_pages, T, shape, dev)
     _require(what, cfg, "v_pages", v_pages, T, shape, dev)
     _require(what, cfg, "table", table, torch.int32, table.shape, dev)
@@ -321,27 +325,30 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     batch, max_pages = table.shape
     _require(what, cfg, "q", q, T, (batch, cfg.Hq, DH), dev)
     if stream is not None:
-        _owned(what, out, lse, workspace)
+        _owned(what, out, lse)
+        if workspace is None and cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None):
+            _owned(what, workspace)
     if out is None:
         out = torch.empty_like(q)
     else:
         _require(what, cfg, "out", out, T, tuple(q.shape), dev)
     if lse is None:
-        lse = torch.empty((batch, cfg.Hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((batch, cfg.Hq), dtype=torch.float32)
     else:
         _require(what, cfg, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
     if weights is not None:
         _require(what, cfg, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
     if workspace is None:
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
         _check_workspace(what, workspace, dev)
+        n = workspace.numel() * workspace.element_size()
     _check_err_word(what, err, dev, torch)
     _call(torch, what, lib.pack3d_cache_attn, dev, stream, ctypes.byref(cfg), batch, q.data_ptr(),
           k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), max_pages, k_pages.shape[0], lengths.data_ptr(),
-          out.data_ptr(), lse.data_ptr(), _p(weights), int(bool(accumulate)), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _p(err))
+          out.data_ptr(), lse.data_ptr(), _p(weights), int(bool(accumulate)), _p(workspace), n, _p(err))
     return out, lse
 
 

@@ -116,7 +116,9 @@ pack3d_status pack3d_cache_append(const pack3d_seq_config *cfg, int32_t batch, i
                                   int32_t *err_word, void *stream);
 
 /* Bytes of device workspace pack3d_cache_attn needs; with_weights != 0 where
- * the call gets a weights buffer (0 on an invalid config or count). */
+ * the call gets a weights buffer.  0 where it needs none (a short capacity
+ * without weights; workspace may then be NULL), and on an invalid config or
+ * count. */
 size_t pack3d_cache_attn_workspace_bytes(const pack3d_seq_config *cfg, int32_t batch, int32_t max_pages,
                                          int32_t with_weights);
 
