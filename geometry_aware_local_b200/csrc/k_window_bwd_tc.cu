@@ -13,12 +13,16 @@
 //   leaves it for the second kernel.
 //
 // window_dkv_tc_kernel: one 128-key tile of one key head per CTA and the
-//   queries whose window reaches it, 128 rows a step, one CTA per SM.  S and dP
-//   (M = 128 rows, N = 128 keys) go to tensor memory; four softmax warpgroups
-//   (one per 32-key chunk) write dS and P as bf16 into shared memory,
-//   MN-major; a second MMA warp accumulates dK += dS^T Q and dV += P^T dout
-//   (M = 128 keys, N = 64, K = 128 rows) in tensor memory.  Chunks that no row
-//   of the step sees are written as zeros without an exponential.
+//   queries whose window reaches it, 128 rows a step, one CTA per SM.  S^T and
+//   dP^T (M = 128 keys, N = 128 rows) go to tensor memory; four softmax
+//   warpgroups (thread = key, one 32-row chunk of the step each) write dS^T and
+//   P^T beside them as packed bf16, from where a second MMA warp accumulates
+//   dK += dS^T Q and dV += P^T dout (M = 128 keys, N = 64, K = 128 rows).
+//   Where no key of a warp is seen by any row of its chunk it writes zeros
+//   without an exponential.  The transposed products cost a broadcast load of
+//   each row's lse and D; with S and dP by rows, dS and P had to go through
+//   64 KiB of shared memory, whose reads held up the tensor cores (65,536
+//   tokens, window 1024 / 4096: 0.874 / 2.51 ms, now 0.825 / 2.29 ms).
 //
 // The first key tile of a sequence holds its sinks, which every later query
 // sees.  Their gradients from the queries beyond the tile's window are formed
@@ -360,15 +364,16 @@ constexpr int kSoftmaxWarps = 16;               // four warpgroups, one 32-key c
 // accumulation, so that S and dP of the next step never queue behind it.
 constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
 constexpr int kMmaWarp = kSoftmaxWarps, kMmaWarp2 = kSoftmaxWarps + 1, kTmaWarp = kSoftmaxWarps + 2;
-constexpr int kColS = 0, kColDP = 128, kColDK = 256, kColDV = 320, kTmemCols = 512;
+// S^T, dP^T (lane = key, column = query row), dK, dV, and P^T, dS^T as packed bf16.
+constexpr int kColS = 0, kColDP = 128, kColDK = 256, kColDV = 320, kColP = 384, kColDS = 448, kTmemCols = 512;
 constexpr int kKeyTileBytes = kKeys * kDh * 2;  // 16 KiB
-// The operand buffer holds dS^T (two 16 KiB halves: keys 0-63, 64-127) and then P^T.
-constexpr int kOpBytes = 4 * kQTileBytes, kPInOp = 2 * kQTileBytes;
 constexpr int kKOff = 0, kVOff = kKeyTileBytes, kStageOff = 2 * kKeyTileBytes;
 constexpr int kStageBytes = 2 * kQTileBytes;    // Q at +0, dout at +kQTileBytes
 constexpr int kStages = 4;
-constexpr int kOpOff = kStageOff + kStages * kStageBytes;
-constexpr int kBarOff = kOpOff + kOpBytes;
+// Each softmax warp's 32 (lse, D) of the step's rows: lse2 negated, then -D.
+constexpr int kRowOff = kStageOff + kStages * kStageBytes;
+constexpr int kRowBytes = 64 * 4;
+constexpr int kBarOff = kRowOff + kSoftmaxWarps * kRowBytes;
 // barriers: full[S], empty[S], kvfull, o_final, s_full, s_free, p_full, p_free, drain[2]
 constexpr int kNumBars = 2 * kStages + 8;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
@@ -376,8 +381,8 @@ constexpr int kTileOff = kCtlOff + 32;
 constexpr int kRedoOff = kTileOff + 64;         // one byte per key row
 constexpr int kSmemBytes = kRedoOff + kKeys + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRowsPerTile, kKeys, false);      // S, dP: N = 128 keys
-constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32_ab(kKeys, kDh, true, true);      // dK, dV: A, B MN-major
+constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kKeys, kRowsPerTile, false);      // S^T, dP^T: N = 128 rows
+constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32(kKeys, kDh, true);               // dK, dV: B MN-major
 
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
@@ -505,26 +510,25 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         const uint32_t oaddr = qaddr + kQTileBytes;
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tS, ptx::smem_desc_sw128(qaddr + kk * 32, 16, 1024),
-                      ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024), kIdescS, kk > 0);
+          ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(qaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tDP, ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024),
-                      ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024), kIdescS, kk > 0);
+          ptx::mma_ss(tDP, ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
         ptx::tc_commit(s_full);
       };
       auto issue_dkv = [&](int t) {
         const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
         const uint32_t oaddr = qaddr + kQTileBytes;
-        const uint32_t op = sbase + kOpOff;
 #pragma unroll
         for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-          ptx::mma_ss(tDK, ptx::smem_desc_sw128(op + kk * 2048, 2 * 8192, 1024),
-                      ptx::smem_desc_sw128(qaddr + kk * 2048, 8192, 1024), kIdescKV, (t > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_ts(tDK, tmem + kColDS + kk * 8, ptx::smem_desc_sw128(qaddr + kk * 2048, 8192, 1024), kIdescKV,
+                      (t > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-          ptx::mma_ss(tDV, ptx::smem_desc_sw128(op + kPInOp + kk * 2048, 2 * 8192, 1024),
-                      ptx::smem_desc_sw128(oaddr + kk * 2048, 8192, 1024), kIdescKV, (t > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_ts(tDV, tmem + kColP + kk * 8, ptx::smem_desc_sw128(oaddr + kk * 2048, 8192, 1024), kIdescKV,
+                      (t > 0 || kk > 0) ? 1u : 0u);
         ptx::tc_commit(p_free);
         ptx::tc_commit(empty(t % kStages));
         if (t == nsteps - 1) ptx::tc_commit(o_final);
@@ -550,51 +554,72 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     }
     __syncwarp();
   } else {
-    // ---------------- softmax warps: thread = query row of the step ----------------
-    const int c = warp >> 2;                     // 32-key chunk of the tile
+    // ---------------- softmax warps: thread = key of the tile ----------------
+    const int c = warp >> 2;                     // 32-row chunk of the step
     const int lane_base = (warp & 3) * 32;
-    const int rl = lane_base + lane;             // row inside the step's tile
+    const int rl = lane_base + lane;             // key inside the tile
     const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
     const float2 c2 = make_float2(w.scale_log2, w.scale_log2);
-    const int h = (g << w.gshift) + (rl & (w.G - 1));
-    const int c0 = j0 + 32 * c;                  // the chunk's first key
+    // The rows ka .. kb - 1 of the sequence see this thread's key.
+    const int j = j0 + rl;
+    const int ka = far && j >= w.sinks ? rb + 1 : max(ra, j - shift);
+    const int kb = w.window > 0 && j >= w.sinks ? min(rb, j + w.window - 1 - shift) + 1 : rb + 1;
+    // Row 32 c + lane of a step: -lse in base 2 and -D, or zeros where no key sees it.
+    const int h = (g << w.gshift) + (lane & (w.G - 1));
+    float* rows = reinterpret_cast<float*>(smem + kRowOff + warp * kRowBytes);
+    auto load_row = [&](int t, float& nl, float& nd) {
+      const int r = ra + t * tokens + ((32 * c + lane) >> w.gshift);
+      nl = nd = 0.f;
+      if (r <= rb && r + shift >= 0) {
+        const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
+        nl = -__ldg(w.lse + orow) * kLog2e;
+        nd = -__ldg(w.delta + orow);
+      }
+    };
+    float nl, nd;
+    load_row(0, nl, nd);
     bool ok = true;
 #pragma unroll 1
     for (int t = 0; t < nsteps; ++t) {
-      const int rs = ra + t * tokens;            // the step's first row
-      const int r = rs + (rl >> w.gshift);
-      const bool valid = r <= rb;
-      const int p = valid ? r + shift : -1;
-      float lse2 = 0.f, delta = 0.f;
-      if (valid && p >= 0) {
-        const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
-        lse2 = __ldg(w.lse + orow) * kLog2e;
-        delta = __ldg(w.delta + orow);
-      }
-      const int ps = rs + shift, pe = min(rs + tokens - 1, rb) + shift;   // the step's positions
-      // Whether any row of the step sees a key of the chunk, and whether all rows see all of it.
-      const bool some = c0 <= j1 && c0 <= pe && (c0 + 31 >= window_low(w, max(ps, 0)) || c0 < w.sinks) &&
-                        !(far && c0 >= w.sinks);
-      const bool whole = !far && c0 + 31 <= ps && c0 >= window_low(w, pe) && rs + tokens - 1 <= rb;
+      __syncwarp();
+      rows[lane] = nl;
+      rows[32 + lane] = nd;
+      __syncwarp();
+      load_row(t + 1, nl, nd);
+      // Bit k: row 32 c + k of the step sees the key.
+      const int rs = ra + t * tokens;
+      const int x0 = (min(max(ka - rs, 0), tokens) << w.gshift) - 32 * c;
+      const int x1 = (min(max(kb - rs, 0), tokens) << w.gshift) - 32 * c;
+      const uint32_t see = (x0 >= 32 ? 0u : 0xffffffffu << max(x0, 0)) & (x1 >= 32 ? 0xffffffffu : (1u << max(x1, 0)) - 1u);
+      const bool some = __any_sync(0xffffffffu, see != 0u), whole = __all_sync(0xffffffffu, see == 0xffffffffu);
       if (!(ok = __all_sync(0xffffffffu, wait(s_full, t & 1)))) break;
       ptx::tc_fence_after();
       uint32_t pd[16], pp[16];
       if (some) {
-        uint32_t sv[32], dv[32];
-        ptx::tmem_ld32x2_sync(trow + kColS + 32 * c, trow + kColDP + 32 * c, sv, dv);
-        warp_arrive(s_free);
-        const float2 nl2 = make_float2(-lse2, -lse2), nd2 = make_float2(-delta, -delta);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), c2, nl2);
-          const float2 tt = __fadd2_rn(make_float2(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])), nd2);
-          const float2 pr = make_float2(ptx::ex2(xx.x), ptx::ex2(xx.y));
-          const float2 ds = __fmul2_rn(pr, tt);
-          pd[k] = pack_bf16x2(ds.x, ds.y);
-          pp[k] = pack_bf16x2(pr.x, pr.y);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t sv[16], dv[16];
+          ptx::tmem_ld16x2_sync(trow + kColS + 32 * c + 16 * q, trow + kColDP + 32 * c + 16 * q, sv, dv);
+          if (q == 1) warp_arrive(s_free);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 l4 = reinterpret_cast<const float4*>(rows)[4 * q + k];
+            const float4 d4 = reinterpret_cast<const float4*>(rows + 32)[4 * q + k];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = 4 * k + 2 * e;
+              const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2,
+                                           e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
+              const float2 tt = __fadd2_rn(make_float2(__uint_as_float(dv[i]), __uint_as_float(dv[i + 1])),
+                                           e ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
+              const float2 pr = make_float2(ptx::ex2(xx.x), ptx::ex2(xx.y));
+              const float2 ds = __fmul2_rn(pr, tt);
+              pd[8 * q + 2 * k + e] = pack_bf16x2(ds.x, ds.y);
+              pp[8 * q + 2 * k + e] = pack_bf16x2(pr.x, pr.y);
+            }
+          }
         }
         if (!whole) {
-          const uint32_t see = visible_bits(w, p, window_low(w, p), c0);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint32_t keep = ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
@@ -607,19 +632,12 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
         for (int k = 0; k < 16; ++k) pd[k] = pp[k] = 0u;
       }
-      // The previous step's dK / dV MMAs read the operand buffer: wait for them
-      // only now, so this step's exponentials overlap them.
+      // The previous step's dK / dV MMAs read P^T and dS^T: wait for them only
+      // now, so this step's exponentials overlap them.
       if (t > 0 && !(ok = __all_sync(0xffffffffu, wait(p_free, (t - 1) & 1)))) break;
-      // Row rl of the MN-major operands: keys 32c .. 32c+31 are 16-byte chunks
-      // (c & 1) * 4 + m of half c / 2.
-      const uint32_t op = sbase + kOpOff + (uint32_t)(c >> 1) * kQTileBytes;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t off = ptx::sw128_offset((uint32_t)rl, (uint32_t)(((c & 1) * 4 + m) * 8));
-        ptx::st_shared_v4(op + off, pd[4 * m], pd[4 * m + 1], pd[4 * m + 2], pd[4 * m + 3]);
-        ptx::st_shared_v4(op + kPInOp + off, pp[4 * m], pp[4 * m + 1], pp[4 * m + 2], pp[4 * m + 3]);
-      }
-      ptx::fence_proxy_async_smem();
+      ptx::tmem_st16(trow + kColDS + 16 * c, pd);
+      ptx::tmem_st16(trow + kColP + 16 * c, pp);
+      ptx::tmem_wait_st();
       warp_arrive(p_full);
     }
     if (nsteps == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
