@@ -69,6 +69,15 @@ constexpr int kNumBars = 2 * kStages + 7;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kSmemBytes = kCtlOff + 32 + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+// Row tiles of at most this many key tiles form D from P and dP in a first pass
+// over them.  <dout, out> of the rounded out is off by 2^-9 of its terms, which
+// where a row sees a few dozen keys is as much as all of dS's rounding (dQ and
+// dK off by 1.5 to 1.8 times bf16's own rounding, now 1.4); where it sees more
+// it averages out.  The tiles stay in shared memory for the second pass, so
+// the first costs two products and the exponentials, and saves the reads of out
+// and dout by rows (65,536 tokens, window 65: 0.365 -> 0.349 ms).
+constexpr int kTwice = 3;
+static_assert(kTwice <= kStages, "the first pass's tiles stay");
 constexpr uint32_t kIdescDQ = ptx::idesc_bf16_f32(kRowsPerTile, kDh, true);  // dQ: N = 64 dims, K MN-major
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -131,6 +140,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int p0 = position(s, r0), p1 = position(s, r1);
   const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
   const int T = kt.n, T_load = w.stall ? T - 1 : T;
+  const int first = T <= kTwice ? T : 0;      // steps of the first pass
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
@@ -200,7 +210,14 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ptx::tc_commit(empty(j % kStages));
         if (j == T - 1) ptx::tc_commit(o_final);
       };
-      bool ok = wait(qfull, 0) && wait(full(0), 0);
+      bool ok = wait(qfull, 0);
+#pragma unroll 1
+      for (int j = 0; ok && j < first; ++j) {
+        if (!(ok = wait(full(j), 0) && (j == 0 || wait(s_free, (j - 1) & 1)))) break;
+        ptx::tc_fence_after();
+        issue_sdp(j);
+      }
+      ok = ok && wait(full(0), 0) && (first == 0 || wait(s_free, (first - 1) & 1));
       if (ok) {
         ptx::tc_fence_after();
         issue_sdp(0);
@@ -208,7 +225,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll 1
       for (int j = 0; ok && j < T; ++j) {
         if (j + 1 < T) {
-          if (!(ok = wait(s_free, j & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
+          if (!(ok = wait(s_free, (first + j) & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
           ptx::tc_fence_after();
           issue_sdp(j + 1);
         }
@@ -229,30 +246,49 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const size_t orow = (size_t)(s.q0 + (valid ? r : r0)) * w.Hq + h;
     const int p = valid ? position(s, r) : -1;
     const int low = window_low(w, p), low_last = window_low(w, p1);
-    // D of the row, in float from the bf16 rows; rows past the sequence see
-    // nothing, whatever their lse2 and D are.
-    float delta = 0.f, lse2 = 0.f;
-    if (valid) {
-      const uint4* a = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.out + orow * kDh);
-      const uint4* d = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.dout + orow * kDh);
-      float x[8], y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        chunk_to_float(__ldg(a + i), x, __nv_bfloat16());
-        chunk_to_float(__ldg(d + i), y, __nv_bfloat16());
-#pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
-      }
-      w.delta[orow] = delta;
-      const float lse = w.lse[orow];
-      lse2 = p >= 0 ? lse * kLog2e : 0.f;
-    }
+    // Rows past the sequence see nothing, whatever their lse2 and D are.
+    const float lse2 = valid && p >= 0 ? w.lse[orow] * kLog2e : 0.f;
     const float2 c2 = make_float2(w.scale_log2, w.scale_log2), nl2 = make_float2(-lse2, -lse2);
-    const float2 nd2 = make_float2(-delta, -delta);
+    float delta = 0.f;
     bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < T; ++j) {
+    for (int j = 0; j < first; ++j) {
       if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
+      ptx::tc_fence_after();
+      const int cols = kt.cols(j);
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t sv[16], dv[16];
+        ptx::tmem_ld16x2_sync(trow + kColS + c, trow + kColDP + c, sv, dv);
+        if (c + 16 >= cols) warp_arrive(s_free);
+        const uint32_t see = visible_bits(w, p, low, kt.begin(j) + c);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float pr = ptx::ex2(fmaf(__uint_as_float(sv[k]), w.scale_log2, -lse2));
+          if ((see >> k) & 1u) delta = fmaf(pr, __uint_as_float(dv[k]), delta);
+        }
+      }
+    }
+    if (valid) {
+      if (first == 0) {
+        // D of the row, in float from the bf16 rows.
+        const uint4* a = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.out + orow * kDh);
+        const uint4* d = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.dout + orow * kDh);
+        float x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          chunk_to_float(__ldg(a + i), x, __nv_bfloat16());
+          chunk_to_float(__ldg(d + i), y, __nv_bfloat16());
+#pragma unroll
+          for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+        }
+      }
+      w.delta[orow] = delta;
+    }
+    const float2 nd2 = make_float2(-delta, -delta);
+#pragma unroll 1
+    for (int j = 0; ok && j < T; ++j) {
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full, (first + j) & 1)))) break;
       ptx::tc_fence_after();
       const int k0 = kt.begin(j), cols = kt.cols(j);
       // 32 columns of S and dP at a time: the next step's go to tensor memory

@@ -30,7 +30,7 @@ struct Win {
   void* dq;
   void* dk;
   void* dv;
-  float* delta;                   // workspace [Tq, Hq]: <dout, out>
+  float* delta;                   // workspace [Tq, Hq]: <dout, out>, the row's sum of P dP
   float* part;                    // workspace: partial gradients of the sink rows
   int zero_outside;               // rows of no sequence become 0 instead of staying as they were
   int32_t* err;
