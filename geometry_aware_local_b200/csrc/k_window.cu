@@ -14,29 +14,27 @@ constexpr int kWarps = 8;
 // What a CTA without a tile does: it reports wrong offsets, or fills the rows
 // that belong to no sequence.
 template <typename T>
-__device__ __forceinline__ void no_query_tile(const Win& w, const Tiles& all, void* rows, float* lse) {
-  if (all.bad) {
+__device__ __forceinline__ void no_query_tile(const Win& w, bool bad, void* rows, float* lse) {
+  if (bad) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
   } else if (w.zero_outside && blockIdx.y == 0) {
-    const int part = (blockIdx.x - all.total) * kWarps + (threadIdx.x >> 5), parts = (gridDim.x - all.total) * kWarps;
-    fill_outside(w, w.cu_q, w.Tq, rows, w.Hq * kDh * (int)sizeof(T) / 4, 0u, part, parts);
-    if (lse) fill_outside(w, w.cu_q, w.Tq, lse, w.Hq, 0xff800000u, part, parts);
+    fill_outside(w, w.cu_q, w.Tq, kWarps, blockIdx.x, gridDim.x, kWarps, rows, w.Hq * kDh * (int)sizeof(T) / 4, 0u);
+    if (lse) fill_outside(w, w.cu_q, w.Tq, kWarps, blockIdx.x, gridDim.x, kWarps, lse, w.Hq, 0xff800000u);
   }
 }
 template <typename T>
-__device__ __forceinline__ void no_key_tile(const Win& w, const Tiles& all) {
-  if (all.bad || !w.zero_outside || blockIdx.y != 0) return;
+__device__ __forceinline__ void no_key_tile(const Win& w, bool bad) {
+  if (bad || !w.zero_outside || blockIdx.y != 0) return;
   const int words = w.Hkv * kDh * (int)sizeof(T) / 4;
-  const int part = (blockIdx.x - all.total) * kWarps + (threadIdx.x >> 5), parts = (gridDim.x - all.total) * kWarps;
-  fill_outside(w, w.cu_k, w.Tk, w.dk, words, 0u, part, parts);
-  fill_outside(w, w.cu_k, w.Tk, w.dv, words, 0u, part, parts);
+  fill_outside(w, w.cu_k, w.Tk, kWarps, blockIdx.x, gridDim.x, kWarps, w.dk, words, 0u);
+  fill_outside(w, w.cu_k, w.Tk, kWarps, blockIdx.x, gridDim.x, kWarps, w.dv, words, 0u);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) window_rows_kernel(const Win w) {
   Tile s;
-  Tiles all;
-  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &all)) return no_query_tile<T>(w, all, w.out, w.lse);
+  bool bad;
+  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &bad)) return no_query_tile<T>(w, bad, w.out, w.lse);
   const int r = s.t * kWarps + (threadIdx.x >> 5);
   if (r < s.lq) out_row<T>(w, s, r, blockIdx.y);
 }
@@ -44,8 +42,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_rows_kernel(const Win w) {
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) window_dq_rows_kernel(const Win w) {
   Tile s;
-  Tiles all;
-  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &all)) return no_query_tile<T>(w, all, w.dq, nullptr);
+  bool bad;
+  if (!find_tile(w, blockIdx.x, kWarps, false, &s, &bad)) return no_query_tile<T>(w, bad, w.dq, nullptr);
   const int r = s.t * kWarps + (threadIdx.x >> 5);
   if (r >= s.lq) return;
   delta_row<T>(w, (size_t)(s.q0 + r) * w.Hq + blockIdx.y);
@@ -56,8 +54,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_dq_rows_kernel(const Win w
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win w) {
   Tile s;
-  Tiles all;
-  if (!find_tile(w, blockIdx.x, kWarps, true, &s, &all)) return no_key_tile<T>(w, all);
+  bool bad;
+  if (!find_tile(w, blockIdx.x, kWarps, true, &s, &bad)) return no_key_tile<T>(w, bad);
   const int j = s.t * kWarps + (threadIdx.x >> 5);
   if (j < s.lk) dkv_row<T>(w, s, j, blockIdx.y);
 }

@@ -124,14 +124,12 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   }
   __syncwarp();
   Tile s;
-  Tiles all;
-  if (!find_tile(w, blockIdx.x, tokens, false, &s, &all)) {
-    if (all.bad) {
+  bool bad;
+  if (!find_tile(w, blockIdx.x, tokens, false, &s, &bad)) {
+    if (bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
     } else if (w.zero_outside && blockIdx.y == 0) {
-      constexpr int kWarps = kThreads / 32;
-      fill_outside(w, w.cu_q, w.Tq, w.dq, w.Hq * kDh / 2, 0u, (blockIdx.x - all.total) * kWarps + warp,
-                   (gridDim.x - all.total) * kWarps);
+      fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kThreads / 32, w.dq, w.Hq * kDh / 2, 0u);
     }
     return;
   }
@@ -439,8 +437,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
   Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
-  Tiles* tiles_slot = reinterpret_cast<Tiles*>(tile_slot + 1);
-  int* found_slot = reinterpret_cast<int*>(tiles_slot + 1);
+  int* found_slot = reinterpret_cast<int*>(tile_slot + 1);      // 0: none, 1: one, 2: wrong offsets
   volatile uint8_t* redo = smem + kRedoOff;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kRowsPerTile >> w.gshift;
@@ -449,13 +446,11 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
   if (warp == 0) {
     Tile s;
-    Tiles all;
-    const bool found = far ? find_piece(w, x, [&](int lq, int lk) { return far_pieces<kKeys, kRowsPerTile>(w, lq, lk); }, &s, &all)
-                           : find_tile(w, x, kKeys, true, &s, &all);
+    bool bad;
+    const bool found = far ? find_far<kKeys, kRowsPerTile>(w, x, &s, &bad) : find_tile(w, x, kKeys, true, &s, &bad);
     if (lane == 0) {
       *tile_slot = s;
-      *tiles_slot = all;
-      *found_slot = found;
+      *found_slot = bad ? 2 : found;
     }
   }
   if (threadIdx.x == 32) {
@@ -478,13 +473,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   }
   if (threadIdx.x < kKeys) redo[threadIdx.x] = 0;
   __syncthreads();
-  if (!*found_slot) {
-    const Tiles all = *tiles_slot;
-    if (!far && !all.bad && w.zero_outside && blockIdx.y == 0) {
-      constexpr int kWarps = kThreads / 32;
-      const int part = (x - all.total) * kWarps + warp, parts = (key_grid - all.total) * kWarps;
-      fill_outside(w, w.cu_k, w.Tk, w.dk, w.Hkv * kDh / 2, 0u, part, parts);
-      fill_outside(w, w.cu_k, w.Tk, w.dv, w.Hkv * kDh / 2, 0u, part, parts);
+  if (*found_slot != 1) {
+    if (!far && *found_slot == 0 && w.zero_outside && blockIdx.y == 0) {
+      fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh / 2, 0u);
+      fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dv, w.Hkv * kDh / 2, 0u);
     }
     return;
   }
@@ -697,11 +689,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         sum = fmaf(y, 0.f, sum);
         o[e] = __float_as_uint(y);
       }
-      // Partial sums of the sink rows.  A sequence's first slot is its tile's,
-      // the next ones its far CTAs' (x counts the far CTAs of all sequences).
-      int slot = x + s.b + 1;
-      if (split_rows > 0 && !far)
-        slot = pieces_before(w, s.b, [&](int lq, int lk) { return far_pieces<kKeys, kRowsPerTile>(w, lq, lk); }) + s.b;
+      const int slot = far ? x + s.b + 1 : part_slot<kRowsPerTile>(w, s);       // of the sink rows' partial sums
       if (rl < split_rows) {
         float4* dst = reinterpret_cast<float4*>(part_row(w, slot, g, rl) + col0);
 #pragma unroll

@@ -144,17 +144,17 @@ __device__ __forceinline__ bool not_finite(const float* c) {
 
 // The query tile of a CTA; false where it has none (the rows outside are filled).
 __device__ __forceinline__ bool query_tile(const Win& w, Tile* s, void* rows, float* lse) {
-  Tiles all;
-  if (find_tile(w, blockIdx.x, kRows >> w.gshift, false, s, &all)) {
+  const int tokens = kRows >> w.gshift;
+  bool bad;
+  if (find_tile(w, blockIdx.x, tokens, false, s, &bad)) {
     s->t = s->n - 1 - s->t;      // the tiles with most keys first
     return true;
   }
-  if (all.bad) {
+  if (bad) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
   } else if (w.zero_outside && blockIdx.y == 0) {
-    const int part = (blockIdx.x - all.total) * 4 + (threadIdx.x >> 5), parts = (gridDim.x - all.total) * 4;
-    fill_outside(w, w.cu_q, w.Tq, rows, w.Hq * kDh, 0u, part, parts);
-    if (lse) fill_outside(w, w.cu_q, w.Tq, lse, w.Hq, 0xff800000u, part, parts);
+    fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kThreads / 32, rows, w.Hq * kDh, 0u);
+    if (lse) fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kThreads / 32, lse, w.Hq, 0xff800000u);
   }
   return false;
 }
@@ -326,14 +326,12 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
   const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
   const int x = far ? blockIdx.x - key_grid : blockIdx.x;
   const int g = blockIdx.y, tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  auto pieces = [&](int lq, int lk) { return far_pieces<kKeys, kRows>(w, lq, lk); };
   Tile s;
-  Tiles all;
-  if (!(far ? find_piece(w, x, pieces, &s, &all) : find_tile(w, x, kKeys, true, &s, &all))) {
-    if (!far && !all.bad && w.zero_outside && blockIdx.y == 0) {
-      const int part = (x - all.total) * 4 + (threadIdx.x >> 5), parts = (key_grid - all.total) * 4;
-      fill_outside(w, w.cu_k, w.Tk, w.dk, w.Hkv * kDh, 0u, part, parts);
-      fill_outside(w, w.cu_k, w.Tk, w.dv, w.Hkv * kDh, 0u, part, parts);
+  bool bad;
+  if (!(far ? find_far<kKeys, kRows>(w, x, &s, &bad) : find_tile(w, x, kKeys, true, &s, &bad))) {
+    if (!far && !bad && w.zero_outside && blockIdx.y == 0) {
+      fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh, 0u);
+      fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dv, w.Hkv * kDh, 0u);
     }
     return;
   }
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
     if (w.window > 0) rb = min(rb, j1 + w.window - 1 - shift);
   }
   // Rows below `split_rows` of this tile leave float partial sums.
-  const int split_rows = far || (j0 == 0 && pieces(s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
+  const int split_rows = far || (j0 == 0 && far_pieces<kKeys, kRows>(w, s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
   load_rows(K, [&](int i) { return key_row(w, s, g, w.k, j0 + i); });
   load_rows(V, [&](int i) { return key_row(w, s, g, w.v, j0 + i); });
   if (threadIdx.x < kKeys) redo[threadIdx.x] = 0;
@@ -385,8 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
     __syncthreads();
   }
   if (ra > rb) loads_done();
-  int slot = x + s.b + 1;       // a far piece's; the tile's own comes before its sequence's pieces
-  if (split_rows > 0 && !far) slot = pieces_before(w, s.b, pieces) + s.b;
+  const int slot = far ? x + s.b + 1 : part_slot<kRows>(w, s);      // of the sink rows' partial sums
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = row_tn(i);

@@ -138,15 +138,14 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   }
   __syncwarp();
   Tile s;
-  Tiles all;
-  if (!find_tile(w, blockIdx.x, tokens, false, &s, &all)) {
-    if (all.bad) {
+  bool bad;
+  if (!find_tile(w, blockIdx.x, tokens, false, &s, &bad)) {
+    if (bad) {
       if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
     } else if (w.zero_outside && blockIdx.y == 0 && blockIdx.z == 0) {
       constexpr int kWarps = kThreads / 32;
-      const int part = (blockIdx.x - all.total) * kWarps + warp, parts = (gridDim.x - all.total) * kWarps;
-      fill_outside(w, w.cu_q, w.Tq, w.out, w.Hq * kDh / 2, 0u, part, parts);
-      if (w.lse) fill_outside(w, w.cu_q, w.Tq, w.lse, w.Hq, 0xff800000u, part, parts);
+      fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kWarps, w.out, w.Hq * kDh / 2, 0u);
+      if (w.lse) fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kWarps, w.lse, w.Hq, 0xff800000u);
     }
     return;
   }

@@ -46,12 +46,6 @@ struct Tile {
   int k0, lk;     // its key rows
 };
 
-// What find_tile learns of all sequences together.
-struct Tiles {
-  int total;      // tiles of all sequences
-  bool bad;       // an offset is out of order or out of range
-};
-
 // Position of the query at row r of its sequence among the sequence's keys.
 __device__ __forceinline__ int position(const Tile& s, int r) { return s.lk - s.lq + r; }
 // First key the window of position p reaches.
@@ -62,81 +56,94 @@ __device__ __forceinline__ bool sees(const Win& w, int p, int j) {
   return j <= p && (j >= window_low(w, p) || j < w.sinks);
 }
 
-// Piece number x of all sequences' pieces, count(lq, lk) of them for a sequence
-// of lq queries and lk keys, found by one warp: it adds up the counts 32
-// sequences at a time.  On the way it checks every offset.  All 32 lanes call
-// it and get the same answer: whether there is such a piece (never where an
-// offset is wrong).
+// Which CTA takes which piece of which sequence, where every `per` rows (a power
+// of two) of a sequence are a piece at most: the pieces of sequence b are the
+// CTAs base(b) .. base(b) + n - 1 with base(b) = cu[b] / per + b.  Since
+// base(b + 1) - base(b) >= ceil((cu[b + 1] - cu[b]) / per), no two sequences
+// share a CTA, some CTAs have no piece, and a piece is found without adding up
+// the counts of the sequences before it.
+__device__ __forceinline__ int log2_of(int per) { return __ffs(per) - 1; }
+
+// Whether the offsets of sequence b are out of order or out of range.
+__device__ __forceinline__ bool off_range(const Win& w, int q0, int q1, int k0, int k1) {
+  return q0 < 0 || q1 < q0 || q1 > w.Tq || k0 < 0 || k1 < k0 || k1 > w.Tk;
+}
+__device__ __forceinline__ bool off_range(const Win& w, int b) {
+  return off_range(w, __ldg(w.cu_q + b), __ldg(w.cu_q + b + 1), __ldg(w.cu_k + b), __ldg(w.cu_k + b + 1));
+}
+
+// The piece of CTA number x, `per` rows of queries (or of keys with over_keys)
+// a piece and count(lq, lk) of them in a sequence of lq queries and lk keys:
+// one warp halves the sequences by 32 until 32 are left, one a lane, whose
+// offsets it checks.  All 32 lanes call it and get the same answer: whether
+// there is such a piece, never with offsets that are wrong; *bad: some of those
+// looked at are.
 template <typename Count>
-__device__ __forceinline__ bool find_piece(const Win& w, int x, Count count, Tile* out, Tiles* all) {
-  const int lane = threadIdx.x & 31;
-  int base = 0;
-  bool found = false, wrong = false;
+__device__ __forceinline__ bool find_piece(const Win& w, int x, int per, bool over_keys, Count count, Tile* out,
+                                           bool* bad) {
+  const int lane = threadIdx.x & 31, shift = log2_of(per);
+  const int32_t* cu = over_keys ? w.cu_k : w.cu_q;
+  int lo = 0, hi = w.B;
 #pragma unroll 1
-  for (int b0 = 0; b0 < w.B; b0 += 32) {
-    const int b = b0 + lane;
-    const bool in = b < w.B;
-    const int q0 = in ? __ldg(w.cu_q + b) : 0, q1 = in ? __ldg(w.cu_q + b + 1) : 0;
-    const int k0 = in ? __ldg(w.cu_k + b) : 0, k1 = in ? __ldg(w.cu_k + b + 1) : 0;
-    const bool off = in && (q0 < 0 || q1 < q0 || q1 > w.Tq || k0 < 0 || k1 < k0 || k1 > w.Tk);
-    wrong |= __any_sync(0xffffffffu, off);
-    const int n = !in || off ? 0 : count(q1 - q0, k1 - k0);
-    int incl = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += up;
-    }
-    const int first = base + incl - n;
-    const uint32_t hit = __ballot_sync(0xffffffffu, !found && x >= first && x < first + n);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      out->b = b0 + src;
-      out->t = x - __shfl_sync(0xffffffffu, first, src);
-      out->n = __shfl_sync(0xffffffffu, n, src);
-      out->q0 = __shfl_sync(0xffffffffu, q0, src);
-      out->lq = __shfl_sync(0xffffffffu, q1 - q0, src);
-      out->k0 = __shfl_sync(0xffffffffu, k0, src);
-      out->lk = __shfl_sync(0xffffffffu, k1 - k0, src);
-      found = true;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+  while (hi - lo > 32) {
+    const int step = (hi - lo + 31) >> 5, b = lo + lane * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, lane == 0 || (b < hi && (__ldg(cu + b) >> shift) + b <= x));
+    lo += (at == 0xffffffffu ? 31 : __ffs(~at) - 2) * step;
+    hi = min(hi, lo + step);
   }
-  all->total = base;
-  all->bad = wrong;
-  return found && !wrong;
+  const int b = lo + lane;
+  const bool in = b < hi;
+  const int q0 = in ? __ldg(w.cu_q + b) : 0, q1 = in ? __ldg(w.cu_q + b + 1) : 0;
+  const int k0 = in ? __ldg(w.cu_k + b) : 0, k1 = in ? __ldg(w.cu_k + b + 1) : 0;
+  const bool off = in && off_range(w, q0, q1, k0, k1);
+  *bad = __any_sync(0xffffffffu, off);
+  const int n = !in || off ? 0 : count(q1 - q0, k1 - k0);
+  const int t = x - (((over_keys ? k0 : q0) >> shift) + b);
+  const uint32_t hit = __ballot_sync(0xffffffffu, t >= 0 && t < n);
+  if (!hit || *bad) return false;
+  const int src = __ffs(hit) - 1;
+  out->b = lo + src;
+  out->t = __shfl_sync(0xffffffffu, t, src);
+  out->n = __shfl_sync(0xffffffffu, n, src);
+  out->q0 = __shfl_sync(0xffffffffu, q0, src);
+  out->lq = __shfl_sync(0xffffffffu, q1 - q0, src);
+  out->k0 = __shfl_sync(0xffffffffu, k0, src);
+  out->lk = __shfl_sync(0xffffffffu, k1 - k0, src);
+  return true;
 }
 
-// Pieces of the sequences before sequence b (one warp; the offsets are known to
-// be right).
-template <typename Count>
-__device__ __forceinline__ int pieces_before(const Win& w, int b, Count count) {
-  int n = 0;
-  for (int i = threadIdx.x & 31; i < b; i += 32)
-    n += count(__ldg(w.cu_q + i + 1) - __ldg(w.cu_q + i), __ldg(w.cu_k + i + 1) - __ldg(w.cu_k + i));
-  return __reduce_add_sync(0xffffffffu, n);
+// The tile of CTA number x: `per` rows of queries, or of keys with over_keys, a
+// tile; every sequence starts a new one.  The query tiles' first CTAs look at
+// all offsets between them.
+__device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool over_keys, Tile* out, bool* bad) {
+  const bool found =
+      find_piece(w, x, per, over_keys, [=](int lq, int lk) { return ((over_keys ? lk : lq) + per - 1) / per; }, out, bad);
+  if (over_keys || w.B <= 32 || x > w.B / 32) return found;
+  const int b = 32 * x + (threadIdx.x & 31);
+  *bad |= __any_sync(0xffffffffu, b < w.B && off_range(w, b));
+  return found && !*bad;
 }
 
-// Tile number x of all sequences' tiles: `per` rows of queries, or of keys with
-// over_keys, a tile; every sequence starts a new one.
-__device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool over_keys, Tile* out, Tiles* all) {
-  return find_piece(w, x, [=](int lq, int lk) { return ((over_keys ? lk : lq) + per - 1) / per; }, out, all);
-}
-
-// Grid size that covers every tile whatever the offsets are, and has at least
-// one CTA without a tile: sum over b of ceil(n_b / per) <= rows / per + B.
+// Grid size that covers every tile whatever the offsets are, with a last CTA
+// that has none: base(B) <= rows / per + B.
 inline long tile_grid(long rows, int per, int batch) { return rows / per + batch + 1; }
 
-// Warp number part of `parts` sets its share of the rows outside [cu[0], cu[B])
-// of a tensor of T rows of `words` 32-bit words to `value`.
-__device__ __forceinline__ void fill_outside(const Win& w, const int32_t* cu, int T, void* base, int words,
-                                             uint32_t value, int part, int parts) {
-  const long c0 = __ldg(cu), c1 = __ldg(cu + w.B);
-  const long before = c0 * words, total = before + (T - c1) * words;
+// Sets the rows outside [cu[0], cu[B]) of a tensor of T rows of `words` 32-bit
+// words to `value`: the work of the CTAs x before base(0) and from base(B) on
+// of a tile_grid of `grid`, `warps` a CTA.  Other CTAs return.
+__device__ __forceinline__ void fill_outside(const Win& w, const int32_t* cu, int T, int per, int x, int grid,
+                                             int warps, void* base, int words, uint32_t value) {
+  const int shift = log2_of(per), c0 = __ldg(cu), c1 = __ldg(cu + w.B);
+  if (c0 < 0 || c1 < c0 || c1 > T) return;
+  const int front = c0 >> shift, back = (c1 >> shift) + w.B;
+  if (x >= front && x < back) return;
+  const long part = (long)(x < front ? x : front + x - back) * warps + (threadIdx.x >> 5);
+  const long parts = (long)(front + grid - back) * warps;
+  const long before = (long)c0 * words, total = before + (long)(T - c1) * words;
   uint32_t* p = (uint32_t*)base;
 #pragma unroll 1
-  for (long i = part * 32L + (threadIdx.x & 31); i < total; i += parts * 32L)
-    p[i < before ? i : c1 * words + (i - before)] = value;
+  for (long i = part * 32 + (threadIdx.x & 31); i < total; i += parts * 32)
+    p[i < before ? i : (long)c1 * words + (i - before)] = value;
 }
 
 // SMs of the current device.

@@ -1,5 +1,7 @@
 """The causal sequence operators on the GPU against their definition in 64 bits (seq_reference.py), at the sizes and
 masks where they can go wrong."""
+import random
+
 import pytest
 import torch
 
@@ -71,6 +73,37 @@ def test_many_sequences(p3, cuda_device):
     """More sequences than one pass over the offsets takes at once, most of them short."""
     lens = [(7 * i) % 23 for i in range(150)]
     check_window(p3, lens, lens, 4, 1, 9, 2, torch.bfloat16, cuda_device)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hkv,W,S", [(2, 1, 20, 3), (8, 1, 0, 0)])
+def test_hundreds_of_sequences(p3, cuda_device, Hq, Hkv, W, S, dtype):
+    """Two steps of the search for a CTA's sequence; empty ones, ones of one token and ones of several tiles among
+    them, and keys of their own lengths."""
+    r = random.Random(5)
+    lens = [r.choice((0, 1, 1, 2, 9, 31, 33)) for _ in range(230)] + [300, 0, 1] + [r.choice((0, 5)) for _ in range(60)]
+    klens = [n + r.choice((0, 0, 3, 130)) for n in lens]
+    check_window(p3, lens, klens, Hq, Hkv, W, S, dtype, cuda_device)
+
+
+def test_as_many_sequences_as_there_may_be(p3, cuda_device):
+    """Sequences of one token: the softmax of one score is 1, so out is v, and dv the group's dout."""
+    dev, n = cuda_device, 65535
+    q, k, v, dout = inputs([n], [n], 2, 1, torch.bfloat16, dev, 3)
+    cfg = p3.make_seq_config(Hq=2, Hkv=1, window=16, sinks=1)
+    cu = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = p3.window_attn(cfg, q, k, v, cu, err=err)
+    dv = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout, err=err)[2]
+    assert p3.check_status(err) == 0
+    assert torch.equal(out, v.expand(-1, 2, -1))
+    score = (q.double() * k.double()).sum(-1) / 8
+    assert ((lse.double() - score).abs() <= 2.0 ** -24 * (66 * (q.double() * k.double()).abs().sum(-1) / 8
+                                                          + 16 + 4 * score.abs())).all()
+    # P is within 2^-20 of 1 and rounds to 1; the sum of two and its rounding are left
+    want = dout.double().sum(1, keepdim=True)
+    assert ((dv.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -23) * want.abs() + 2.0 ** -23 * dout.double().abs().sum(
+        1, keepdim=True)).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -188,6 +221,38 @@ def test_wrong_offsets_are_reported(p3, cuda_device):
             assert int(err) == p3.DEVERR_LENGTHS and p3.check_status(err) == 9
             p3.window_attn_bwd(cfg, q, k, v, cu_q, cu_k, out, lse, dout, err=err)
             assert p3.check_status(err) == 9 and p3.check_status(err) == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_wrong_offsets_among_many_are_reported(p3, cuda_device, dtype):
+    """Wherever the wrong offset of a large batch stands, some CTA sees it."""
+    dev, B = cuda_device, 200
+    q, k, v, dout = inputs([4 * B], [4 * B], 2, 1, dtype, dev)
+    cfg = p3.make_seq_config(Hq=2, Hkv=1, window=8, sinks=2, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+    good = torch.arange(B + 1, dtype=torch.int32, device=dev) * 4
+    for at in (0, 1, 31, 32, 33, 100, 199, 200):
+        for value in (-5, 4 * B + 1, 2 ** 31 - 1):
+            bad = good.clone()
+            bad[at] = value
+            for cu_q, cu_k in ((bad, good), (good, bad)):
+                err = torch.zeros(1, dtype=torch.int32, device=dev)
+                out, lse = p3.window_attn(cfg, q, k, v, cu_q, cu_k, err=err)
+                assert p3.check_status(err) == 9
+                p3.window_attn_bwd(cfg, q, k, v, cu_q, cu_k, out, lse, dout, err=err)
+                assert p3.check_status(err) == 9
+
+
+def test_rows_of_no_sequence_of_many(p3, cuda_device):
+    """The rows outside, many before and behind a batch of many sequences."""
+    dev, B = cuda_device, 100
+    for dtype in TYPES:
+        q, k, v, dout = inputs([3000], [3000], 2, 1, dtype, dev, 2)
+        cfg = p3.make_seq_config(Hq=2, Hkv=1, window=20, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+        cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * 7 + 900
+        out, lse = p3.window_attn(cfg, q, k, v, cu)
+        grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout)
+        for t, zero in ((out, 0.0), (lse, -float("inf"))) + tuple((g, 0.0) for g in grads):
+            assert (t[:900] == zero).all() and (t[1600:] == zero).all() and (t[900:1600] != zero).any()
 
 
 def test_autograd_and_same_bits(p3, cuda_device):
