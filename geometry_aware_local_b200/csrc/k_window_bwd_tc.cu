@@ -30,6 +30,12 @@
 // the tile itself leave float partial sums of the sink rows; window_sinks_kernel
 // adds them in a fixed order.  No atomics: the same inputs give the same bits.
 //
+// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.823 ms, 417 TFLOP/s (five
+// products), about 0.35 ms of it the query side.  As in the forward the pace is
+// that of the softmax warps' chains, not of the tensor cores: without any
+// arithmetic between the loads and the stores the key side still takes three
+// quarters of its time, and with an eighth of its products no less.
+//
 // A gradient row that is not finite may be spoilt by 0 times a NaN or an
 // infinity of a row it does not depend on; it is computed again from its
 // visible pairs alone (dq_row, dkv_row).
