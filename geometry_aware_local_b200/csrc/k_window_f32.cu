@@ -3,15 +3,18 @@
 //
 // The tiles are those of the tensor-core kernels (rows = (token, query head)
 // pairs of one key head's group; key range and sinks; see k_window_tc.cu and
-// k_window_bwd_tc.cu), 64 rows by 64 keys.  128 threads hold a 64 x 64 product
-// as 8 x 4 values each: thread (ty, tx) = (tid / 16, tid % 16) has the rows
-// ty + 8 i and the columns tx + 16 j of S and dP (both operands are read four
+// k_window_bwd_tc.cu), 64 rows by 64 keys.  256 threads hold a 64 x 64 product
+// as 4 x 4 values each: thread (ty, tx) = (tid / 16, tid % 16) has the rows
+// ty + 16 i and the columns tx + 16 j of S and dP (both operands are read four
 // contraction steps at a time, 16 bytes a load, from rows padded to 68 floats),
 // and the dims 4 tx .. 4 tx + 3 of O, dQ, dK and dV.  Everything is formed and
-// kept in 32 bits.  Bound: the shared-memory reads (12 loads of 16 bytes per 128
-// multiply-adds and thread) and the multiply-adds themselves.  2,050 tokens in
-// three sequences, 4 / 2 heads, window 200, one sink: forward and backward 0.21 ms
-// (one warp a row of the definition: 1.27 ms).
+// kept in 32 bits, two multiply-adds an instruction.  Bound: the shared-memory
+// reads (8 loads of 16 bytes per 64 multiply-adds and thread; 77 % of their
+// rate).  128 threads with 8 x 4 values read less, but where a call has few
+// tiles their warps are too few.  2,050 tokens in three sequences, 4 / 2 heads,
+// window 200, one sink: forward 33 us (128 threads, a multiply-add an
+// instruction: 42), backward 119 us (166, with the two sides one after the
+// other).  16,384 tokens, 8 / 2 heads: 0.323 and 1.05 ms (0.330, 1.14).
 //
 // What is hidden has P = 0; rows that 0 times a NaN or an infinity spoilt are
 // computed again (out_row, dq_row, dkv_row), as in the tensor-core kernels.
@@ -22,76 +25,89 @@ namespace pack3d {
 namespace seq {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kPer = 64 * 16 / kThreads, kSub = kThreads / 16;      // a thread's rows of a product, and their distance
 constexpr int kPad = kDh + 4;
 constexpr int kTileFloats = 64 * kPad;
 
-typedef float Micro[8][4];
+typedef float Micro[kPer][4];
 
 __device__ __forceinline__ void zero(Micro c) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < kPer; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
 }
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// c[i][j] += sum_d a[ty + 8 i][d] b[tx + 16 j][d]: both operands' rows run along
-// the contraction.
+// c[i][j] += sum_d a[ty + kSub i][d] b[tx + 16 j][d]: both operands' rows run
+// along the contraction, even and odd steps apart.
 __device__ __forceinline__ void mul_nt(Micro c, const float* a, const float* b) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  float2 e[kPer][4];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
   for (int d = 0; d < kDh; d += 4) {
-    float4 x[8], y[4];
+    float4 x[kPer], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = at4(a + (ty + 8 * i) * kPad + d);
+    for (int i = 0; i < kPer; ++i) x[i] = at4(a + (ty + kSub * i) * kPad + d);
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = at4(b + (tx + 16 * j) * kPad + d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kPer; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z, fmaf(x[i].y, y[j].y, fmaf(x[i].x, y[j].x, c[i][j]))));
+      for (int j = 0; j < 4; ++j) {
+        e[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), e[i][j]);
+        e[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), e[i][j]);
+      }
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] = e[i][j].x + e[i][j].y;
 }
-// c[i][j] += sum_k a[ty + 8 i][k] b[k][4 tx + j].
+__device__ __forceinline__ void axpy(float* c, float v, float4 y) {
+  const float2 p = __ffma2_rn(make_float2(v, v), make_float2(y.x, y.y), make_float2(c[0], c[1]));
+  const float2 q = __ffma2_rn(make_float2(v, v), make_float2(y.z, y.w), make_float2(c[2], c[3]));
+  c[0] = p.x; c[1] = p.y; c[2] = q.x; c[3] = q.y;
+}
+// c[i][j] += sum_k a[ty + kSub i][k] b[k][4 tx + j].
 __device__ __forceinline__ void mul_nn(Micro c, const float* a, const float* b) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll 2
   for (int k = 0; k < 64; k += 4) {
-    float4 x[8], y[4];
+    float4 x[kPer], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = at4(a + (ty + 8 * i) * kPad + k);
+    for (int i = 0; i < kPer; ++i) x[i] = at4(a + (ty + kSub * i) * kPad + k);
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = at4(b + (k + j) * kPad + 4 * tx);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[i][0] = fmaf(v[j], y[j].x, c[i][0]);
-        c[i][1] = fmaf(v[j], y[j].y, c[i][1]);
-        c[i][2] = fmaf(v[j], y[j].z, c[i][2]);
-        c[i][3] = fmaf(v[j], y[j].w, c[i][3]);
-      }
+    for (int i = 0; i < kPer; ++i) {
+      axpy(c[i], x[i].x, y[0]);
+      axpy(c[i], x[i].y, y[1]);
+      axpy(c[i], x[i].z, y[2]);
+      axpy(c[i], x[i].w, y[3]);
     }
   }
 }
 // Row of the product of the transposed operand that c[i] belongs to.
-__device__ __forceinline__ int row_tn(int i) { return 4 * (threadIdx.x >> 4) + (i & 3) + 32 * (i >> 2); }
+__device__ __forceinline__ int row_tn(int i) { return 4 * (threadIdx.x >> 4) + (i & 3) + 4 * kSub * (i >> 2); }
 // c[i][j] += sum_k a[k][row_tn(i)] b[k][4 tx + j].
 __device__ __forceinline__ void mul_tn(Micro c, const float* a, const float* b) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll 4
   for (int k = 0; k < 64; ++k) {
-    const float4 x0 = at4(a + k * kPad + 4 * ty), x1 = at4(a + k * kPad + 4 * ty + 32), y = at4(b + k * kPad + 4 * tx);
-    const float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    const float4 y = at4(b + k * kPad + 4 * tx);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i][0] = fmaf(v[i], y.x, c[i][0]);
-      c[i][1] = fmaf(v[i], y.y, c[i][1]);
-      c[i][2] = fmaf(v[i], y.z, c[i][2]);
-      c[i][3] = fmaf(v[i], y.w, c[i][3]);
+    for (int i = 0; i < kPer; i += 4) {
+      const float4 x = at4(a + k * kPad + 4 * ty + kSub * i);
+      axpy(c[i], x.x, y);
+      axpy(c[i + 1], x.y, y);
+      axpy(c[i + 2], x.z, y);
+      axpy(c[i + 3], x.w, y);
     }
   }
 }
@@ -102,8 +118,8 @@ template <typename RowOf>
 __device__ __forceinline__ void load_rows(float* tile, RowOf row_of) {
   const uint32_t base = ptx::smem_u32(tile);
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const int i = (threadIdx.x >> 4) + 8 * n, x = threadIdx.x & 15;
+  for (int n = 0; n < kPer; ++n) {
+    const int i = (threadIdx.x >> 4) + kSub * n, x = threadIdx.x & 15;
     const float* src = row_of(i);
     const uint32_t dst = base + (i * kPad + 4 * x) * 4;
     if (src) ptx::cp_async16(dst, src + 4 * x, 16);
@@ -144,40 +160,47 @@ __device__ __forceinline__ bool not_finite(const float* c) {
   return !(fmaf(c[0], 0.f, fmaf(c[1], 0.f, fmaf(c[2], 0.f, c[3] * 0.f))) == 0.f);
 }
 
-// The query tile of a CTA; false where it has none (the rows outside are filled).
-__device__ __forceinline__ bool query_tile(const Win& w, Tile* s, void* rows, float* lse) {
+// <dout, out> of the thread's row i, from its four dims of out.
+__device__ __forceinline__ float dot_row(const float* dout, int i, float4 y) {
+  const float4 x = at4(dout + ((threadIdx.x >> 4) + kSub * i) * kPad + 4 * (threadIdx.x & 15));
+  return row_sum(fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w))));
+}
+
+// The query tile x of `grid` of key head g; false where there is none (the rows
+// outside are filled).
+__device__ __forceinline__ bool query_tile(const Win& w, int x, int grid, int g, Tile* s, void* rows, float* lse) {
   const int tokens = kRows >> w.gshift;
   bool bad;
-  if (find_tile(w, blockIdx.x, tokens, false, s, &bad)) {
+  if (find_tile(w, x, tokens, false, s, &bad)) {
     s->t = s->n - 1 - s->t;      // the tiles with most keys first
     return true;
   }
   if (bad) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
-  } else if (w.zero_outside && blockIdx.y == 0) {
-    fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kThreads / 32, rows, w.Hq * kDh, 0u);
-    if (lse) fill_outside(w, w.cu_q, w.Tq, tokens, blockIdx.x, gridDim.x, kThreads / 32, lse, w.Hq, 0xff800000u);
+  } else if (w.zero_outside && g == 0) {
+    fill_outside(w, w.cu_q, w.Tq, tokens, x, grid, kThreads / 32, rows, w.Hq * kDh, 0u);
+    if (lse) fill_outside(w, w.cu_q, w.Tq, tokens, x, grid, kThreads / 32, lse, w.Hq, 0xff800000u);
   }
   return false;
 }
 
-__global__ void __launch_bounds__(kThreads, 3) window_attn_f32_kernel(const Win w) {
+__global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win w) {
   extern __shared__ float4 smem4[];
   float* Q = reinterpret_cast<float*>(smem4);
   float *K = Q + kTileFloats, *V = K + kTileFloats, *P = V + kTileFloats;
   __shared__ int redo[kRows];
   Tile s;
-  if (!query_tile(w, &s, w.out, w.lse)) return;
+  if (!query_tile(w, blockIdx.x, gridDim.x, blockIdx.y, &s, w.out, w.lse)) return;
   const int g = blockIdx.y, tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const KeyTiles<kKeys> kt = key_tiles<kKeys>(w, position(s, r0), position(s, r1));
   load_rows(Q, [&](int i) { return query_row(w, s, g, r0, r1, w.q, i); });
   if (threadIdx.x < kRows) redo[threadIdx.x] = 0;
-  float m[8], l[8];
+  float m[kPer], l[kPer];
   Micro o;
   zero(o);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
   }
@@ -188,11 +211,10 @@ __global__ void __launch_bounds__(kThreads, 3) window_attn_f32_kernel(const Win 
     load_rows(V, [&](int i) { return i < cols ? key_row(w, s, g, w.v, k0 + i) : nullptr; });
     loads_done();
     Micro c;
-    zero(c);
     mul_nt(c, Q, K);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + ((ty + 8 * i) >> w.gshift), p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + ((ty + kSub * i) >> w.gshift), p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
       float top = m[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -210,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 3) window_attn_f32_kernel(const Win 
         const float e = exp2f(c[i][j] - sub);
         l[i] += e;                      // of this thread's columns
         o[i][j] *= f;
-        P[(ty + 8 * i) * kPad + tx + 16 * j] = e;
+        P[(ty + kSub * i) * kPad + tx + 16 * j] = e;
       }
     }
     __syncthreads();
@@ -219,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 3) window_attn_f32_kernel(const Win 
   }
   if (kt.n == 0) loads_done();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = ty + 8 * i, r = r0 + (row >> w.gshift);
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
     const float sum = row_sum(l[i]);
     // A row that sees no key: its O is 0, or a NaN from a hidden value.
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -245,8 +267,8 @@ __device__ __forceinline__ void store_grads(const Win& w, const Tile& s, int r0,
                                             float* dS) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = ty + 8 * i, r = r0 + (row >> w.gshift), p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ty + kSub * i, r = r0 + (row >> w.gshift), p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = tx + 16 * j, key = k0 + col;
@@ -258,14 +280,12 @@ __device__ __forceinline__ void store_grads(const Win& w, const Tile& s, int r0,
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 2) window_dq_f32_kernel(const Win w) {
-  extern __shared__ float4 smem4[];
-  float* Q = reinterpret_cast<float*>(smem4);
+// dQ of query tile x; redo: 64 ints of shared memory.
+__device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g, float* Q, int* redo) {
   float *D = Q + kTileFloats, *K = D + kTileFloats, *V = K + kTileFloats, *dS = V + kTileFloats;
-  __shared__ int redo[kRows];
   Tile s;
-  if (!query_tile(w, &s, w.dq, nullptr)) return;
-  const int g = blockIdx.y, tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  if (!query_tile(w, x, grid, g, &s, w.dq, nullptr)) return;
+  const int tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const KeyTiles<kKeys> kt = key_tiles<kKeys>(w, position(s, r0), position(s, r1));
   load_rows(Q, [&](int i) { return query_row(w, s, g, r0, r1, w.q, i); });
@@ -273,12 +293,11 @@ __global__ void __launch_bounds__(kThreads, 2) window_dq_f32_kernel(const Win w)
   load_rows(K, [&](int i) { return query_row(w, s, g, r0, r1, w.out, i); });      // for <dout, out>
   if (threadIdx.x < kRows) redo[threadIdx.x] = 0;
   loads_done();
-  float lse2[8], delta[8];
+  float lse2[kPer], delta[kPer];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = ty + 8 * i, r = r0 + (row >> w.gshift);
-    const float4 x = at4(D + row * kPad + 4 * tx), y = at4(K + row * kPad + 4 * tx);
-    delta[i] = row_sum(fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w))));
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
+    delta[i] = dot_row(D, i, at4(K + row * kPad + 4 * tx));
     lse2[i] = 0.f;
     if (r <= r1) {
       const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
@@ -296,8 +315,6 @@ __global__ void __launch_bounds__(kThreads, 2) window_dq_f32_kernel(const Win w)
     load_rows(V, [&](int i) { return i < cols ? key_row(w, s, g, w.v, k0 + i) : nullptr; });
     loads_done();
     Micro c, d;
-    zero(c);
-    zero(d);
     mul_nt(c, Q, K);
     mul_nt(d, D, V);
     store_grads(w, s, r0, r1, k0, cols, s.lk, lse2, delta, c, d, nullptr, dS);
@@ -305,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 2) window_dq_f32_kernel(const Win w)
     mul_nn(o, dS, K);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = ty + 8 * i, r = r0 + (row >> w.gshift);
+  for (int i = 0; i < kPer; ++i) {
+    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
     if (r > r1) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[i][j] *= w.scale;
@@ -320,18 +337,17 @@ __global__ void __launch_bounds__(kThreads, 2) window_dq_f32_kernel(const Win w)
     if (redo[row]) dq_row<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
 }
 
-__global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w, int key_grid) {
-  extern __shared__ float4 smem4[];
-  float* K = reinterpret_cast<float*>(smem4);
+// dK and dV of key tile `at`, or from key_grid on of a piece of the sinks' far
+// queries.
+__device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int g, float* K, int* redo) {
   float *V = K + kTileFloats, *Q = V + kTileFloats, *D = Q + kTileFloats, *P = D + kTileFloats, *dS = P + kTileFloats;
-  __shared__ int redo[kKeys];
-  const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
-  const int x = far ? blockIdx.x - key_grid : blockIdx.x;
-  const int g = blockIdx.y, tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const bool far = at >= key_grid;
+  const int x = far ? at - key_grid : at;
+  const int tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   Tile s;
   bool bad;
   if (!(far ? find_far<kKeys, kRows>(w, x, &s, &bad) : find_tile(w, x, kKeys, true, &s, &bad))) {
-    if (!far && !bad && w.zero_outside && blockIdx.y == 0) {
+    if (!far && !bad && w.zero_outside && g == 0) {
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh, 0u);
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dv, w.Hkv * kDh, 0u);
     }
@@ -361,21 +377,23 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
   for (int rs = ra; rs <= rb; rs += tokens) {
     load_rows(Q, [&](int i) { return query_row(w, s, g, rs, rb, w.q, i); });
     load_rows(D, [&](int i) { return query_row(w, s, g, rs, rb, w.dout, i); });
-    float lse2[8], delta[8];
+    float lse2[kPer], delta[kPer];
+    float4 out[kPer];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = ty + 8 * i, r = rs + (row >> w.gshift);
-      lse2[i] = delta[i] = 0.f;
+    for (int i = 0; i < kPer; ++i) {
+      const int row = ty + kSub * i, r = rs + (row >> w.gshift);
+      lse2[i] = 0.f;
+      out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r <= rb) {
         const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
         lse2[i] = __ldg(w.lse + at) * 1.4426950408889634f;
-        delta[i] = __ldg(w.delta + at);
+        out[i] = __ldg(reinterpret_cast<const float4*>((const float*)w.out + at * kDh) + tx);
       }
     }
     loads_done();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) delta[i] = dot_row(D, i, out[i]);
     Micro c, d;
-    zero(c);
-    zero(d);
     mul_nt(c, Q, K);
     mul_nt(d, D, V);
     store_grads(w, s, rs, rb, j0, kKeys, s.lk, lse2, delta, c, d, P, dS);
@@ -387,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
   if (ra > rb) loads_done();
   const int slot = far ? x + s.b + 1 : part_slot<kRows>(w, s);      // of the sink rows' partial sums
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int row = row_tn(i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) ak[i][j] *= w.scale;
@@ -408,6 +426,20 @@ __global__ void __launch_bounds__(kThreads, 2) window_dkv_f32_kernel(const Win w
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kKeys; row += kThreads / 32)
     if (redo[row]) dkv_row<float>(w, s, j0 + row, g);
+}
+
+// Both sides in one launch, so that few tiles fill more of the GPU: neither reads
+// what the other writes (each forms <dout, out> of its rows).  The key sides come
+// first, as the longer ones (behind the query sides 6 % later), and a tile's
+// heads side by side (heads one after the other: up to a third later).
+__global__ void __launch_bounds__(kThreads, 2) window_bwd_f32_kernel(const Win w, int key_grid, int key_ctas,
+                                                                     int query_ctas) {
+  extern __shared__ float4 smem4[];
+  __shared__ int redo[64];
+  float* tiles = reinterpret_cast<float*>(smem4);
+  const int x = blockIdx.x, y = x - key_ctas * w.Hkv;
+  if (y < 0) key_side(w, x / w.Hkv, key_grid, x % w.Hkv, tiles, redo);
+  else query_side(w, y / w.Hkv, query_ctas, y % w.Hkv, tiles, redo);
 }
 
 template <typename K>
@@ -433,16 +465,12 @@ cudaError_t launch_window_attn_f32(const Win& w, cudaStream_t st) {
 }
 
 cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st) {
-  cudaError_t e = allow(window_dq_f32_kernel, 5);
-  if (e == cudaSuccess) e = allow(window_dkv_f32_kernel, 6);
+  cudaError_t e = allow(window_bwd_f32_kernel, 6);
   if (e != cudaSuccess) return e;
-  const dim3 gq((unsigned)tile_grid(w.Tq, kRows >> w.gshift, w.B), w.Hkv);
-  window_dq_f32_kernel<<<gq, kThreads, 5 * kTileFloats * 4, st>>>(w);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int key_grid = (int)tile_grid(w.Tk, kKeys, w.B);
-  const dim3 gk((unsigned)(key_grid + far_grid<kRows>(w)), w.Hkv);
-  window_dkv_f32_kernel<<<gk, kThreads, 6 * kTileFloats * 4, st>>>(w, key_grid);
+  const int key_grid = (int)tile_grid(w.Tk, kKeys, w.B), key_ctas = key_grid + (int)far_grid<kRows>(w);
+  const int query_ctas = (int)tile_grid(w.Tq, kRows >> w.gshift, w.B);
+  window_bwd_f32_kernel<<<(unsigned)(key_ctas + query_ctas) * w.Hkv, kThreads, 6 * kTileFloats * 4, st>>>(
+      w, key_grid, key_ctas, query_ctas);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_window_sinks<float, kKeys, kRows>(w, st);

@@ -261,7 +261,9 @@ __device__ __noinline__ void dkv_row(const Win& w, const Tile& s, int j, int g) 
     for (int h = g << w.gshift; h < (g + 1) << w.gshift; ++h) {
       const size_t row = (size_t)(s.q0 + r) * w.Hq + h;
       const float2 q = load2((const T*)w.q + row * kDh), d = load2((const T*)w.dout + row * kDh);
-      const float2 pd = pair_grad(w, q, d, w.lse[row], w.delta[row], k, v);
+      // (The float kernels run both sides at once: there may be no delta yet.)
+      const float delta = sizeof(T) == 4 ? dot2(d, load2((const T*)w.out + row * kDh)) : w.delta[row];
+      const float2 pd = pair_grad(w, q, d, w.lse[row], delta, k, v);
       ak.x = fmaf(pd.y, q.x, ak.x);
       ak.y = fmaf(pd.y, q.y, ak.y);
       av.x = fmaf(pd.x, d.x, av.x);
