@@ -13,16 +13,22 @@
 //   leaves it for the second kernel.
 //
 // window_dkv_tc_kernel: one 128-key tile of one key head per CTA and the
-//   queries whose window reaches it, 128 rows a step, one CTA per SM.  S^T and
-//   dP^T (M = 128 keys, N = 128 rows) go to tensor memory; four softmax
-//   warpgroups (thread = key, one 32-row chunk of the step each) write dS^T and
-//   P^T beside them as packed bf16, from where a second MMA warp accumulates
-//   dK += dS^T Q and dV += P^T dout (M = 128 keys, N = 64, K = 128 rows).
-//   Where no key of a warp is seen by any row of its chunk it writes zeros
-//   without an exponential.  The transposed products cost a broadcast load of
-//   each row's lse and D; with S and dP by rows, dS and P had to go through
-//   64 KiB of shared memory, whose reads held up the tensor cores (65,536
-//   tokens, window 1024 / 4096: 0.874 / 2.51 ms, now 0.825 / 2.29 ms).
+//   queries whose window reaches it, 64 rows a step, one CTA per SM.  S^T and
+//   dP^T (M = 128 keys, N = 64 rows) go to tensor memory, already less the rows'
+//   lse / scale and D: one more product of K = 16, a column of ones by each term
+//   in three bf16 pieces, which the query side leaves beside D.  The softmax warps
+//   (thread = key, a 32-row chunk of the step each) write dS^T and P^T beside
+//   them as packed bf16, from where a second MMA warp accumulates
+//   dK += dS^T Q and dV += P^T dout (M = 128 keys, N = 64, K = 64 rows).  Two
+//   groups of eight softmax warps take every other step, each with its own
+//   tensor memory.  Where no key of a warp is seen by any row of its chunk it
+//   writes zeros without an exponential.
+//   65,536 tokens, window 1,024 / 8,192 tokens, 16 / 2 heads, no window, both
+//   kernels: S and dP by rows, dS and P through 64 KiB of shared memory for the
+//   second product 0.874 / - ms; transposed, with the terms added by the threads
+//   from shared memory 0.837 / 0.963; two groups 0.807 / 0.910; the terms added by
+//   the tensor cores 0.748 / 0.786.  (A thread's load of 16 bytes that every lane
+//   wants is four passes of shared memory, which the products' operands need.)
 //
 // The first key tile of a sequence holds its sinks, which every later query
 // sees.  Their gradients from the queries beyond the tile's window are formed
@@ -30,11 +36,10 @@
 // the tile itself leave float partial sums of the sink rows; window_sinks_kernel
 // adds them in a fixed order.  No atomics: the same inputs give the same bits.
 //
-// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.823 ms, 417 TFLOP/s (five
-// products), about 0.35 ms of it the query side.  As in the forward the pace is
-// that of the softmax warps' chains, not of the tensor cores: without any
-// arithmetic between the loads and the stores the key side still takes three
-// quarters of its time, and with an eighth of its products no less.
+// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.748 ms, 459 TFLOP/s (five
+// products), about 0.37 ms of it the query side.  As in the forward the pace is
+// that of the softmax warps' chains (load, exponentials, store, arrive), not of
+// the tensor cores.
 //
 // A gradient row that is not finite may be spoilt by 0 times a NaN or an
 // infinity of a row it does not depend on; it is computed again from its
@@ -53,6 +58,14 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   ptx::tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
+
+// A term of row `orow` for the key side's products, as three bf16 pieces whose sum
+// is off by 2^-24 of it: each takes what the ones before leave.
+__device__ __forceinline__ void write_terms(const Win& w, int plane, size_t orow, float x) {
+  const float hi = __bfloat162float(__float2bfloat16(x)), mid = __bfloat162float(__float2bfloat16(x - hi));
+  reinterpret_cast<uint4*>(w.terms)[(size_t)plane * w.Tq * w.Hq + orow] =
+      make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(x - hi - mid, 0.f), 0u, 0u);
 }
 
 // ============================================================================
@@ -288,6 +301,8 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
       }
       w.delta[orow] = delta;
+      write_terms(w, 0, orow, p >= 0 ? -w.lse[orow] / w.scale : 0.f);
+      write_terms(w, 1, orow, -delta);
     }
     const float2 nd2 = make_float2(-delta, -delta);
 #pragma unroll 1
@@ -399,35 +414,45 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 namespace k_side {
 
 constexpr int kKeys = 128;                      // keys per CTA (M of the dK / dV accumulators)
-constexpr int kSoftmaxWarps = 16;               // four warpgroups, one 32-key chunk each
+constexpr int kSoftmaxWarps = 16;               // two groups of 128 keys x two 32-row chunks
 // Two MMA warps: the first issues each step's S and dP, the second its dK / dV
 // accumulation, so that S and dP of the next step never queue behind it.
 constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
 constexpr int kMmaWarp = kSoftmaxWarps, kMmaWarp2 = kSoftmaxWarps + 1, kTmaWarp = kSoftmaxWarps + 2;
-// S^T, dP^T (lane = key, column = query row), dK, dV, and P^T, dS^T as packed bf16.
-constexpr int kColS = 0, kColDP = 128, kColDK = 256, kColDV = 320, kColP = 384, kColDS = 448, kTmemCols = 512;
+constexpr int kStep = 64;                       // query rows of a step
+// Tensor memory: each group's S^T and dP^T (lane = key, column = row), dK, dV,
+// and each group's P^T and dS^T as packed bf16.
+constexpr int kColDK = 256, kColDV = 320, kTmemCols = 512;
+__device__ __forceinline__ constexpr int col_s(int b) { return 128 * b; }
+__device__ __forceinline__ constexpr int col_dp(int b) { return 128 * b + 64; }
+__device__ __forceinline__ constexpr int col_p(int b) { return 384 + 64 * b; }
+__device__ __forceinline__ constexpr int col_ds(int b) { return 416 + 64 * b; }
+constexpr int kStepBytes = kStep * kDh * 2;     // 8 KiB
 constexpr int kKeyTileBytes = kKeys * kDh * 2;  // 16 KiB
-constexpr int kKOff = 0, kVOff = kKeyTileBytes, kStageOff = 2 * kKeyTileBytes;
-constexpr int kStageBytes = 2 * kQTileBytes;    // Q at +0, dout at +kQTileBytes
-constexpr int kStages = 4;
-// Each softmax warp's 32 (lse, D) of the step's rows: lse2 negated, then -D.
-constexpr int kRowOff = kStageOff + kStages * kStageBytes;
-constexpr int kRowBytes = 64 * 4;
-constexpr int kBarOff = kRowOff + kSoftmaxWarps * kRowBytes;
-// barriers: full[S], empty[S], kvfull, o_final, s_full, s_free, p_full, p_free, drain[2]
-constexpr int kNumBars = 2 * kStages + 8;
+// Three planes of 128 rows x 8 elements: (1, 1, 1, 0, ..), zeros, (1, 1, 1, 0, ..).
+constexpr int kPlaneBytes = kKeys * 16, kOnesOff = 0;
+constexpr int kStageOff = 3 * kPlaneBytes;
+// Q at +0, dout at +kStepBytes, then the rows' terms: planes of -lse / scale and -D.
+constexpr int kTermBytes = kStep * 16, kTermsAt = 2 * kStepBytes;
+constexpr int kStageBytes = 2 * kStepBytes + 2 * kTermBytes;
+constexpr int kStages = 8;
+constexpr int kKOff = kStageOff + kStages * kStageBytes, kVOff = kKOff + kKeyTileBytes;
+static_assert(kStageOff % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles");
+constexpr int kBarOff = kVOff + kKeyTileBytes;
+// barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2]
+constexpr int kNumBars = 2 * kStages + 12;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kTileOff = kCtlOff + 32;
 constexpr int kRedoOff = kTileOff + 64;         // one byte per key row
 constexpr int kSmemBytes = kRedoOff + kKeys + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kKeys, kRowsPerTile, false);      // S^T, dP^T: N = 128 rows
+constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kKeys, kStep, false);             // S^T, dP^T: N = 64 rows
 constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32(kKeys, kDh, true);               // dK, dV: B MN-major
 
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Win w,
-                     int key_grid) {
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmT, const Win w, int key_grid) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -437,16 +462,19 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
   const uint32_t kvfull = bar0 + 8 * (2 * kStages);
-  const uint32_t o_final = kvfull + 8, s_full = kvfull + 16, s_free = kvfull + 24, p_full = kvfull + 32,
-                 p_free = kvfull + 40;
-  auto drain = [&](int i) { return kvfull + 48 + 8 * i; };
+  const uint32_t o_final = kvfull + 8;
+  auto s_full = [&](int b) { return kvfull + 16 + 8 * b; };
+  auto s_free = [&](int b) { return kvfull + 32 + 8 * b; };
+  auto p_full = [&](int b) { return kvfull + 48 + 8 * b; };
+  auto p_free = [&](int b) { return kvfull + 64 + 8 * b; };
+  auto drain = [&](int i) { return kvfull + 80 + 8 * i; };
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
   Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
   int* found_slot = reinterpret_cast<int*>(tile_slot + 1);      // 0: none, 1: one, 2: wrong offsets
   volatile uint8_t* redo = smem + kRedoOff;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
-  const int tokens = kRowsPerTile >> w.gshift;
+  const int tokens = kStep >> w.gshift;
   const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
   const int x = far ? blockIdx.x - key_grid : blockIdx.x;
 
@@ -465,11 +493,13 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::mbar_init(empty(s), 1);
     }
     ptx::mbar_init(kvfull, 1);
-    ptx::mbar_init(s_full, 1);
-    ptx::mbar_init(s_free, kSoftmaxWarps);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(s_full(b), 1);
+      ptx::mbar_init(s_free(b), kSoftmaxWarps / 2);
+      ptx::mbar_init(p_full(b), kSoftmaxWarps / 2);
+      ptx::mbar_init(p_free(b), 1);
+    }
     ptx::mbar_init(o_final, 1);
-    ptx::mbar_init(p_full, kSoftmaxWarps);
-    ptx::mbar_init(p_free, 1);
     ptx::mbar_init(drain(0), 1);
     ptx::mbar_init(drain(1), 1);
     ctl->abort = 0;
@@ -477,7 +507,14 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     ctl->limit_ns = w.wait_ns;
     ptx::fence_mbar_init();
   }
-  if (threadIdx.x < kKeys) redo[threadIdx.x] = 0;
+  if (threadIdx.x < kKeys) {
+    redo[threadIdx.x] = 0;
+    const uint32_t at = sbase + kOnesOff + 16 * threadIdx.x;
+    ptx::st_shared_v4(at, 0x3f803f80u, 0x3f80u, 0u, 0u);
+    ptx::st_shared_v4(at + kPlaneBytes, 0u, 0u, 0u, 0u);
+    ptx::st_shared_v4(at + 2 * kPlaneBytes, 0x3f803f80u, 0x3f80u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
   __syncthreads();
   if (*found_slot != 1) {
     if (!far && *found_slot == 0 && w.zero_outside && blockIdx.y == 0) {
@@ -500,8 +537,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const int j0 = far ? 0 : s.t * kKeys, j1 = min(s.lk, j0 + kKeys) - 1;
   int ra, rb;
   if (far) {
-    ra = far_begin<kKeys>(w, s.lq, s.lk) + s.t * far_steps<kRowsPerTile> * tokens;
-    rb = min(s.lq, ra + far_steps<kRowsPerTile> * tokens) - 1;
+    ra = far_begin<kKeys>(w, s.lq, s.lk) + s.t * far_rows<kRowsPerTile>(w);
+    rb = min(s.lq, ra + far_rows<kRowsPerTile>(w)) - 1;
   } else {
     ra = max(0, j0 - shift);
     rb = s.lq - 1;
@@ -517,6 +554,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::tma_prefetch(&tmO);
       ptx::tma_prefetch(&tmK);
       ptx::tma_prefetch(&tmV);
+      ptx::tma_prefetch(&tmT);
       ptx::mbar_expect_tx(kvfull, 2 * kKeyTileBytes);
       ptx::tma_load_3d(sbase + kKOff, &tmK, 0, g, s.k0 + j0, kvfull);
       ptx::tma_load_3d(sbase + kVOff, &tmV, 0, g, s.k0 + j0, kvfull);
@@ -530,7 +568,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         const int tok0 = s.q0 + ra + t * tokens;
         ptx::mbar_expect_tx(full(st), kStageBytes);
         ptx::tma_load_4d(dst, &tmQ, 0, 0, g, tok0, full(st));
-        ptx::tma_load_4d(dst + kQTileBytes, &tmO, 0, 0, g, tok0, full(st));
+        ptx::tma_load_4d(dst + kStepBytes, &tmO, 0, 0, g, tok0, full(st));
+        ptx::tma_load_5d(dst + kTermsAt, &tmT, 0, 0, g, tok0, 0, full(st));
         issued = t + 1;
       }
       ctl->issued = issued;
@@ -538,32 +577,35 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     if (nsteps > 0 && ptx::elect_one()) {
-      const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDK = tmem + kColDK, tDV = tmem + kColDV;
+      const uint32_t tDK = tmem + kColDK, tDV = tmem + kColDV;
       auto issue_sdp = [&](int t) {
         const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
-        const uint32_t oaddr = qaddr + kQTileBytes;
+        const uint32_t oaddr = qaddr + kStepBytes, ones = sbase + kOnesOff;
+        const uint64_t terms = ptx::smem_desc_plain(qaddr + kTermsAt, kTermBytes, 128);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024),
+          ptx::mma_ss(tmem + col_s(t & 1), ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(qaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
+        ptx::mma_ss(tmem + col_s(t & 1), ptx::smem_desc_plain(ones, kPlaneBytes, 128), terms, kIdescS, 1u);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tDP, ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024),
+          ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
-        ptx::tc_commit(s_full);
+        ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_plain(ones + kPlaneBytes, kPlaneBytes, 128), terms, kIdescS, 1u);
+        ptx::tc_commit(s_full(t & 1));
       };
       auto issue_dkv = [&](int t) {
         const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
-        const uint32_t oaddr = qaddr + kQTileBytes;
+        const uint32_t oaddr = qaddr + kStepBytes;
 #pragma unroll
-        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-          ptx::mma_ts(tDK, tmem + kColDS + kk * 8, ptx::smem_desc_sw128(qaddr + kk * 2048, 8192, 1024), kIdescKV,
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          ptx::mma_ts(tDK, tmem + col_ds(t & 1) + kk * 8, ptx::smem_desc_sw128(qaddr + kk * 2048, 8192, 1024), kIdescKV,
                       (t > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < kRowsPerTile / 16; ++kk)
-          ptx::mma_ts(tDV, tmem + kColP + kk * 8, ptx::smem_desc_sw128(oaddr + kk * 2048, 8192, 1024), kIdescKV,
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          ptx::mma_ts(tDV, tmem + col_p(t & 1) + kk * 8, ptx::smem_desc_sw128(oaddr + kk * 2048, 8192, 1024), kIdescKV,
                       (t > 0 || kk > 0) ? 1u : 0u);
-        ptx::tc_commit(p_free);
+        ptx::tc_commit(p_free(t & 1));
         ptx::tc_commit(empty(t % kStages));
         if (t == nsteps - 1) ptx::tc_commit(o_final);
       };
@@ -573,14 +615,14 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
           if (!(ok = wait(full(t % kStages), (t / kStages) & 1))) break;
-          if (t > 0 && !(ok = wait(s_free, (t - 1) & 1))) break;
+          if (t > 1 && !(ok = wait(s_free(t & 1), ((t >> 1) - 1) & 1))) break;
           ptx::tc_fence_after();
           issue_sdp(t);
         }
       } else {
 #pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
-          if (!(ok = wait(p_full, t & 1))) break;
+          if (!(ok = wait(p_full(t & 1), (t >> 1) & 1))) break;
           ptx::tc_fence_after();
           issue_dkv(t);
         }
@@ -589,7 +631,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     __syncwarp();
   } else {
     // ---------------- softmax warps: thread = key of the tile ----------------
-    const int c = warp >> 2;                     // 32-row chunk of the step
+    const int group = warp >> 3;                 // of the even or of the odd steps
+    const int c = (warp >> 2) & 1;               // 32-row chunk of the step
     const int lane_base = (warp & 3) * 32;
     const int rl = lane_base + lane;             // key inside the tile
     const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
@@ -598,59 +641,34 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const int j = j0 + rl;
     const int ka = far && j >= w.sinks ? rb + 1 : max(ra, j - shift);
     const int kb = w.window > 0 && j >= w.sinks ? min(rb, j + w.window - 1 - shift) + 1 : rb + 1;
-    // Row 32 c + lane of a step: -lse in base 2 and -D, or zeros where no key sees it.
-    const int h = (g << w.gshift) + (lane & (w.G - 1));
-    float* rows = reinterpret_cast<float*>(smem + kRowOff + warp * kRowBytes);
-    auto load_row = [&](int t, float& nl, float& nd) {
-      const int r = ra + t * tokens + ((32 * c + lane) >> w.gshift);
-      nl = nd = 0.f;
-      if (r <= rb && r + shift >= 0) {
-        const size_t orow = (size_t)(s.q0 + r) * w.Hq + h;
-        nl = -__ldg(w.lse + orow) * kLog2e;
-        nd = -__ldg(w.delta + orow);
-      }
-    };
-    float nl, nd;
-    load_row(0, nl, nd);
     bool ok = true;
+    const uint32_t tsd = trow + 128 * group + 32 * c, tp = trow + 384 + 64 * group + 16 * c;
+    const uint32_t s_full_g = s_full(group), s_free_g = s_free(group), p_full_g = p_full(group), p_free_g = p_free(group);
+    uint32_t phase = 0;
 #pragma unroll 1
-    for (int t = 0; t < nsteps; ++t) {
-      __syncwarp();
-      rows[lane] = nl;
-      rows[32 + lane] = nd;
-      __syncwarp();
-      load_row(t + 1, nl, nd);
+    for (int t = group; t < nsteps; t += 2, phase ^= 1) {
       // Bit k: row 32 c + k of the step sees the key.
       const int rs = ra + t * tokens;
       const int x0 = (min(max(ka - rs, 0), tokens) << w.gshift) - 32 * c;
       const int x1 = (min(max(kb - rs, 0), tokens) << w.gshift) - 32 * c;
       const uint32_t see = (x0 >= 32 ? 0u : 0xffffffffu << max(x0, 0)) & (x1 >= 32 ? 0xffffffffu : (1u << max(x1, 0)) - 1u);
       const bool some = __any_sync(0xffffffffu, see != 0u), whole = __all_sync(0xffffffffu, see == 0xffffffffu);
-      if (!(ok = __all_sync(0xffffffffu, wait(s_full, t & 1)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full_g, phase)))) break;
       ptx::tc_fence_after();
       uint32_t pd[16], pp[16];
       if (some) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t sv[16], dv[16];
-          ptx::tmem_ld16x2_sync(trow + kColS + 32 * c + 16 * q, trow + kColDP + 32 * c + 16 * q, sv, dv);
-          if (q == 1) warp_arrive(s_free);
+          ptx::tmem_ld16x2_sync(tsd + 16 * q, tsd + 64 + 16 * q, sv, dv);
+          if (q == 1) warp_arrive(s_free_g);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 l4 = reinterpret_cast<const float4*>(rows)[4 * q + k];
-            const float4 d4 = reinterpret_cast<const float4*>(rows + 32)[4 * q + k];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 4 * k + 2 * e;
-              const float2 xx = __ffma2_rn(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2,
-                                           e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y));
-              const float2 tt = __fadd2_rn(make_float2(__uint_as_float(dv[i]), __uint_as_float(dv[i + 1])),
-                                           e ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y));
-              const float2 pr = make_float2(ptx::ex2(xx.x), ptx::ex2(xx.y));
-              const float2 ds = __fmul2_rn(pr, tt);
-              pd[8 * q + 2 * k + e] = pack_bf16x2(ds.x, ds.y);
-              pp[8 * q + 2 * k + e] = pack_bf16x2(pr.x, pr.y);
-            }
+          for (int k = 0; k < 8; ++k) {
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), c2);
+            const float2 pr = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+            const float2 ds = __fmul2_rn(pr, make_float2(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])));
+            pd[8 * q + k] = pack_bf16x2(ds.x, ds.y);
+            pp[8 * q + k] = pack_bf16x2(pr.x, pr.y);
           }
         }
         if (!whole) {
@@ -662,22 +680,22 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           }
         }
       } else {
-        warp_arrive(s_free);
+        warp_arrive(s_free_g);
 #pragma unroll
         for (int k = 0; k < 16; ++k) pd[k] = pp[k] = 0u;
       }
       // The previous step's dK / dV MMAs read P^T and dS^T: wait for them only
       // now, so this step's exponentials overlap them.
-      if (t > 0 && !(ok = __all_sync(0xffffffffu, wait(p_free, (t - 1) & 1)))) break;
-      ptx::tmem_st16(trow + kColDS + 16 * c, pd);
-      ptx::tmem_st16(trow + kColP + 16 * c, pp);
+      if (t > 1 && !(ok = __all_sync(0xffffffffu, wait(p_free_g, phase ^ 1)))) break;
+      ptx::tmem_st16(tp + 32, pd);
+      ptx::tmem_st16(tp, pp);
       ptx::tmem_wait_st();
-      warp_arrive(p_full);
+      warp_arrive(p_full_g);
     }
     if (nsteps == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
       // Accumulator lane = key of this tile.  The warpgroups share the 128
       // accumulator columns (dK 64, then dV 64): 32 each.
-      const int col0 = 32 * c;
+      const int col0 = 32 * (warp >> 2);
       const bool is_k = col0 < kDh;
       uint32_t o[32];
       if (nsteps > 0) {
@@ -748,6 +766,15 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 }  // namespace k_side
+
+// Win::terms viewed as [2][Tq][Hkv][G][8]: boxes of both planes of a step's rows.
+inline bool map_terms(CUtensorMap* m, const Win& w) {
+  const cuuint64_t dims[5] = {8, (cuuint64_t)w.G, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tq, 2};
+  const cuuint64_t strides[4] = {16, (cuuint64_t)w.G * 16, (cuuint64_t)w.Hq * 16, (cuuint64_t)w.Tq * w.Hq * 16};
+  const cuuint32_t box[5] = {8, (cuuint32_t)w.G, 1, (cuuint32_t)(k_side::kStep / w.G), 2};
+  return tma::encode_bf16(m, w.terms, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 }  // namespace
 
 cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
@@ -759,10 +786,11 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
     e = cudaFuncSetAttribute(k_side::window_dkv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              k_side::kSmemBytes);
   if (e != cudaSuccess) return e;
-  CUtensorMap tq, to, tk, tv, tk128, tv128;
+  CUtensorMap tq, to, tk, tv, tk128, tv128, tq64, to64, tt;
   if (!map_query_rows(&tq, w, w.q) || !map_query_rows(&to, w, w.dout) || !map_key_rows(&tk, w, w.k, 32) ||
       !map_key_rows(&tv, w, w.v, 32) || !map_key_rows(&tk128, w, w.k, k_side::kKeys) ||
-      !map_key_rows(&tv128, w, w.v, k_side::kKeys))
+      !map_key_rows(&tv128, w, w.v, k_side::kKeys) || !map_query_rows(&tq64, w, w.q, k_side::kStep) ||
+      !map_query_rows(&to64, w, w.dout, k_side::kStep) || !map_terms(&tt, w))
     return cudaErrorInvalidValue;
   const dim3 gq((unsigned)tile_grid(w.Tq, kRowsPerTile >> w.gshift, w.B), w.Hkv);
   q_side::window_dq_tc_kernel<<<gq, q_side::kThreads, q_side::kSmemBytes, st>>>(tq, to, tk, tv, w);
@@ -770,7 +798,8 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int key_grid = (int)tile_grid(w.Tk, k_side::kKeys, w.B);
   const dim3 gk((unsigned)(key_grid + far_grid<kRowsPerTile>(w)), w.Hkv);
-  k_side::window_dkv_tc_kernel<<<gk, k_side::kThreads, k_side::kSmemBytes, st>>>(tq, to, tk128, tv128, w, key_grid);
+  k_side::window_dkv_tc_kernel<<<gk, k_side::kThreads, k_side::kSmemBytes, st>>>(tq64, to64, tk128, tv128, tt, w,
+                                                                                key_grid);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_window_sinks<__nv_bfloat16, k_side::kKeys, kRowsPerTile>(w, st);

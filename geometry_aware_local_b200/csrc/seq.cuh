@@ -31,6 +31,7 @@ struct Win {
   void* dk;
   void* dv;
   float* delta;                   // workspace [Tq, Hq]: <dout, out>, the row's sum of P dP
+  void* terms;                    // workspace, bf16 [2][Tq, Hq, 8]: -lse / scale, then -delta, in three pieces
   float* part;                    // workspace: partial gradients of the sink rows
   int zero_outside;               // rows of no sequence become 0 instead of staying as they were
   int32_t* err;

@@ -94,10 +94,13 @@ seq::Cache make_cache(const pack3d_seq_config& c, int32_t batch, const int32_t* 
   return r;
 }
 
-// The backward's workspace: Win::delta, then Win::part.
+// The backward's workspace: Win::delta, in bf16 Win::terms, then Win::part.
 size_t delta_bytes(const seq::Win& w) { return ((size_t)w.Tq * w.Hq * 4 + 1023) / 1024 * 1024; }
+size_t terms_bytes(const seq::Win& w, int dtype) {
+  return dtype == PACK3D_BF16 ? ((size_t)w.Tq * w.Hq * 32 + 1023) / 1024 * 1024 : 0;
+}
 size_t bwd_bytes(const seq::Win& w, int dtype) {
-  return delta_bytes(w) + (seq::window_bwd_part_bytes(w, dtype) + 1023) / 1024 * 1024;
+  return delta_bytes(w) + terms_bytes(w, dtype) + (seq::window_bwd_part_bytes(w, dtype) + 1023) / 1024 * 1024;
 }
 
 }  // namespace
@@ -189,7 +192,8 @@ pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config* cfg, int32_t batch
   w.dk = dk;
   w.dv = dv;
   w.delta = (float*)workspace;
-  w.part = (float*)((char*)workspace + delta_bytes(w));
+  w.terms = (char*)workspace + delta_bytes(w);
+  w.part = (float*)((char*)w.terms + terms_bytes(w, cfg->dtype));
   w.zero_outside = zero_outside != 0;
   w.err = err_word;
   return cuda_status(seq::launch_window_bwd(w, cfg->dtype, (cudaStream_t)stream));

@@ -70,12 +70,12 @@ __device__ __forceinline__ uint32_t visible_bits(const Win& w, int p, int low, i
   return upto & ((a >= 32 ? 0u : 0xffffffffu << a) | sink);
 }
 
-// Query-shaped tensor [Tq][Hq][64] viewed as [Tq][Hkv][G][64]: a box of 128/G
-// tokens x G heads x 64 dims of one key head is one 128-row tile.
-inline bool map_query_rows(CUtensorMap* m, const Win& w, const void* base) {
+// Query-shaped tensor [Tq][Hq][64] viewed as [Tq][Hkv][G][64]: a box of rows/G
+// tokens x G heads x 64 dims of one key head is one tile of `rows` rows.
+inline bool map_query_rows(CUtensorMap* m, const Win& w, const void* base, int rows = kRowsPerTile) {
   const cuuint64_t dims[4] = {(cuuint64_t)kDh, (cuuint64_t)w.G, (cuuint64_t)w.Hkv, (cuuint64_t)w.Tq};
   const cuuint64_t strides[3] = {(cuuint64_t)kDh * 2, (cuuint64_t)w.G * kDh * 2, (cuuint64_t)w.Hq * kDh * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)kDh, (cuuint32_t)w.G, 1, (cuuint32_t)(kRowsPerTile / w.G)};
+  const cuuint32_t box[4] = {(cuuint32_t)kDh, (cuuint32_t)w.G, 1, (cuuint32_t)(rows / w.G)};
   return tma::encode_bf16_sw128(m, base, 4, dims, strides, box);
 }
 

@@ -1,4 +1,4 @@
-// Host-side TMA tensor-map encoding for the tcgen05 kernels: bf16 tiles with
+// Host-side TMA tensor-map encoding for the tcgen05 kernels: bf16 tiles, most with
 // 128-byte swizzle, out-of-bounds boxes zero-filled.  cuTensorMapEncodeTiled
 // is reached through the runtime's driver entry point (no libcuda link).
 #pragma once
@@ -26,14 +26,18 @@ inline EncodeTiledFn encode_fn() {
 }
 
 // rank-dimensional bf16 map: dims innermost first, strides in bytes of dims 1..rank-1.
-inline bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-                              const cuuint64_t* strides, const cuuint32_t* box) {
+inline bool encode_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                        const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                              const cuuint64_t* strides, const cuuint32_t* box) {
+  return encode_bf16(m, base, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace tma
