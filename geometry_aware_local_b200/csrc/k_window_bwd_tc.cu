@@ -546,7 +546,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   }
   const int nsteps = rb >= ra ? (rb - ra) / tokens + 1 : 0;
   // Rows below `split_rows` of this tile leave float partial sums.
-  const int split_rows = far || (j0 == 0 && far_pieces<kKeys, kRowsPerTile>(w, s.lq, s.lk) > 0) ? min(w.sinks, s.lk) : 0;
+  const bool shared = far || (j0 == 0 && far_pieces<kKeys, kRowsPerTile>(w, s.lq, s.lk) > 0);
+  const int split_rows = shared ? min(w.sinks, s.lk) : 0;
 
   if (warp == kTmaWarp) {
     if (lane == 0 && nsteps > 0) {
@@ -591,7 +592,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         for (int kk = 0; kk < kDh / 16; ++kk)
           ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
-        ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_plain(ones + kPlaneBytes, kPlaneBytes, 128), terms, kIdescS, 1u);
+        ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_plain(ones + kPlaneBytes, kPlaneBytes, 128), terms, kIdescS,
+                    1u);
         ptx::tc_commit(s_full(t & 1));
       };
       auto issue_dkv = [&](int t) {
@@ -642,8 +644,9 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const int ka = far && j >= w.sinks ? rb + 1 : max(ra, j - shift);
     const int kb = w.window > 0 && j >= w.sinks ? min(rb, j + w.window - 1 - shift) + 1 : rb + 1;
     bool ok = true;
-    const uint32_t tsd = trow + 128 * group + 32 * c, tp = trow + 384 + 64 * group + 16 * c;
-    const uint32_t s_full_g = s_full(group), s_free_g = s_free(group), p_full_g = p_full(group), p_free_g = p_free(group);
+    const uint32_t tsd = trow + col_s(group) + 32 * c, tp = trow + col_p(group) + 16 * c;
+    const uint32_t s_full_g = s_full(group), s_free_g = s_free(group);
+    const uint32_t p_full_g = p_full(group), p_free_g = p_free(group);
     uint32_t phase = 0;
 #pragma unroll 1
     for (int t = group; t < nsteps; t += 2, phase ^= 1) {
@@ -651,7 +654,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int rs = ra + t * tokens;
       const int x0 = (min(max(ka - rs, 0), tokens) << w.gshift) - 32 * c;
       const int x1 = (min(max(kb - rs, 0), tokens) << w.gshift) - 32 * c;
-      const uint32_t see = (x0 >= 32 ? 0u : 0xffffffffu << max(x0, 0)) & (x1 >= 32 ? 0xffffffffu : (1u << max(x1, 0)) - 1u);
+      const uint32_t from = x0 >= 32 ? 0u : 0xffffffffu << max(x0, 0);
+      const uint32_t see = from & (x1 >= 32 ? 0xffffffffu : (1u << max(x1, 0)) - 1u);
       const bool some = __any_sync(0xffffffffu, see != 0u), whole = __all_sync(0xffffffffu, see == 0xffffffffu);
       if (!(ok = __all_sync(0xffffffffu, wait(s_full_g, phase)))) break;
       ptx::tc_fence_after();
@@ -686,7 +690,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       }
       // The previous step's dK / dV MMAs read P^T and dS^T: wait for them only
       // now, so this step's exponentials overlap them.
-      if (t > 1 && !(ok = __all_sync(0xffffffffu, wait(p_free_g, phase ^ 1)))) break;
+      if (t > 1) {
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free_g, phase ^ 1)))) break;
+        ptx::tc_fence_after();
+      }
       ptx::tmem_st16(tp + 32, pd);
       ptx::tmem_st16(tp, pp);
       ptx::tmem_wait_st();

@@ -117,8 +117,8 @@ __device__ __forceinline__ bool find_piece(const Win& w, int x, int per, bool ov
 // tile; every sequence starts a new one.  The query tiles' first CTAs look at
 // all offsets between them.
 __device__ __forceinline__ bool find_tile(const Win& w, int x, int per, bool over_keys, Tile* out, bool* bad) {
-  const bool found =
-      find_piece(w, x, per, over_keys, [=](int lq, int lk) { return ((over_keys ? lk : lq) + per - 1) / per; }, out, bad);
+  auto count = [=](int lq, int lk) { return ((over_keys ? lk : lq) + per - 1) / per; };
+  const bool found = find_piece(w, x, per, over_keys, count, out, bad);
   if (over_keys || w.B <= 32 || x > w.B / 32) return found;
   const int b = 32 * x + (threadIdx.x & 31);
   *bad |= __any_sync(0xffffffffu, b < w.B && off_range(w, b));
