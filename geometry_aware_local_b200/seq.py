@@ -28,6 +28,8 @@ from typing import Optional
 
 from . import BF16, F32, Pack3DError, check_status, lib
 
+ERR_WORKSPACE = 6     # PACK3D_ERR_WORKSPACE
+
 DH = 64
 
 
@@ -116,6 +118,18 @@ def _torch():
     return _modules[0]
 
 
+_templates = {}
+
+
+def _new(device, dtype, *shape):
+    """torch.empty, from an empty tensor of the device and type: it takes half as long as naming both."""
+    key = device.index, dtype
+    t = _templates.get(key)
+    if t is None:
+        t = _templates[key] = _torch()[0].empty(0, dtype=dtype, device=device)
+    return t.new_empty(*shape)
+
+
 def _check_err_word(what, err, device, torch):
     if err is not None and (err.dtype != torch.int32 or err.numel() < 1 or err.device != device):
         raise ValueError(f"{what}: the error word must be an int32 tensor of at least one element on {device}")
@@ -141,17 +155,21 @@ def _raw_stream(device):
     return _modules[0][0]._C._cuda_getCurrentRawStream(device.index)
 
 
-def _call(torch, what, fn, device, stream, *args):
-    """Runs a C entry point on `stream` (the device's current one by default) with the tensors' device current."""
+def _run(torch, fn, device, stream, *args):
+    """Runs a C entry point on `stream` (the device's current one by default) with the tensors' device current, and
+    returns its status."""
     if stream is None:
         stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream)
+        return fn(*args, stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream)
+
+
+def _call(torch, what, fn, device, stream, *args):
+    st = _run(torch, fn, device, stream, *args)
     if st != 0:
         raise Pack3DError(st, what)
 
@@ -189,7 +207,7 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
     new = out is None
     if new:
         out = torch.empty_like(q)
-        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+        lse = _new(dev, torch.float32, q.shape[0], cfg.Hq)
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
             return out.zero_(), lse.fill_(-math.inf)
     else:
@@ -229,7 +247,7 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
             _require(what, cfg, name, t, T, tuple(like.shape), dev)
     if workspace is None:
         n = window_attn_bwd_workspace_bytes(cfg, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        workspace = _new(dev, torch.uint8, max(n, 256))
     else:
         _check_workspace(what, workspace, dev)
     _check_err_word(what, err, dev, torch)
@@ -333,22 +351,26 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     else:
         _require(what, cfg, "out", out, T, tuple(q.shape), dev)
     if lse is None:
-        lse = q.new_empty((batch, cfg.Hq), dtype=torch.float32)
+        lse = _new(dev, torch.float32, batch, cfg.Hq)
     else:
         _require(what, cfg, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
     if weights is not None:
         _require(what, cfg, "weights", weights, torch.float32, (batch, max_pages * cfg.page), dev)
-    if workspace is None:
-        n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    else:
+    n = 0
+    if workspace is not None:
         _check_workspace(what, workspace, dev)
         n = workspace.numel() * workspace.element_size()
     _check_err_word(what, err, dev, torch)
-    _call(torch, what, lib.pack3d_cache_attn, dev, stream, ctypes.byref(cfg), batch, q.data_ptr(),
-          k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), max_pages, k_pages.shape[0], lengths.data_ptr(),
-          out.data_ptr(), lse.data_ptr(), _p(weights), int(bool(accumulate)), _p(workspace), n, _p(err))
+    args = (ctypes.byref(cfg), batch, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
+            max_pages, k_pages.shape[0], lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), _p(weights),
+            int(bool(accumulate)))
+    st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, _p(workspace), n, _p(err))
+    if st == ERR_WORKSPACE and workspace is None:      # short calls need none: ask only when told so
+        n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
+        workspace = _new(dev, torch.uint8, n)
+        st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, workspace.data_ptr(), n, _p(err))
+    if st != 0:
+        raise Pack3DError(st, what)
     return out, lse
 
 
@@ -371,7 +393,7 @@ def cache_evict(cfg: SeqConfig, k_pages, v_pages, table, lengths, weights, new_t
     for name, t, dt, shape in (("kept", kept, torch.int32, shapes[0]), ("new_weights", new_weights, torch.float32,
                                shapes[1]), ("new_lengths", new_lengths, torch.int32, shapes[2])):
         if t is None:
-            t = torch.empty(shape, dtype=dt, device=dev)
+            t = _new(dev, dt, *shape)
         else:
             _require(what, cfg, name, t, dt, shape, dev)
         outs.append(t)
