@@ -6,11 +6,14 @@
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dout.
 //
 // window_dq_tc_kernel: one 128-row query tile of one key head per CTA (rows,
-//   key range and sinks as in the forward), 64 keys a step, two CTAs per SM.
-//   S and dP go to tensor memory (N = the step's columns, K = 64); the softmax
-//   warps (thread = row) write dS as packed bf16 into tensor memory; dQ += dS K
-//   with the same K tile read MN-major.  It also forms D of its rows and
-//   leaves it for the second kernel.
+//   key range and sinks as in the forward), 32 keys a step, two CTAs per SM.
+//   One MMA warp issues S and dP into tensor memory (N = 32 keys, K = 64); two
+//   groups of four softmax warps (thread = row) take every other step, each with
+//   its own tensor memory, and write dS there as packed bf16; a second MMA warp
+//   issues dQ += dS K with the same K tile read MN-major.  It also forms D of its
+//   rows and leaves it for the second kernel.  (65,536 tokens, window 1,024, both
+//   kernels: one group and 64 keys a step 0.748 ms, two warps a row quarter on the
+//   same step 0.751, now 0.711.)
 //
 // window_dkv_tc_kernel: one 128-key tile of one key head per CTA and the
 //   queries whose window reaches it, 64 rows a step, one CTA per SM.  S^T and
@@ -36,8 +39,8 @@
 // the tile itself leave float partial sums of the sink rows; window_sinks_kernel
 // adds them in a fixed order.  No atomics: the same inputs give the same bits.
 //
-// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.748 ms, 459 TFLOP/s (five
-// products), about 0.37 ms of it the query side.  As in the forward the pace is
+// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.711 ms, 483 TFLOP/s (five
+// products), about 0.33 ms of it the query side.  As in the forward the pace is
 // that of the softmax warps' chains (load, exponentials, store, arrive), not of
 // the tensor cores.
 //
@@ -68,25 +71,45 @@ __device__ __forceinline__ void write_terms(const Win& w, int plane, size_t orow
       make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(x - hi - mid, 0.f), 0u, 0u);
 }
 
+// The halves of a bf16 pair that bits 2 k and 2 k + 1 of `see` keep.
+__device__ __forceinline__ uint32_t kept_pair(uint32_t see, int k) {
+  return ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+}
+
 // ============================================================================
 // Query side
 // ============================================================================
 namespace q_side {
 
-constexpr int kBN = 64;
-constexpr int kThreads = 192;                   // 4 softmax warps, MMA warp, TMA warp
-constexpr int kMmaWarp = 4, kTmaWarp = 5;
-constexpr int kColS = 0, kColDP = kBN, kColDS = 2 * kBN, kColDQ = 2 * kBN + kBN / 2, kTmemCols = 256;
+constexpr int kBN = 32;
+// The key tiles of a query tile, as in the forward but of 32 columns: the sinks'
+// (up to two) in front.
+struct SmallTiles {
+  int lo, sink_tiles, n;
+  __device__ __forceinline__ int begin(int j) const { return j < sink_tiles ? j * kBN : lo + (j - sink_tiles) * kBN; }
+};
+__device__ __forceinline__ SmallTiles small_tiles(const Win& w, int p0, int p1) {
+  const KeyTiles<2 * kBN> k = key_tiles<2 * kBN>(w, p0, p1);      // a tile holds every sink
+  const int sink_tiles = k.sink_cols / kBN;
+  return SmallTiles{k.lo, sink_tiles, p1 < 0 ? 0 : (k.hi - k.lo) / kBN + 1 + sink_tiles};
+}
+// Two groups of softmax warps on alternate steps; two MMA warps; TMA warp.
+constexpr int kSoftmaxWarps = 8, kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kMmaWarp = kSoftmaxWarps, kMmaWarp2 = kSoftmaxWarps + 1, kTmaWarp = kSoftmaxWarps + 2;
+// Group b's S, dP and dS (packed bf16) at 80 b, + 32, + 64.
+constexpr int kGroupCols = 2 * kBN + kBN / 2, kColDQ = 2 * kGroupCols, kTmemCols = 256;
 static_assert(kColDQ + kDh <= kTmemCols, "tensor memory plan");
-constexpr int kKVBytes = kBN * kDh * 2;         // 8 KiB
-constexpr int kStages = 4;
+constexpr int kKVBytes = kBN * kDh * 2;         // 4 KiB
+constexpr int kStages = 8;
 constexpr int kQOff = 0, kDOOff = kQTileBytes, kStageOff = 2 * kQTileBytes;
 constexpr int kStageBytes = 2 * kKVBytes;       // K at +0, V at +kKVBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, s_full, s_free, p_full, p_free, o_final, drain
-constexpr int kNumBars = 2 * kStages + 7;
+// barriers: full[S], empty[S], qfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2]
+constexpr int kNumBars = 2 * kStages + 12;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
-constexpr int kSmemBytes = kCtlOff + 32 + 1024;
+constexpr int kHalfOff = kCtlOff + 32;          // float [2][128]: the groups' shares of D
+constexpr int kRedoOff = kHalfOff + 2 * kRowsPerTile * 4;       // one byte per row
+constexpr int kSmemBytes = kRedoOff + kRowsPerTile + 1024;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 // Row tiles of at most this many key tiles form D from P and dP in a first pass
 // over them.  <dout, out> of the rounded out is off by 2^-9 of its terms, which
@@ -95,8 +118,9 @@ static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 // it averages out.  The tiles stay in shared memory for the second pass, so
 // the first costs two products and the exponentials, and saves the reads of out
 // and dout by rows (65,536 tokens, window 65: 0.365 -> 0.349 ms).
-constexpr int kTwice = 3;
+constexpr int kTwice = 6;
 static_assert(kTwice <= kStages, "the first pass's tiles stay");
+constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRowsPerTile, kBN, false);
 constexpr uint32_t kIdescDQ = ptx::idesc_bf16_f32(kRowsPerTile, kDh, true);  // dQ: N = 64 dims, K MN-major
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -111,8 +135,14 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
   const uint32_t qfull = bar0 + 8 * (2 * kStages);
-  const uint32_t s_full = qfull + 8, s_free = qfull + 16, p_full = qfull + 24, p_free = qfull + 32,
-                 o_final = qfull + 40, drain = qfull + 48;
+  const uint32_t o_final = qfull + 8;
+  auto s_full = [&](int b) { return qfull + 16 + 8 * b; };
+  auto s_free = [&](int b) { return qfull + 32 + 8 * b; };
+  auto p_full = [&](int b) { return qfull + 48 + 8 * b; };
+  auto p_free = [&](int b) { return qfull + 64 + 8 * b; };
+  auto drain = [&](int i) { return qfull + 80 + 8 * i; };
+  float* shares = reinterpret_cast<float*>(smem + kHalfOff);
+  volatile uint8_t* redo = smem + kRedoOff;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
@@ -130,12 +160,14 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ptx::mbar_init(empty(s), 1);
     }
     ptx::mbar_init(qfull, 1);
-    ptx::mbar_init(s_full, 1);
-    ptx::mbar_init(s_free, 4);
-    ptx::mbar_init(p_full, 4);
-    ptx::mbar_init(p_free, 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(s_full(b), 1);
+      ptx::mbar_init(s_free(b), 4);
+      ptx::mbar_init(p_full(b), 4);
+      ptx::mbar_init(p_free(b), 1);
+      ptx::mbar_init(drain(b), 1);
+    }
     ptx::mbar_init(o_final, 1);
-    ptx::mbar_init(drain, 1);
     ctl->abort = 0;
     ctl->issued = 0;
     ctl->limit_ns = w.wait_ns;
@@ -155,19 +187,15 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   s.t = s.n - 1 - s.t;      // the tiles with most keys first
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const int p0 = position(s, r0), p1 = position(s, r1);
-  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
+  const SmallTiles kt = small_tiles(w, p0, p1);
   const int T = kt.n, T_load = w.stall ? T - 1 : T;
   const int first = T <= kTwice ? T : 0;      // steps of the first pass
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
-    const int cols = kt.cols(j), row = s.k0 + kt.begin(j);
-    ptx::mbar_expect_tx(full(st), 2 * (cols / 32) * kChunkBytes);
-#pragma unroll 1
-    for (int c = 0; c < cols / 32; ++c) {
-      ptx::tma_load_3d(dst + c * kChunkBytes, &tmK, 0, g, row + 32 * c, full(st));
-      ptx::tma_load_3d(dst + kKVBytes + c * kChunkBytes, &tmV, 0, g, row + 32 * c, full(st));
-    }
+    ptx::mbar_expect_tx(full(st), kStageBytes);
+    ptx::tma_load_3d(dst, &tmK, 0, g, s.k0 + kt.begin(j), full(st));
+    ptx::tma_load_3d(dst + kKVBytes, &tmV, 0, g, s.k0 + kt.begin(j), full(st));
   };
   if (warp == kTmaWarp && lane == 0 && T > 0) {
     ptx::mbar_expect_tx(qfull, 2 * kQTileBytes);
@@ -198,63 +226,59 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ctl->issued = issued;
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     if (T > 0 && ptx::elect_one()) {
-      const uint32_t tS = tmem + kColS, tDP = tmem + kColDP, tDS = tmem + kColDS, tDQ = tmem + kColDQ;
-      auto issue_sdp = [&](int j) {
+      const uint32_t tDQ = tmem + kColDQ;
+      auto issue_sdp = [&](int j, int b) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
         const uint32_t vaddr = kaddr + kKVBytes;
-        const uint32_t idesc = ptx::idesc_bf16_f32(kRowsPerTile, kt.cols(j), false);
+        const uint32_t tS = tmem + kGroupCols * b;
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
           ptx::mma_ss(tS, ptx::smem_desc_sw128(sbase + kQOff + kk * 32, 16, 1024),
-                      ptx::smem_desc_sw128(kaddr + kk * 32, 16, 1024), idesc, kk > 0);
+                      ptx::smem_desc_sw128(kaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
-          ptx::mma_ss(tDP, ptx::smem_desc_sw128(sbase + kDOOff + kk * 32, 16, 1024),
-                      ptx::smem_desc_sw128(vaddr + kk * 32, 16, 1024), idesc, kk > 0);
-        ptx::tc_commit(s_full);
+          ptx::mma_ss(tS + kBN, ptx::smem_desc_sw128(sbase + kDOOff + kk * 32, 16, 1024),
+                      ptx::smem_desc_sw128(vaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
+        ptx::tc_commit(s_full(b));
       };
-      auto issue_dq = [&](int j) {
+      auto issue_dq = [&](int j, int b) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
-        const int cols = kt.cols(j);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          if (kk * 16 < cols)
-            ptx::mma_ts(tDQ, tDS + kk * 8, ptx::smem_desc_sw128(kaddr + kk * 2048, 8192, 1024), kIdescDQ,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-        ptx::tc_commit(p_free);
+          ptx::mma_ts(tDQ, tmem + kGroupCols * b + 2 * kBN + kk * 8,
+                      ptx::smem_desc_sw128(kaddr + kk * 2048, 8192, 1024), kIdescDQ, (j > 0 || kk > 0) ? 1u : 0u);
+        ptx::tc_commit(p_free(b));
         ptx::tc_commit(empty(j % kStages));
         if (j == T - 1) ptx::tc_commit(o_final);
       };
-      bool ok = wait(qfull, 0);
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        ok = wait(qfull, 0);
+        // The first pass's tiles, then all.
 #pragma unroll 1
-      for (int j = 0; ok && j < first; ++j) {
-        if (!(ok = wait(full(j), 0) && (j == 0 || wait(s_free, (j - 1) & 1)))) break;
-        ptx::tc_fence_after();
-        issue_sdp(j);
-      }
-      ok = ok && wait(full(0), 0) && (first == 0 || wait(s_free, (first - 1) & 1));
-      if (ok) {
-        ptx::tc_fence_after();
-        issue_sdp(0);
-      }
-#pragma unroll 1
-      for (int j = 0; ok && j < T; ++j) {
-        if (j + 1 < T) {
-          if (!(ok = wait(s_free, (first + j) & 1) && wait(full((j + 1) % kStages), ((j + 1) / kStages) & 1))) break;
+        for (int u = 0; ok && u < first + T; ++u) {
+          const int j = u < first ? u : u - first;
+          ok = wait(full(j % kStages), (j / kStages) & 1) && (u < 2 || wait(s_free(u & 1), ((u >> 1) - 1) & 1));
+          if (!ok) break;
           ptx::tc_fence_after();
-          issue_sdp(j + 1);
+          issue_sdp(j, u & 1);
         }
-        if (!(ok = wait(p_full, j & 1))) break;
-        ptx::tc_fence_after();
-        issue_dq(j);
+      } else {
+#pragma unroll 1
+        for (int j = 0; ok && j < T; ++j) {
+          const int b = (first + j) & 1;
+          if (!(ok = wait(p_full(b), (j >> 1) & 1))) break;
+          ptx::tc_fence_after();
+          issue_dq(j, b);
+        }
       }
     }
     __syncwarp();
   } else {
-    // ---------------- softmax warps: thread = row = tensor-memory lane ----------------
-    const int lane_base = warp * 32;
+    // ---------------- softmax warps: thread = row (lane of tensor memory) of every other step ----------------
+    const int lane_base = (warp & 3) * 32, group = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
     const int row = lane_base + lane;
     const int r = r0 + (row >> w.gshift);
@@ -263,21 +287,22 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const size_t orow = (size_t)(s.q0 + (valid ? r : r0)) * w.Hq + h;
     const int p = valid ? position(s, r) : -1;
     const int low = window_low(w, p), low_last = window_low(w, p1);
+    if (group == 0) redo[row] = 0;
     // Rows past the sequence see nothing, whatever their lse2 and D are.
-    const float lse2 = valid && p >= 0 ? w.lse[orow] * kLog2e : 0.f;
+    const float lse = valid && p >= 0 ? w.lse[orow] : 0.f, lse2 = lse * kLog2e;
     const float2 c2 = make_float2(w.scale_log2, w.scale_log2), nl2 = make_float2(-lse2, -lse2);
+    // This group's share of D.
     float delta = 0.f;
     bool ok = true;
+    const uint32_t ts = trow + kGroupCols * group;
 #pragma unroll 1
-    for (int j = 0; j < first; ++j) {
-      if (!(ok = __all_sync(0xffffffffu, wait(s_full, j & 1)))) break;
+    for (int j = group; j < first; j += 2) {
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full(group), (j >> 1) & 1)))) break;
       ptx::tc_fence_after();
-      const int cols = kt.cols(j);
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 16) {
+      for (int c = 0; c < kBN; c += 16) {
         uint32_t sv[16], dv[16];
-        ptx::tmem_ld16x2_sync(trow + kColS + c, trow + kColDP + c, sv, dv);
-        if (c + 16 >= cols) warp_arrive(s_free);
+        ptx::tmem_ld16x2_sync(ts + c, ts + kBN + c, sv, dv);
         const uint32_t see = visible_bits(w, p, low, kt.begin(j) + c);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -285,98 +310,91 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           if ((see >> k) & 1u) delta = fmaf(pr, __uint_as_float(dv[k]), delta);
         }
       }
+      warp_arrive(s_free(group));
     }
-    if (valid) {
-      if (first == 0) {
-        // D of the row, in float from the bf16 rows.
-        const uint4* a = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.out + orow * kDh);
-        const uint4* d = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.dout + orow * kDh);
-        float x[8], y[8];
+    if (valid && first == 0) {
+      // In float from the bf16 rows.
+      const uint4* a = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.out + orow * kDh) + 4 * group;
+      const uint4* d = reinterpret_cast<const uint4*>((const __nv_bfloat16*)w.dout + orow * kDh) + 4 * group;
+      float x[8], y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          chunk_to_float(__ldg(a + i), x, __nv_bfloat16());
-          chunk_to_float(__ldg(d + i), y, __nv_bfloat16());
+      for (int i = 0; i < 4; ++i) {
+        chunk_to_float(__ldg(a + i), x, __nv_bfloat16());
+        chunk_to_float(__ldg(d + i), y, __nv_bfloat16());
 #pragma unroll
-          for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
-        }
+        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
       }
+    }
+    shares[group * kRowsPerTile + row] = delta;
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");        // the softmax warps
+    delta = shares[row] + shares[kRowsPerTile + row];
+    if (valid && group == 0) {
       w.delta[orow] = delta;
-      write_terms(w, 0, orow, p >= 0 ? -w.lse[orow] / w.scale : 0.f);
+      write_terms(w, 0, orow, -lse / w.scale);
       write_terms(w, 1, orow, -delta);
     }
     const float2 nd2 = make_float2(-delta, -delta);
 #pragma unroll 1
-    for (int j = 0; ok && j < T; ++j) {
-      if (!(ok = __all_sync(0xffffffffu, wait(s_full, (first + j) & 1)))) break;
+    for (int j = group ^ (first & 1); ok && j < T; j += 2) {
+      if (!(ok = __all_sync(0xffffffffu, wait(s_full(group), ((first + j) >> 1) & 1)))) break;
       ptx::tc_fence_after();
-      const int k0 = kt.begin(j), cols = kt.cols(j);
-      // 32 columns of S and dP at a time: the next step's go to tensor memory
-      // once the last are read.
-      uint32_t pk[32];
+      const int c0 = kt.begin(j);
+      uint32_t pk[16];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        if (32 * q >= cols) break;
-        uint32_t sv[32], dv[32];
-        ptx::tmem_ld32x2_sync(trow + kColS + 32 * q, trow + kColDP + 32 * q, sv, dv);
-        if (32 * q + 32 >= cols) warp_arrive(s_free);
-        const int c0 = k0 + 32 * q;
+        uint32_t sv[16], dv[16];
+        ptx::tmem_ld16x2_sync(ts + 16 * q, ts + kBN + 16 * q, sv, dv);
+        if (q == 1) warp_arrive(s_free(group));
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), c2, nl2);
           const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])), nd2);
           const float2 ds = __fmul2_rn(make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), t);
-          pk[16 * q + k] = pack_bf16x2(ds.x, ds.y);
-        }
-        if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {   // some row sees the chunk in part
-          const uint32_t see = visible_bits(w, p, low, c0);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t keep = ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
-            pk[16 * q + k] &= keep;
-          }
+          pk[8 * q + k] = pack_bf16x2(ds.x, ds.y);
         }
       }
-      // dS of the previous step is read by its dQ MMAs until p_free: wait only
-      // now, so this step's exponentials overlap them.
-      if (j > 0) {
-        if (!(ok = __all_sync(0xffffffffu, wait(p_free, (j - 1) & 1)))) break;
+      if (c0 < low_last || c0 + 31 > p0 || r0 + tokens > s.lq) {   // some row sees the chunk in part
+        const uint32_t see = visible_bits(w, p, low, c0);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          pk[k] &= kept_pair(see, k);
+        }
+      }
+      // dS of the group's previous step is read by its dQ MMAs until p_free: wait
+      // only now, so this step's exponentials overlap them.
+      if (j > 1) {
+        if (!(ok = __all_sync(0xffffffffu, wait(p_free(group), ((j >> 1) - 1) & 1)))) break;
         ptx::tc_fence_after();
       }
-      ptx::tmem_st16(trow + kColDS, pk);
-      if (cols == 64) ptx::tmem_st16(trow + kColDS + 16, pk + 16);
+      ptx::tmem_st16(ts + 2 * kBN, pk);
       ptx::tmem_wait_st();
-      warp_arrive(p_full);
+      warp_arrive(p_full(group));
     }
     if (T == 0 || (ok && __all_sync(0xffffffffu, wait(o_final, 0)))) {
-      uint32_t o[kDh];
+      uint32_t o[32];
       if (T > 0) {
         ptx::tc_fence_after();
-        ptx::tmem_ld64_sync(trow + kColDQ, o);
+        ptx::tmem_ld32_sync(trow + kColDQ + 32 * group, o);
       } else {
 #pragma unroll
-        for (int e = 0; e < kDh; ++e) o[e] = 0u;
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
       float sum = 0.f;                                 // not finite where any element is not
 #pragma unroll
-      for (int e = 0; e < kDh; ++e) {
+      for (int e = 0; e < 32; ++e) {
         const float x = __uint_as_float(o[e]) * w.scale;
         sum = fmaf(x, 0.f, sum);
         o[e] = __float_as_uint(x);
       }
-      const bool again = valid && !(sum == 0.f);
       if (valid) {
-        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.dq + orow * kDh);
+        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.dq + orow * kDh) + 4 * group;
 #pragma unroll
-        for (int q = 0; q < kDh / 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
           const float* x = reinterpret_cast<const float*>(o + 8 * q);
           dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                               pack_bf16x2(x[6], x[7]));
         }
-      }
-      __syncwarp();
-      for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
-        const int rr = lane_base + __ffs(todo) - 1;
-        dq_row<__nv_bfloat16>(w, s, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
+        if (!(sum == 0.f)) redo[row] = 1;
       }
     }
   }
@@ -386,9 +404,10 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   if (ctl->abort) {
     // Every role has finished: the MMAs and loads this CTA started complete
     // before its tensor and shared memory are released.
-    if (warp == kMmaWarp && lane == 0) {
-      ptx::tc_commit(drain);
-      ptx::mbar_wait_drain(drain, 0, ctl->limit_ns);
+    if ((warp == kMmaWarp || warp == kMmaWarp2) && lane == 0) {
+      const uint32_t d = drain(warp - kMmaWarp);
+      ptx::tc_commit(d);
+      ptx::mbar_wait_drain(d, 0, ctl->limit_ns);
     }
     if (warp == kTmaWarp && lane == 0) {
       ptx::mbar_wait_drain(qfull, 0, ctl->limit_ns);
@@ -403,7 +422,13 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
-  if (threadIdx.x == 0 && ctl->abort) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+  if (ctl->abort) {
+    if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
+    return;
+  }
+#pragma unroll 1
+  for (int row = warp; row < kRowsPerTile; row += kThreads / 32)
+    if (redo[row]) dq_row<__nv_bfloat16>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
 }
 
 }  // namespace q_side
@@ -678,7 +703,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         if (!whole) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const uint32_t keep = ((see >> (2 * k)) & 1u ? 0xffffu : 0u) | ((see >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+            const uint32_t keep = kept_pair(see, k);
             pd[k] &= keep;
             pp[k] &= keep;
           }
