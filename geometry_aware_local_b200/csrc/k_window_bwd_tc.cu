@@ -81,18 +81,7 @@ __device__ __forceinline__ uint32_t kept_pair(uint32_t see, int k) {
 // ============================================================================
 namespace q_side {
 
-constexpr int kBN = 32;
-// The key tiles of a query tile, as in the forward but of 32 columns: the sinks'
-// (up to two) in front.
-struct SmallTiles {
-  int lo, sink_tiles, n;
-  __device__ __forceinline__ int begin(int j) const { return j < sink_tiles ? j * kBN : lo + (j - sink_tiles) * kBN; }
-};
-__device__ __forceinline__ SmallTiles small_tiles(const Win& w, int p0, int p1) {
-  const KeyTiles<2 * kBN> k = key_tiles<2 * kBN>(w, p0, p1);      // a tile holds every sink
-  const int sink_tiles = k.sink_cols / kBN;
-  return SmallTiles{k.lo, sink_tiles, p1 < 0 ? 0 : (k.hi - k.lo) / kBN + 1 + sink_tiles};
-}
+constexpr int kBN = kSmallTile;
 // Two groups of softmax warps on alternate steps; two MMA warps; TMA warp.
 constexpr int kSoftmaxWarps = 8, kThreads = 32 * (kSoftmaxWarps + 3);
 constexpr int kMmaWarp = kSoftmaxWarps, kMmaWarp2 = kSoftmaxWarps + 1, kTmaWarp = kSoftmaxWarps + 2;

@@ -7,10 +7,11 @@
 // head) pairs of the group, 128/G tokens of one sequence x G heads, so the
 // heads that share keys share every key tile.  The tile's visible keys are one
 // range [lo, hi] (the first token's window to the last token) and, where the
-// window has moved past them, the sinks as one short tile in front.  Keys come
-// in tiles of 96 from lo on; the last tile, and the sinks' one, are cut to a
-// multiple of 32 columns, so the work follows the range in steps of 32 keys.
-// Masks are evaluated only in the 32-column chunks that some row sees in part.
+// window has moved past them, the sinks in front.  Keys come in tiles of 32 from
+// lo on, four CTAs an SM, or where a call has too few CTAs for that in tiles of
+// 96, two an SM, the last tile and the sinks' one cut to a multiple of 32 columns
+// (narrow() says when).  Masks are evaluated only in the 32-column chunks that
+// some row sees in part.
 //   * the last warp loads the Q tile and a ring of K / V tiles by TMA (boxes of
 //     32 keys x 64 dims, 128-byte swizzle); the first loads are under way
 //     before the CTA first meets;
@@ -19,22 +20,24 @@
 //   * four softmax warps (thread = row = TMEM lane) run the online softmax in
 //     base 2 with a lazily moved maximum: O is rescaled only when a row maximum
 //     grows by more than 2^8.
-// Tensor memory of a CTA, 256 columns (two CTAs per SM): two regions of 96 and
+// Tensor memory of a CTA, 128 or 256 columns: two regions of a tile's width and
 // O (64).  Tile j's S and then, over it, its P (packed bf16) are in region
 // j % 2: a warp has its rows of S in registers before it writes P.  S of tile
 // j + 1 is under way while tile j is exponentiated, and S of tile j + 2 follows
-// the product with P of tile j.  (S and two P buffers apart, one S region: 0.298
-// against 0.288 ms at the size below.)
+// the product with P of tile j.
 //
 // At d_h = 64 an exponential pairs with only 256 MMA flops, so the bound is the
-// exponentials' rate (16 a clock and SM: 0.12 ms at that size); what paces the
-// kernel is the softmax warps' chain of a tile (wait, load, maximum,
-// exponentials, store, arrive), of which two CTAs overlap, and a CTA's start
-// and end, which a window of 1,024 keys pays every 11 tiles.  The code is kept
-// small on purpose: the roles' loops evict one another from the instruction
-// cache, and a second copy of the softmax body for tiles without masks made the
-// kernel a quarter slower.  Persistent CTAs that walk the tiles measured 0.320 ms.
-// 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.288 ms, 475 TFLOP/s.
+// exponentials' rate (16 a clock and SM: 0.115 ms at the size below); what paces
+// the kernel is the softmax warps' chain of a tile (wait, load, maximum,
+// exponentials, store, arrive), so the number of CTAs that overlap theirs decides:
+// narrow tiles let four share an SM's tensor memory and registers, although they
+// pay each tile's barriers three times as often.  The code is kept small on
+// purpose: the roles' loops evict one another from the instruction cache, and a
+// second copy of the softmax body for tiles without masks made the kernel a
+// quarter slower.
+// 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.230 ms, 595 TFLOP/s, with
+// narrow tiles; 0.287 with wide ones (0.298 with S and two P buffers apart, 0.320
+// with persistent CTAs that walk the tiles).
 //
 // Few query tiles before many keys (a piece of a long prompt) would leave most
 // SMs idle: then the CTAs of a cluster (2, 4 or 8) share a tile's key tiles and
@@ -51,20 +54,37 @@ namespace pack3d {
 namespace seq {
 namespace {
 
-constexpr int kBM = kRowsPerTile, kBN = 96;
+constexpr int kBM = kRowsPerTile;
 constexpr int kMmaWarp = 4, kTmaWarp = 5, kThreads = 192;
-constexpr int kColO = 2 * kBN, kTmemCols = 256;   // tile j: S, then P over it, at (j & 1) * kBN
-static_assert(kColO + kDh <= kTmemCols, "tensor memory plan");
-constexpr int kQBytes = kBM * kDh * 2, kTileBytes = kBN * kDh * 2;
-constexpr int kStages = 3;
-constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;     // K at +0, V at +kTileBytes
-constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, s_full[2], p_full[2], pv_done[2], o_final, drain
-constexpr int kNumBars = 2 * kStages + 9;
-constexpr int kCtlOff = kBarOff + kNumBars * 8;
-constexpr int kPlanOff = kCtlOff + 32;
-constexpr int kSmemBytes = kPlanOff + 64 + 1024;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr int kQBytes = kBM * kDh * 2;
+constexpr int kWide = 96;                       // columns of a key tile with two CTAs an SM; kSmallTile with four
+// What the width of a key tile decides.
+template <int BN>
+struct Layout {
+  using Tiles = KeyTiles<BN>;
+  static constexpr int kCtas = 2, kStages = 3, kTmemCols = 256;
+  static __device__ __forceinline__ Tiles tiles(const Win& w, int p0, int p1) { return key_tiles<BN>(w, p0, p1); }
+};
+template <>
+struct Layout<kSmallTile> {
+  using Tiles = SmallTiles;
+  static constexpr int kCtas = 4, kStages = 4, kTmemCols = 128;
+  static __device__ __forceinline__ Tiles tiles(const Win& w, int p0, int p1) { return small_tiles(w, p0, p1); }
+};
+template <int BN>
+struct Smem {
+  static constexpr int kStages = Layout<BN>::kStages, kTileBytes = BN * kDh * 2;
+  static constexpr int kColO = 2 * BN;          // tile j: S, then P over it, at (j & 1) * BN
+  static constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;      // K at +0, V at +kTileBytes
+  static constexpr int kBarOff = kStageOff + kStages * kStageBytes;
+  // barriers: full[S], empty[S], qfull, s_full[2], p_full[2], pv_done[2], o_final, drain
+  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kCtlOff = kBarOff + kNumBars * 8;
+  static constexpr int kPlanOff = kCtlOff + 32;
+  static constexpr int kBytes = kPlanOff + 64 + 1024;
+  static_assert(kColO + kDh <= Layout<BN>::kTmemCols, "tensor memory plan");
+  static_assert(Layout<BN>::kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
+};
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kDh, true);   // V MN-major
 
@@ -82,7 +102,7 @@ struct Share {
   float o[kBM][kDh + 4];
   float m[kBM], l[kBM];
 };
-static_assert(sizeof(Share) <= kStages * kStageBytes, "share slot");
+static_assert(sizeof(Share) <= Smem<kWide>::kStages * Smem<kWide>::kStageBytes, "share slot");
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -91,16 +111,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // kSplit: the CTAs of a cluster along z share the tile's key tiles.
-template <bool kSplit>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kBN, bool kSplit>
+__global__ void __launch_bounds__(kThreads, Layout<kBN>::kCtas)
 window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Win w) {
+  using M = Smem<kBN>;
+  constexpr int kStages = M::kStages, kStageOff = M::kStageOff, kStageBytes = M::kStageBytes;
+  constexpr int kTileBytes = M::kTileBytes, kTmemCols = Layout<kBN>::kTmemCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y;
   const uint32_t sbase = ptx::smem_u32(smem);
-  const uint32_t bar0 = sbase + kBarOff;
+  const uint32_t bar0 = sbase + M::kBarOff;
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
   const uint32_t qfull = bar0 + 8 * (2 * kStages);
@@ -108,8 +131,8 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   auto s_full = [&](int b) { return qfull + 24 + 8 * b; };
   auto p_full = [&](int b) { return qfull + 40 + 8 * b; };
   auto pv_done = [&](int b) { return qfull + 56 + 8 * b; };
-  volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
+  volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + M::kCtlOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::kCtlOff + sizeof(ptx::WaitCtl));
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kBM >> w.gshift;     // per tile
 
@@ -152,12 +175,12 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   s.t = s.n - 1 - s.t;      // the tiles with most keys first
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const int p0 = position(s, r0), p1 = position(s, r1);
-  const KeyTiles<kBN> kt = key_tiles<kBN>(w, p0, p1);
+  const typename Layout<kBN>::Tiles kt = Layout<kBN>::tiles(w, p0, p1);
   // This CTA's key tiles: [jo, jo + T).
   const int jo = kSplit ? (int)((long)kt.n * blockIdx.z / gridDim.z) : 0;
   const int T = kSplit ? (int)((long)kt.n * (blockIdx.z + 1) / gridDim.z) - jo : kt.n;
   const int T_load = w.stall ? max(T - 1, 0) : T;
-  volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + kPlanOff);
+  volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + M::kPlanOff);
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
@@ -202,7 +225,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issuer ----------------
     if (T > 0 && ptx::elect_one()) {
-      const uint32_t tO = tmem + kColO;
+      const uint32_t tO = tmem + M::kColO;
       auto issue_s = [&](int j) {
         const uint32_t kaddr = sbase + kStageOff + (j % kStages) * kStageBytes;
         const uint32_t idesc = ptx::idesc_bf16_f32(kBM, kt.cols(jo + j), false);
@@ -246,7 +269,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     // ---------------- softmax warps: thread = row = tensor-memory lane ----------------
     const int lane_base = warp * 32;
     const uint32_t trow = tmem + ((uint32_t)lane_base << 16);
-    const uint32_t tO = trow + kColO;
+    const uint32_t tO = trow + M::kColO;
     const float c = w.scale_log2;
     // A 32-key chunk is seen in full by every row if it lies in [full_lo,
     // full_hi]: behind the last row's window start and not past the first row's
@@ -266,9 +289,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       ptx::tc_fence_after();
       const uint32_t tS = trow + (j & 1) * kBN;
       uint32_t sv[kBN];
-      if (cols > 32) ptx::tmem_ld64_sync(tS, sv);
-      else ptx::tmem_ld32_sync(tS, sv);
-      if (cols > 64) ptx::tmem_ld32_sync(tS + 64, sv + 64);
+      if constexpr (kBN == kSmallTile) {
+        ptx::tmem_ld32_sync(tS, sv);
+      } else {
+        if (cols > 32) ptx::tmem_ld64_sync(tS, sv);
+        else ptx::tmem_ld32_sync(tS, sv);
+        if (cols > 64) ptx::tmem_ld32_sync(tS + 64, sv + 64);
+      }
       float mx = -INFINITY;
 #pragma unroll
       for (int q = 0; q < kBN / 32; ++q) {
@@ -454,47 +481,63 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   }
 }
 
-}  // namespace
-
 // CTAs of a cluster per query tile: as many as keep two CTAs an SM busy and
 // leave each at least four key tiles (2,048 queries before 16,384 keys, 8 heads
 // to one key head: 0.238 ms with 1, 0.131 with 2).
 int split_of(const Win& w, long tiles) {
-  const long keys = w.window > 0 ? min((long)w.Tk, (long)w.window + 2 * kBN) : w.Tk;
+  const long keys = w.window > 0 ? min((long)w.Tk, (long)w.window + 2 * kWide) : w.Tk;
   int S = 1;
-  while (S < 8 && tiles * w.Hkv * S * 2 <= 2L * sm_count() && keys / kBN >= 8L * S) S *= 2;
+  while (S < 8 && tiles * w.Hkv * S * 2 <= 2L * sm_count() && keys / kWide >= 8L * S) S *= 2;
   return S;
 }
 
-cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st) {
+// Whether the key tiles are narrow, with four CTAs an SM: where there are CTAs
+// for them.  Without a window the CTAs' lengths differ, and it takes more than
+// four an SM for the short ones to fill the gaps.  Narrow against wide: 65,536
+// tokens, window 1,024 0.230 : 0.287 ms; 6,300 tokens, 8 key heads, window 256
+// (400 CTAs) 23 : 27 us; 4,096, window 512 (256) 19.5 : 18.5; 8,192, no window
+// (512) 163 : 154; the same with 16 heads (1,024) 225 : 238.
+bool narrow(const Win& w, long tiles) {
+  return tiles * w.Hkv > (w.window > 0 ? 2L : 4L) * sm_count();
+}
+
+template <int BN, bool kSplit>
+cudaError_t launch_tc(const Win& w, const dim3& grid, cudaStream_t st) {
+  constexpr int kBytes = Smem<BN>::kBytes;
   // First, so that a thread that has made no CUDA call yet (autograd's) has the
   // device's context when the tensor maps are encoded.
-  cudaError_t e =
-      cudaFuncSetAttribute(window_attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(window_attn_tc_kernel<BN, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kBytes);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
   if (!map_query_rows(&tq, w, w.q) || !map_key_rows(&tk, w, w.k, 32) || !map_key_rows(&tv, w, w.v, 32))
     return cudaErrorInvalidValue;
-  const long tiles = tile_grid(w.Tq, kBM >> w.gshift, w.B);
-  const int S = split_of(w, tiles - 1);
-  if (S == 1) {
-    window_attn_tc_kernel<false><<<dim3((unsigned)tiles, w.Hkv), kThreads, kSmemBytes, st>>>(tq, tk, tv, w);
+  if constexpr (!kSplit) {
+    window_attn_tc_kernel<BN, false><<<grid, kThreads, kBytes, st>>>(tq, tk, tv, w);
     return cudaGetLastError();
   }
-  e = cudaFuncSetAttribute(window_attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = cluster.val.clusterDim.y = 1;
-  cluster.val.clusterDim.z = S;
+  cluster.val.clusterDim.z = grid.z;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)tiles, w.Hkv, S);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = st;
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, window_attn_tc_kernel<true>, tq, tk, tv, w);
+  return cudaLaunchKernelEx(&cfg, window_attn_tc_kernel<BN, kSplit>, tq, tk, tv, w);
+}
+
+}  // namespace
+
+cudaError_t launch_window_attn_tc(const Win& w, cudaStream_t st) {
+  const long tiles = tile_grid(w.Tq, kBM >> w.gshift, w.B);
+  if (narrow(w, tiles - 1)) return launch_tc<kSmallTile, false>(w, dim3((unsigned)tiles, w.Hkv), st);
+  const int S = split_of(w, tiles - 1);
+  if (S == 1) return launch_tc<kWide, false>(w, dim3((unsigned)tiles, w.Hkv), st);
+  return launch_tc<kWide, true>(w, dim3((unsigned)tiles, w.Hkv, S), st);
 }
 
 }  // namespace seq

@@ -60,6 +60,21 @@ __device__ __forceinline__ KeyTiles<BN> key_tiles(const Win& w, int p0, int p1) 
   return k;
 }
 
+// The same in tiles of 32 columns: the sinks' (one or two) in front.
+constexpr int kSmallTile = 32;
+struct SmallTiles {
+  int lo, sink_tiles, n;
+  __device__ __forceinline__ int begin(int j) const {
+    return j < sink_tiles ? j * kSmallTile : lo + (j - sink_tiles) * kSmallTile;
+  }
+  static __device__ __forceinline__ constexpr int cols(int) { return kSmallTile; }
+};
+__device__ __forceinline__ SmallTiles small_tiles(const Win& w, int p0, int p1) {
+  const KeyTiles<2 * kSmallTile> k = key_tiles<2 * kSmallTile>(w, p0, p1);      // a tile holds every sink
+  const int sink_tiles = k.sink_cols / kSmallTile;
+  return SmallTiles{k.lo, sink_tiles, p1 < 0 ? 0 : (k.hi - k.lo) / kSmallTile + 1 + sink_tiles};
+}
+
 // Bit k: the query at position p (window start `low`) sees key c0 + k.  p < 0:
 // none.
 __device__ __forceinline__ uint32_t visible_bits(const Win& w, int p, int low, int c0) {

@@ -86,6 +86,35 @@ def test_hundreds_of_sequences(p3, cuda_device, Hq, Hkv, W, S, dtype):
     check_window(p3, lens, klens, Hq, Hkv, W, S, dtype, cuda_device)
 
 
+@pytest.mark.parametrize("lens,klens,Hq,Hkv,W,S", [
+    ([65], [65], 320, 320, 33, 64),                    # every key a sink
+    ([300], [300], 240, 120, 33, 64),                  # two tiles of sinks
+    ([300, 0, 211], [300, 0, 211], 120, 120, 97, 1),
+    ([40, 130], [700, 130], 640, 160, 64, 3),
+    ([9, 70], [4, 50], 400, 200, 0, 0),                # more queries than keys
+    ([1], [1], 1024, 1024, 0, 0),
+    ([500], [500], 1024, 128, 100, 64),
+    ([31, 32, 33], [64, 96, 160], 400, 200, 32, 33),
+])
+def test_as_many_heads_as_fill_the_gpu(p3, cuda_device, lens, klens, Hq, Hkv, W, S):
+    """Enough tiles for the narrow key tiles of the bf16 forward, at the masks' edges."""
+    check_window(p3, lens, klens, Hq, Hkv, W, S, torch.bfloat16, cuda_device)
+
+
+def test_hidden_nan_in_narrow_tiles(p3, cuda_device):
+    dev, n, W, S, bad = cuda_device, 5000, 40, 3, 2500
+    q, k, v, _ = inputs([n], [n], 8, 2, torch.bfloat16, dev, 7)
+    cfg = p3.make_seq_config(window=W, sinks=S)
+    r = ref.window(q, k, v, [n], [n], W, S, cfg.softmax_scale)
+    v[bad], k[bad] = float("nan"), float("inf")
+    out, lse = p3.window_attn(cfg, q, k, v, offsets([n], dev))
+    rows = torch.arange(n, device=dev)
+    reads = (rows >= bad) & (rows - bad < W)
+    assert torch.isnan(out[reads].float()).all()
+    ref.close(out[~reads], r["out"][~reads], r["out_tol"][~reads], "out")
+    ref.close(lse[~reads], r["lse"][~reads], r["lse_tol"][~reads], "lse")
+
+
 def test_as_many_sequences_as_there_may_be(p3, cuda_device):
     """Sequences of one token: the softmax of one score is 1, so out is v, and dv the group's dout."""
     dev, n = cuda_device, 65535

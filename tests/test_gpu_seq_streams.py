@@ -66,8 +66,9 @@ def test_hidden_nan_in_a_shared_tile(p3):
 
 # ---- bounded waits -----------------------------------------------------------------------
 
-@pytest.mark.parametrize("lens,klens,W,S", [([5], [5], 0, 0), ([700], [700], 100, 4), ([70], [4000], 0, 0)],
-                         ids=["one-tile", "several", "cluster"])
+@pytest.mark.parametrize("lens,klens,W,S", [([5], [5], 0, 0), ([700], [700], 100, 4), ([70], [4000], 0, 0),
+                                              ([5000], [5000], 100, 4)],
+                         ids=["one-tile", "several", "cluster", "narrow"])
 def test_times_out_then_recovers(p3, lens, klens, W, S):
     """Every tensor-core kernel withholds its last tile: the call reports the timeout, and the same call without the
     flag is right afterwards.  (The waits are bounded at 2 ms; nothing faults or hangs.)"""
