@@ -239,23 +239,34 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     new = dq is None
     if (dk is None) != new or (dv is None) != new:
         raise ValueError(f"{what}: give all of dq, dk and dv or none of them")
-    grads = [torch.empty_like(t) for t in (q, k, v)] if new else [dq, dk, dv]
-    if new and cu_q.shape[0] == 1:
-        return tuple(t.zero_() for t in grads)
     if not new:
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             _require(what, cfg, name, t, T, tuple(like.shape), dev)
-    if workspace is None:
-        n = window_attn_bwd_workspace_bytes(cfg, cu_q.shape[0] - 1, q.shape[0], k.shape[0])
-        workspace = _new(dev, torch.uint8, max(n, 256))
-    else:
+    if workspace is not None:
         _check_workspace(what, workspace, dev)
     _check_err_word(what, err, dev, torch)
-    _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), cu_q.shape[0] - 1, q.shape[0],
-          k.shape[0], cu_q.data_ptr(), cu_k.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-          lse.data_ptr(), dout.data_ptr(), *[t.data_ptr() for t in grads], int(new),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _p(err))
-    return tuple(grads)
+    return _window_bwd(torch, what, cfg, q, k, v, cu_q, cu_k, out, lse, dout, None if new else (dq, dk, dv), workspace,
+                       err, stream)
+
+
+def _window_bwd(torch, what, cfg, q, k, v, cu_q, cu_k, out, lse, dout, grads, workspace, err, stream):
+    """window_attn_bwd behind its checks; grads None: made here."""
+    new = grads is None
+    if new:
+        grads = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
+            return tuple(t.zero_() for t in grads)
+    dq, dk, dv = grads
+    batch, q_rows, k_rows, dev = cu_q.shape[0] - 1, q.shape[0], k.shape[0], q.device
+    if workspace is None:
+        n = window_attn_bwd_workspace_bytes(cfg, batch, q_rows, k_rows)
+        workspace = _new(dev, torch.uint8, max(n, 256))
+    else:
+        n = workspace.numel() * workspace.element_size()
+    _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), batch, q_rows, k_rows,
+          cu_q.data_ptr(), cu_k.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), int(new), workspace.data_ptr(), n, _p(err))
+    return grads
 
 
 def window_attention(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, err=None):
@@ -287,9 +298,9 @@ def _autograd():
             @staticmethod
             @once_differentiable
             def backward(ctx, dout):
-                q, k, v, cu_q, cu_k, out, lse = ctx.saved_tensors
-                dq, dk, dv = window_attn_bwd(ctx.cfg, q, k, v, cu_q, cu_k, out, lse, dout.to(q.dtype).contiguous(),
-                                             err=ctx.err)
+                q, k, v, cu_q, cu_k, out, lse = ctx.saved_tensors      # checked by the forward
+                dq, dk, dv = _window_bwd(torch, "pack3d_window_attn_bwd", ctx.cfg, q, k, v, cu_q, cu_k, out, lse,
+                                         dout.to(q.dtype).contiguous(), None, None, ctx.err, None)
                 return None, dq, dk, dv, None, None, None
 
         _autograd_class = WindowAttention
