@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
   __shared__ uint32_t s_prefix;
   __shared__ int2 warp_count[kSelWarps];
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  let_next_begin();
   const int n = cached(c, b);
   const float* w = weights + (size_t)b * c.cap;
   int32_t* kb = kept + (size_t)b * budget;
@@ -203,16 +204,17 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const Cache c
 
 // Copies the kept rows to the new pages: one thread per 16-byte chunk of a key
 // and a value row.
-__global__ void __launch_bounds__(256) cache_move_kernel(const Cache c, const int32_t* __restrict__ kept, int budget,
+__global__ void __launch_bounds__(256) cache_move_kernel(const Cache c, const int32_t* kept, int budget,
                                                          const int32_t* __restrict__ new_table, int new_max_pages,
                                                          int chunks) {
   const long total = (long)budget * chunks;
   const int b = blockIdx.y;
   Cache to = c;
   to.max_pages = new_max_pages;
+  wait_for_last();
   for (long i = blockIdx.x * (long)blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
     const int slot = (int)(i / chunks), chunk = (int)(i - (long)slot * chunks);
-    const int from = __ldg(kept + (size_t)b * budget + slot);
+    const int from = kept[(size_t)b * budget + slot];
     if (from < 0) continue;
     const long src = pool_row(c, c.table + (size_t)b * c.max_pages, from);
     const long dst = pool_row(to, new_table + (size_t)b * new_max_pages, slot);
@@ -249,8 +251,7 @@ cudaError_t launch_cache_evict(const Cache& c, const float* weights, int budget,
   const int chunks = c.Hkv * kDh * c.elem_bytes / 16;
   const long want = ((long)budget * chunks + 255) / 256;
   const dim3 grid((unsigned)min(want, 148L * 16), c.B);
-  cache_move_kernel<<<grid, 256, 0, st>>>(c, kept, budget, new_table, new_max_pages, chunks);
-  return cudaGetLastError();
+  return launch_behind(cache_move_kernel, grid, 256, 0, st, c, kept, budget, new_table, new_max_pages, chunks);
 }
 
 }  // namespace seq

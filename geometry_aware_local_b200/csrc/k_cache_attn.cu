@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const DecodeArg
   CtaSmem<G>* sm = reinterpret_cast<CtaSmem<G>*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Cache& c = a.c;
+  let_next_begin();
   if (threadIdx.x < 2 * kWarps) sm->spans[threadIdx.x].b = -1;
   // This CTA's run of units: where it begins, and how many.
   Unit at;
@@ -643,6 +644,8 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a) {
   const Cache& c = a.c;
   const int b = blockIdx.x / c.Hq, hq = blockIdx.x % c.Hq, g = hq / G, h = hq % G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  let_next_begin();
+  wait_for_last();
   const int2 from = a.joins[b * c.Hkv + g];
   if (units_of(c, b) == 0) {          // nothing cached: no CTA had it
     if (warp == 0) write_row<T>(a, b, hq, -INFINITY, 0.f, make_float2(0.f, 0.f));
@@ -692,19 +695,19 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const DecodeArgs a) {
 
 // The token's weight of every slot: softmax weights from the kept scores and
 // the rows' denominators, summed over the heads.
-__global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const float* __restrict__ logits,
-                                                            const float* __restrict__ row_lse2,
-                                                            float* __restrict__ weights, int accumulate) {
+__global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const float* logits, const float* row_lse2,
+                                                            float* weights, int accumulate) {
   const int b = blockIdx.y;
   const int n = cached(c, b);
   const Seen v = seen(c, n);
+  wait_for_last();
   for (int j = blockIdx.x * 256 + threadIdx.x; j < n; j += gridDim.x * 256) {
     const int i = j < v.s0 ? j : (j >= v.lo ? j - v.lo + v.s0 : -1);
     float total = 0.f;
     if (i >= 0)
       for (int h = 0; h < c.Hq; ++h) {
         const size_t at = (size_t)b * c.Hq + h;
-        total += ptx::ex2(__ldg(logits + at * c.cap + i) - __ldg(row_lse2 + at));
+        total += ptx::ex2(logits[at * c.cap + i] - row_lse2[at]);
       }
     float* dst = weights + (size_t)b * c.cap + j;
     *dst = accumulate ? *dst + total : total;
@@ -745,8 +748,7 @@ cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
   cache_attn_kernel<T, G><<<ctas, kThreads, kSmem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
-  cache_join_kernel<T, G><<<c.B * c.Hq, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(cache_join_kernel<T, G>, c.B * c.Hq, 256, 0, st, a);
 }
 
 template <typename T>
@@ -789,8 +791,7 @@ cudaError_t launch_cache_attn(const Cache& c, int dtype, const void* q, void* ou
   cudaError_t e = dtype == PACK3D_BF16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
   if (e != cudaSuccess || !weights || c.cap == 0) return e;
   const dim3 grid((unsigned)((c.cap + 255) / 256), c.B);
-  cache_weights_kernel<<<grid, 256, 0, st>>>(c, a.logits, a.row_lse2, weights, accumulate);
-  return cudaGetLastError();
+  return launch_behind(cache_weights_kernel, grid, 256, 0, st, c, a.logits, a.row_lse2, weights, (int)accumulate);
 }
 
 }  // namespace seq

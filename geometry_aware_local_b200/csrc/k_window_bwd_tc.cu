@@ -137,6 +137,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kRowsPerTile >> w.gshift;
 
+  let_next_begin();
   // The producer sets the barriers up, and every warp finds the tile for
   // itself, so that the first loads are under way before the CTA meets.
   if (warp == kTmaWarp && lane == 0) {
@@ -489,6 +490,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   volatile uint8_t* redo = smem + kRedoOff;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kStep >> w.gshift;
+  let_next_begin();
   const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
   const int x = far ? blockIdx.x - key_grid : blockIdx.x;
 
@@ -530,6 +532,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     ptx::fence_proxy_async_smem();
   }
   __syncthreads();
+  wait_for_last();                                      // for delta and the rows' terms
   if (*found_slot != 1) {
     if (!far && *found_slot == 0 && w.zero_outside && blockIdx.y == 0) {
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh / 2, 0u);
@@ -819,9 +822,8 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int key_grid = (int)tile_grid(w.Tk, k_side::kKeys, w.B);
   const dim3 gk((unsigned)(key_grid + far_grid<kRowsPerTile>(w)), w.Hkv);
-  k_side::window_dkv_tc_kernel<<<gk, k_side::kThreads, k_side::kSmemBytes, st>>>(tq64, to64, tk128, tv128, tt, w,
-                                                                                key_grid);
-  e = cudaGetLastError();
+  e = launch_behind(k_side::window_dkv_tc_kernel, gk, k_side::kThreads, k_side::kSmemBytes, st, tq64, to64, tk128, tv128,
+                    tt, w, key_grid);
   if (e != cudaSuccess) return e;
   return launch_window_sinks<__nv_bfloat16, k_side::kKeys, kRowsPerTile>(w, st);
 }

@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_bwd_f32_kernel(const Win w
   extern __shared__ float4 smem4[];
   __shared__ int redo[64];
   float* tiles = reinterpret_cast<float*>(smem4);
+  let_next_begin();
   const int x = blockIdx.x, y = x - key_ctas * w.Hkv;
   if (y < 0) key_side(w, x / w.Hkv, key_grid, x % w.Hkv, tiles, redo);
   else query_side(w, y / w.Hkv, query_ctas, y % w.Hkv, tiles, redo);

@@ -147,6 +147,27 @@ __device__ __forceinline__ void fill_outside(const Win& w, const int32_t* cu, in
     p[i < before ? i : (long)c1 * words + (i - before)] = value;
 }
 
+// Launches that follow one another in a call overlap: the second is put in place
+// while the first's last CTAs run (they say so as they begin), and each of its
+// CTAs waits, before it touches what the first writes or returns, for the first
+// to end.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // SMs of the current device.
 inline int sm_count() {
   int dev = 0, n = 148;

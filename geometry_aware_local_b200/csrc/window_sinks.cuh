@@ -64,6 +64,7 @@ template <typename T, int Keys, int Rows>
 __global__ void __launch_bounds__(256) window_sinks_kernel(const Win w) {
   __shared__ float4 sums[8][32];
   const int g = blockIdx.y, j = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_last();
 #pragma unroll 1
   for (int b = blockIdx.x; b < w.B; b += gridDim.x) {
     if (off_range(w, b)) continue;
@@ -114,8 +115,7 @@ __global__ void __launch_bounds__(256) window_sinks_kernel(const Win w) {
 template <typename T, int Keys, int Rows>
 cudaError_t launch_window_sinks(const Win& w, cudaStream_t st) {
   if (w.sinks == 0 || w.window == 0) return cudaSuccess;
-  window_sinks_kernel<T, Keys, Rows><<<dim3(min(w.B, kSinksGrid), w.Hkv, w.sinks), 256, 0, st>>>(w);
-  return cudaGetLastError();
+  return launch_behind(window_sinks_kernel<T, Keys, Rows>, dim3(min(w.B, kSinksGrid), w.Hkv, w.sinks), 256, 0, st, w);
 }
 
 }  // namespace seq
