@@ -29,10 +29,10 @@
 // float: 16 lanes share a row, two rows at a time, on CUDA cores.
 //
 // Measured: 48 sequences of 1 to 32,768 slots, 8 / 2 heads, bf16, 371 MB: 80 us,
-// 4.6 TB/s, and 5 us for the join (the rate between two sizes is 5.4 TB/s, and
-// 7.1 in float, where a warp turns half as often for the same bytes: each turn's
-// chain of wait, products, softmax and copies, with four warps a scheduler, is
-// what bounds bf16).  One sequence of 311 slots: 7 us.
+// 4.6 TB/s, and 3 us more for the join, which begins behind it.  On a like batch of
+// 407 MB (89 us) the arithmetic is 5 us of it and the look-up of the pages 8: what
+// bounds it is reading rows of 128 bytes and the two turns' starts (between two
+// sizes the rate is 5.4 TB/s, 7.1 in float).  One sequence of 311 slots: 7 us.
 #include "seq.cuh"
 #include "tc_ptx.cuh"
 

@@ -421,7 +421,8 @@ class PagedCache:
 
     Every sequence owns the pages of `capacity` slots.  With a `budget` (evict's), attend collects the attention
     weights and every sequence owns the pages of `budget` further slots, which evict fills and exchanges for the old
-    ones.  Nothing here waits for the device; check() does."""
+    ones.  No two rows of the table name the same page, and evict relies on that.  Rows beyond the capacity are not
+    written and set the error that check() raises.  Nothing here waits for the device; check() does."""
 
     def __init__(self, cfg: SeqConfig, batch: int, capacity: int, budget: int = 0, device="cuda"):
         st = validate_seq(cfg)

@@ -489,6 +489,20 @@ def test_append(p3, cuda_device, dtype):
             assert torch.equal(torch.nan_to_num(got, nan=9.0), torch.nan_to_num(want, nan=9.0))
 
 
+def test_append_reports_offsets_that_no_row_meets(p3, cuda_device):
+    dev = cuda_device
+    cfg = p3.make_seq_config(Hq=2, Hkv=1, page=16)
+    pages = [torch.zeros(12, 16, 1, 64, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    table = torch.arange(12, dtype=torch.int32, device=dev).view(3, 4)
+    lengths = torch.zeros(3, dtype=torch.int32, device=dev)
+    rows = torch.randn(20, 1, 64, device=dev).bfloat16()
+    for cu, want in (([0, 10, 5, 20], p3.DEVERR_LENGTHS), ([0, 10, 15, 21], p3.DEVERR_LENGTHS), ([0, 10, 10, 20], 0)):
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        p3.cache_append(cfg, rows, rows, *pages, table, lengths, torch.tensor(cu, dtype=torch.int32, device=dev),
+                        err=err)
+        assert int(err) == want
+
+
 def test_append_reports_what_does_not_fit(p3, cuda_device):
     """Rows behind the capacity, negative lengths, pages outside the pool and wrong offsets: reported, not written."""
     dev = cuda_device
