@@ -371,12 +371,15 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     if workspace is not None:
         _check_workspace(what, workspace, dev)
         n = workspace.numel() * workspace.element_size()
+    elif weights is not None and batch:                # always needs one
+        n = cache_attn_workspace_bytes(cfg, batch, max_pages, True)
+        workspace = _new(dev, torch.uint8, n)
     _check_err_word(what, err, dev, torch)
     args = (ctypes.byref(cfg), batch, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
             max_pages, k_pages.shape[0], lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), _p(weights),
             int(bool(accumulate)))
     st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, _p(workspace), n, _p(err))
-    if st == ERR_WORKSPACE and workspace is None:      # short calls need none: ask only when told so
+    if st == ERR_WORKSPACE and workspace is None:      # short calls need none: asked for only when missed
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
         workspace = _new(dev, torch.uint8, n)
         st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, workspace.data_ptr(), n, _p(err))
