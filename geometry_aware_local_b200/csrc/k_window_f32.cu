@@ -18,6 +18,8 @@
 //
 // What is hidden has P = 0; rows that 0 times a NaN or an infinity spoilt are
 // computed again (out_row, dq_row, dkv_row), as in the tensor-core kernels.
+#include <cooperative_groups.h>
+
 #include "seq_tc.cuh"
 #include "window_sinks.cuh"
 
@@ -178,7 +180,7 @@ __device__ __forceinline__ bool query_tile(const Win& w, int x, int grid, int g,
   if (bad) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_LENGTHS);
   } else if (w.zero_outside && g == 0) {
-    fill_outside(w, w.cu_q, w.Tq, tokens, x, grid, kThreads / 32, rows, w.Hq * kDh, 0u);
+    if (rows) fill_outside(w, w.cu_q, w.Tq, tokens, x, grid, kThreads / 32, rows, w.Hq * kDh, 0u);
     if (lse) fill_outside(w, w.cu_q, w.Tq, tokens, x, grid, kThreads / 32, lse, w.Hq, 0xff800000u);
   }
   return false;
@@ -280,11 +282,50 @@ __device__ __forceinline__ void store_grads(const Win& w, const Tile& s, int r0,
   }
 }
 
+// The backward's CTAs of a cluster (kSplit) share a tile's steps: this one takes
+// the steps [from, to) of n, and of the joined sums the rows [row0, row1) of 64.
+template <bool kSplit>
+struct Part {
+  int rank = 0, size = 1;
+  __device__ __forceinline__ Part() {
+    if constexpr (kSplit) {
+      rank = cooperative_groups::this_cluster().block_rank();
+      size = cooperative_groups::this_cluster().num_blocks();
+    }
+  }
+  __device__ __forceinline__ int from(int n) const { return (int)((long)n * rank / size); }
+  __device__ __forceinline__ int to(int n) const { return (int)((long)n * (rank + 1) / size); }
+  // Sum over the cluster of four floats at `at`, in the steps' order.
+  __device__ __forceinline__ float4 sum(float* at) const {
+    if constexpr (!kSplit) return at4(at);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z = 0; z < size; ++z) {
+      const float4 y = at4(cooperative_groups::this_cluster().map_shared_rank(at, z));
+      t.x += y.x;
+      t.y += y.y;
+      t.z += y.z;
+      t.w += y.w;
+    }
+    return t;
+  }
+  // Before the sums are read, and before a CTA ends.
+  __device__ __forceinline__ void meet() const {
+    if constexpr (kSplit) cooperative_groups::this_cluster().sync();
+    else __syncthreads();
+  }
+};
+__device__ __forceinline__ bool not_finite(float4 c) {
+  return !(fmaf(c.x, 0.f, fmaf(c.y, 0.f, fmaf(c.z, 0.f, c.w * 0.f))) == 0.f);
+}
+__device__ __forceinline__ float4 times(float4 c, float f) { return make_float4(c.x * f, c.y * f, c.z * f, c.w * f); }
+
 // dQ of query tile x; redo: 64 ints of shared memory.
+template <bool kSplit>
 __device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g, float* Q, int* redo) {
   float *D = Q + kTileFloats, *K = D + kTileFloats, *V = K + kTileFloats, *dS = V + kTileFloats;
+  const Part<kSplit> part;
   Tile s;
-  if (!query_tile(w, x, grid, g, &s, w.dq, nullptr)) return;
+  if (!query_tile(w, x, grid, g, &s, part.rank == 0 ? w.dq : nullptr, nullptr)) return;
   const int tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const KeyTiles<kKeys> kt = key_tiles<kKeys>(w, position(s, r0), position(s, r1));
@@ -308,7 +349,7 @@ __device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g,
   Micro o;
   zero(o);
 #pragma unroll 1
-  for (int t = 0; t < kt.n; ++t) {
+  for (int t = part.from(kt.n); t < part.to(kt.n); ++t) {
     const int k0 = kt.begin(t), cols = kt.cols(t);
     __syncthreads();
     load_rows(K, [&](int i) { return i < cols ? key_row(w, s, g, w.k, k0 + i) : nullptr; });
@@ -321,17 +362,21 @@ __device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g,
     __syncthreads();
     mul_nn(o, dS, K);
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
-    if (r > r1) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] *= w.scale;
-    const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
-    *reinterpret_cast<float4*>((float*)w.dq + at * kDh + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-    if (not_finite(o[i])) redo[row] = 1;
-  }
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    *reinterpret_cast<float4*>(dS + (ty + kSub * i) * kPad + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+  part.meet();
+#pragma unroll 1
+  for (int row = part.from(kRows) + ty; row < part.to(kRows); row += kSub) {
+    const int r = r0 + (row >> w.gshift);
+    if (r > r1) continue;
+    const float4 f = times(part.sum(dS + row * kPad + 4 * tx), w.scale);
+    const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
+    *reinterpret_cast<float4*>((float*)w.dq + at * kDh + 4 * tx) = f;
+    if (not_finite(f)) redo[row] = 1;
+  }
+  part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kRows; row += kThreads / 32)
     if (redo[row]) dq_row<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
@@ -339,15 +384,17 @@ __device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g,
 
 // dK and dV of key tile `at`, or from key_grid on of a piece of the sinks' far
 // queries.
+template <bool kSplit>
 __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int g, float* K, int* redo) {
   float *V = K + kTileFloats, *Q = V + kTileFloats, *D = Q + kTileFloats, *P = D + kTileFloats, *dS = P + kTileFloats;
+  const Part<kSplit> part;
   const bool far = at >= key_grid;
   const int x = far ? at - key_grid : at;
   const int tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   Tile s;
   bool bad;
   if (!(far ? find_far<kKeys, kRows>(w, x, &s, &bad) : find_tile(w, x, kKeys, true, &s, &bad))) {
-    if (!far && !bad && w.zero_outside && g == 0) {
+    if (!far && !bad && w.zero_outside && g == 0 && part.rank == 0) {
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh, 0u);
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dv, w.Hkv * kDh, 0u);
     }
@@ -370,11 +417,13 @@ __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int
   load_rows(K, [&](int i) { return key_row(w, s, g, w.k, j0 + i); });
   load_rows(V, [&](int i) { return key_row(w, s, g, w.v, j0 + i); });
   if (threadIdx.x < kKeys) redo[threadIdx.x] = 0;
+  const int steps = rb >= ra ? (rb - ra) / tokens + 1 : 0;
   Micro ak, av;
   zero(ak);
   zero(av);
 #pragma unroll 1
-  for (int rs = ra; rs <= rb; rs += tokens) {
+  for (int t = part.from(steps); t < part.to(steps); ++t) {
+    const int rs = ra + t * tokens;
     load_rows(Q, [&](int i) { return query_row(w, s, g, rs, rb, w.q, i); });
     load_rows(D, [&](int i) { return query_row(w, s, g, rs, rb, w.dout, i); });
     float lse2[kPer], delta[kPer];
@@ -402,27 +451,29 @@ __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int
     mul_tn(av, P, D);
     __syncthreads();
   }
-  if (ra > rb) loads_done();
-  const int slot = far ? x + s.b + 1 : part_slot<kRows>(w, s);      // of the sink rows' partial sums
+  if (part.from(steps) == part.to(steps)) loads_done();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int row = row_tn(i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) ak[i][j] *= w.scale;
-    const float4 fk = make_float4(ak[i][0], ak[i][1], ak[i][2], ak[i][3]);
-    const float4 fv = make_float4(av[i][0], av[i][1], av[i][2], av[i][3]);
+    *reinterpret_cast<float4*>(P + row_tn(i) * kPad + 4 * tx) = make_float4(ak[i][0], ak[i][1], ak[i][2], ak[i][3]);
+    *reinterpret_cast<float4*>(dS + row_tn(i) * kPad + 4 * tx) = make_float4(av[i][0], av[i][1], av[i][2], av[i][3]);
+  }
+  part.meet();
+  const int slot = far ? x + s.b + 1 : part_slot<kRows>(w, s);      // of the sink rows' partial sums
+#pragma unroll 1
+  for (int row = part.from(kKeys) + ty; row < part.to(kKeys); row += kSub) {
+    const float4 fk = times(part.sum(P + row * kPad + 4 * tx), w.scale), fv = part.sum(dS + row * kPad + 4 * tx);
     if (row < split_rows) {
       float4* dst = reinterpret_cast<float4*>(part_row(w, slot, g, row));
       dst[tx] = fk;
       dst[16 + tx] = fv;
     } else if (!far && j0 + row <= j1) {
-      const size_t at = ((size_t)(s.k0 + j0 + row) * w.Hkv + g) * kDh + 4 * tx;
-      *reinterpret_cast<float4*>((float*)w.dk + at) = fk;
-      *reinterpret_cast<float4*>((float*)w.dv + at) = fv;
-      if (not_finite(ak[i]) || not_finite(av[i])) redo[row] = 1;
+      const size_t to = ((size_t)(s.k0 + j0 + row) * w.Hkv + g) * kDh + 4 * tx;
+      *reinterpret_cast<float4*>((float*)w.dk + to) = fk;
+      *reinterpret_cast<float4*>((float*)w.dv + to) = fv;
+      if (not_finite(fk) || not_finite(fv)) redo[row] = 1;
     }
   }
-  __syncthreads();
+  part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kKeys; row += kThreads / 32)
     if (redo[row]) dkv_row<float>(w, s, j0 + row, g);
@@ -432,15 +483,16 @@ __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int
 // what the other writes (each forms <dout, out> of its rows).  The key sides come
 // first, as the longer ones (behind the query sides 6 % later), and a tile's
 // heads side by side (heads one after the other: up to a third later).
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2) window_bwd_f32_kernel(const Win w, int key_grid, int key_ctas,
                                                                      int query_ctas) {
   extern __shared__ float4 smem4[];
   __shared__ int redo[64];
   float* tiles = reinterpret_cast<float*>(smem4);
   let_next_begin();
-  const int x = blockIdx.x, y = x - key_ctas * w.Hkv;
-  if (y < 0) key_side(w, x / w.Hkv, key_grid, x % w.Hkv, tiles, redo);
-  else query_side(w, y / w.Hkv, query_ctas, y % w.Hkv, tiles, redo);
+  const int x = kSplit ? blockIdx.x / Part<kSplit>().size : blockIdx.x, y = x - key_ctas * w.Hkv;
+  if (y < 0) key_side<kSplit>(w, x / w.Hkv, key_grid, x % w.Hkv, tiles, redo);
+  else query_side<kSplit>(w, y / w.Hkv, query_ctas, y % w.Hkv, tiles, redo);
 }
 
 template <typename K>
@@ -465,14 +517,48 @@ cudaError_t launch_window_attn_f32(const Win& w, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st) {
-  cudaError_t e = allow(window_bwd_f32_kernel, 6);
+// CTAs of a cluster that share a tile, of `tiles` in the call: a share should be
+// eight steps long, two where the SMs would have four CTAs at most, one where
+// there is a CTA an SM at most.  `steps` is that of a key tile in a sequence of
+// the mean length.  (3,000 tokens, 2 / 1 heads, no window: 1 CTA 0.926 ms, 8 CTAs
+// 0.299; 1,000, 4 heads: 1, 4, 8: 163, 87, 117 us; 2,600, 8 / 2, window 300: 1, 2, 4:
+// 279, 231, 280; 1,000 in two, 8 heads, window 64, two steps: 1, 2: 37, 47.)
+int split_of(const Win& w, long tiles) {
+  const long mean = (w.Tq + w.B - 1) / w.B, rows = w.window > 0 ? min(mean, (long)w.window + kKeys) : mean;
+  const long steps = (rows * w.G + kRows - 1) / kRows, sms = sm_count();
+  auto good = [&](long S) {
+    return (tiles * S <= sms && steps >= S) || (tiles * S <= 4 * sms && steps >= 2 * S) ||
+           (tiles * S <= 8 * sms && steps >= 8 * S);
+  };
+  int S = 1;
+  while (S < 8 && good(2 * S)) S *= 2;
+  return S;
+}
+
+template <bool kSplit>
+cudaError_t launch_bwd(const Win& w, int key_grid, int key_ctas, int query_ctas, int S, cudaStream_t st) {
+  cudaError_t e = allow(window_bwd_f32_kernel<kSplit>, 6);
   if (e != cudaSuccess) return e;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = S;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(key_ctas + query_ctas) * w.Hkv * S);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 6 * kTileFloats * 4;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = kSplit ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, window_bwd_f32_kernel<kSplit>, w, key_grid, key_ctas, query_ctas);
+}
+
+cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st) {
   const int key_grid = (int)tile_grid(w.Tk, kKeys, w.B), key_ctas = key_grid + (int)far_grid<kRows>(w);
   const int query_ctas = (int)tile_grid(w.Tq, kRows >> w.gshift, w.B);
-  window_bwd_f32_kernel<<<(unsigned)(key_ctas + query_ctas) * w.Hkv, kThreads, 6 * kTileFloats * 4, st>>>(
-      w, key_grid, key_ctas, query_ctas);
-  e = cudaGetLastError();
+  const int S = split_of(w, ((long)key_ctas + query_ctas) * w.Hkv);
+  const cudaError_t e = S > 1 ? launch_bwd<true>(w, key_grid, key_ctas, query_ctas, S, st)
+                              : launch_bwd<false>(w, key_grid, key_ctas, query_ctas, 1, st);
   if (e != cudaSuccess) return e;
   return launch_window_sinks<float, kKeys, kRows>(w, st);
 }
