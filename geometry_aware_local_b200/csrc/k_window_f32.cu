@@ -158,9 +158,6 @@ __device__ __forceinline__ float row_sum(float x) {
   for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
 }
-__device__ __forceinline__ bool not_finite(const float* c) {
-  return !(fmaf(c[0], 0.f, fmaf(c[1], 0.f, fmaf(c[2], 0.f, c[3] * 0.f))) == 0.f);
-}
 
 // <dout, out> of the thread's row i, from its four dims of out.
 __device__ __forceinline__ float dot_row(const float* dout, int i, float4 y) {
@@ -186,13 +183,60 @@ __device__ __forceinline__ bool query_tile(const Win& w, int x, int grid, int g,
   return false;
 }
 
+// The CTAs of a cluster (kSplit) share a tile's steps: this one takes the steps
+// [from, to) of n, and as many of the tile's 64 rows of the joined sums.
+template <bool kSplit>
+struct Part {
+  int rank = 0, size = 1;
+  __device__ __forceinline__ Part() {
+    if constexpr (kSplit) {
+      rank = cooperative_groups::this_cluster().block_rank();
+      size = cooperative_groups::this_cluster().num_blocks();
+    }
+  }
+  __device__ __forceinline__ int from(int n) const { return (int)((long)n * rank / size); }
+  __device__ __forceinline__ int to(int n) const { return (int)((long)n * (rank + 1) / size); }
+  // CTA z's value of what is at `at` in this one's shared memory.
+  __device__ __forceinline__ float* of(float* at, int z) const {
+    if constexpr (kSplit) return cooperative_groups::this_cluster().map_shared_rank(at, z);
+    return at;
+  }
+  // Sum over the cluster of four floats at `at`, in the steps' order.
+  __device__ __forceinline__ float4 sum(float* at) const {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z = 0; z < (kSplit ? size : 1); ++z) {
+      const float4 y = at4(of(at, z));
+      t.x += y.x;
+      t.y += y.y;
+      t.z += y.z;
+      t.w += y.w;
+    }
+    return t;
+  }
+  // Before the sums are read, and before a CTA ends.
+  __device__ __forceinline__ void meet() const {
+    if constexpr (kSplit) cooperative_groups::this_cluster().sync();
+    else __syncthreads();
+  }
+};
+__device__ __forceinline__ bool not_finite(float4 c) {
+  return !(fmaf(c.x, 0.f, fmaf(c.y, 0.f, fmaf(c.z, 0.f, c.w * 0.f))) == 0.f);
+}
+__device__ __forceinline__ float4 times(float4 c, float f) { return make_float4(c.x * f, c.y * f, c.z * f, c.w * f); }
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win w) {
   extern __shared__ float4 smem4[];
   float* Q = reinterpret_cast<float*>(smem4);
   float *K = Q + kTileFloats, *V = K + kTileFloats, *P = V + kTileFloats;
   __shared__ int redo[kRows];
   Tile s;
-  if (!query_tile(w, blockIdx.x, gridDim.x, blockIdx.y, &s, w.out, w.lse)) return;
+  __shared__ float row_m[kRows], row_l[kRows];
+  const Part<kSplit> part;
+  const bool first = part.rank == 0;
+  if (!query_tile(w, blockIdx.x / part.size, gridDim.x / part.size, blockIdx.y, &s, first ? w.out : nullptr,
+                  first ? w.lse : nullptr))
+    return;
   const int g = blockIdx.y, tokens = kRows >> w.gshift, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int r0 = s.t * tokens, r1 = min(s.lq, r0 + tokens) - 1;
   const KeyTiles<kKeys> kt = key_tiles<kKeys>(w, position(s, r0), position(s, r1));
@@ -207,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win 
     l[i] = 0.f;
   }
 #pragma unroll 1
-  for (int t = 0; t < kt.n; ++t) {
+  for (int t = part.from(kt.n); t < part.to(kt.n); ++t) {
     const int k0 = kt.begin(t), cols = kt.cols(t);
     load_rows(K, [&](int i) { return i < cols ? key_row(w, s, g, w.k, k0 + i) : nullptr; });
     load_rows(V, [&](int i) { return i < cols ? key_row(w, s, g, w.v, k0 + i) : nullptr; });
@@ -241,22 +285,40 @@ __global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win 
     mul_nn(o, P, V);
     __syncthreads();
   }
-  if (kt.n == 0) loads_done();
+  if (part.from(kt.n) == part.to(kt.n)) loads_done();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
+    const int row = ty + kSub * i;
     const float sum = row_sum(l[i]);
-    // A row that sees no key: its O is 0, or a NaN from a hidden value.
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (r > r1) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] *= inv;
-    const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
-    *reinterpret_cast<float4*>((float*)w.out + at * kDh + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-    if (tx == 0 && w.lse) w.lse[at] = sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * 0.69314718f;
-    if (not_finite(o[i])) redo[row] = 1;
+    if (tx == 0) {
+      row_m[row] = m[i];
+      row_l[row] = sum;
+    }
+    *reinterpret_cast<float4*>(P + row * kPad + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
   }
-  __syncthreads();
+  part.meet();
+#pragma unroll 1
+  for (int row = part.from(kRows) + ty; row < part.to(kRows); row += kSub) {
+    const int r = r0 + (row >> w.gshift);
+    if (r > r1) continue;
+    // The shares of the row in the keys' order, on their largest maximum.
+    float top = -INFINITY, sum = 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z = 0; z < (kSplit ? part.size : 1); ++z) top = fmaxf(top, *part.of(row_m + row, z));
+    for (int z = 0; z < (kSplit ? part.size : 1); ++z) {
+      const float mz = *part.of(row_m + row, z), e = mz == top ? 1.f : exp2f(mz - top);
+      const float4 y = at4(part.of(P + row * kPad + 4 * tx, z));
+      sum = fmaf(*part.of(row_l + row, z), e, sum);
+      f = make_float4(fmaf(y.x, e, f.x), fmaf(y.y, e, f.y), fmaf(y.z, e, f.z), fmaf(y.w, e, f.w));
+    }
+    // A row that sees no key: its O is 0, or a NaN from a hidden value.
+    f = times(f, sum == 0.f ? 0.f : 1.f / sum);
+    const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
+    *reinterpret_cast<float4*>((float*)w.out + at * kDh + 4 * tx) = f;
+    if (tx == 0 && w.lse) w.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
+    if (not_finite(f)) redo[row] = 1;
+  }
+  part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kRows; row += kThreads / 32)
     if (redo[row]) out_row<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
@@ -281,43 +343,6 @@ __device__ __forceinline__ void store_grads(const Win& w, const Tile& s, int r0,
     }
   }
 }
-
-// The backward's CTAs of a cluster (kSplit) share a tile's steps: this one takes
-// the steps [from, to) of n, and of the joined sums the rows [row0, row1) of 64.
-template <bool kSplit>
-struct Part {
-  int rank = 0, size = 1;
-  __device__ __forceinline__ Part() {
-    if constexpr (kSplit) {
-      rank = cooperative_groups::this_cluster().block_rank();
-      size = cooperative_groups::this_cluster().num_blocks();
-    }
-  }
-  __device__ __forceinline__ int from(int n) const { return (int)((long)n * rank / size); }
-  __device__ __forceinline__ int to(int n) const { return (int)((long)n * (rank + 1) / size); }
-  // Sum over the cluster of four floats at `at`, in the steps' order.
-  __device__ __forceinline__ float4 sum(float* at) const {
-    if constexpr (!kSplit) return at4(at);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int z = 0; z < size; ++z) {
-      const float4 y = at4(cooperative_groups::this_cluster().map_shared_rank(at, z));
-      t.x += y.x;
-      t.y += y.y;
-      t.z += y.z;
-      t.w += y.w;
-    }
-    return t;
-  }
-  // Before the sums are read, and before a CTA ends.
-  __device__ __forceinline__ void meet() const {
-    if constexpr (kSplit) cooperative_groups::this_cluster().sync();
-    else __syncthreads();
-  }
-};
-__device__ __forceinline__ bool not_finite(float4 c) {
-  return !(fmaf(c.x, 0.f, fmaf(c.y, 0.f, fmaf(c.z, 0.f, c.w * 0.f))) == 0.f);
-}
-__device__ __forceinline__ float4 times(float4 c, float f) { return make_float4(c.x * f, c.y * f, c.z * f, c.w * f); }
 
 // dQ of query tile x; redo: 64 ints of shared memory.
 template <bool kSplit>
@@ -500,6 +525,50 @@ cudaError_t allow(K kernel, int tiles) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tiles * kTileFloats * 4);
 }
 
+// CTAs of a cluster that share a tile, of `tiles` in the call: a share should be
+// eight steps long, two where the SMs would have four CTAs at most, one where
+// there is a CTA an SM at most.  (Backward: 3,000 tokens, 2 / 1 heads, no window,
+// 1 CTA 0.926 ms, 8 CTAs 0.299; 1,000, 4 heads: 1, 4, 8 CTAs 163, 87, 117 us; 2,600,
+// 8 / 2 heads, window 300: 1, 2, 4: 279, 231, 280; 1,000 in two, 8 heads, window 64,
+// which is two steps: 1, 2: 37, 47.)
+int split_of(long tiles, long steps) {
+  const long sms = sm_count();
+  auto good = [&](long S) {
+    return (tiles * S <= sms && steps >= S) || (tiles * S <= 4 * sms && steps >= 2 * S) ||
+           (tiles * S <= 8 * sms && steps >= 8 * S);
+  };
+  int S = 1;
+  while (S < 8 && good(2 * S)) S *= 2;
+  return S;
+}
+
+// A kernel with `tiles` tiles of shared memory and clusters of S.
+template <typename... P, typename... A>
+cudaError_t launch_shared(void (*kernel)(P...), dim3 grid, int tiles, int S, cudaStream_t st, A... args) {
+  cudaError_t e = allow(kernel, tiles);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = S;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  grid.x *= S;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = tiles * kTileFloats * 4;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = S > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Tokens of a sequence of the mean length, at most those that a window reaches
+// from a tile of `tile` tokens.
+long reach(const Win& w, long tokens, long tile) {
+  const long mean = (tokens + w.B - 1) / w.B;
+  return w.window > 0 ? min(mean, (long)w.window + tile) : mean;
+}
+
 }  // namespace
 
 size_t window_bwd_part_bytes(const Win& w, int dtype) {
@@ -510,55 +579,22 @@ size_t window_bwd_part_bytes(const Win& w, int dtype) {
 }
 
 cudaError_t launch_window_attn_f32(const Win& w, cudaStream_t st) {
-  const cudaError_t e = allow(window_attn_f32_kernel, 4);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)tile_grid(w.Tq, kRows >> w.gshift, w.B), w.Hkv);
-  window_attn_f32_kernel<<<grid, kThreads, 4 * kTileFloats * 4, st>>>(w);
-  return cudaGetLastError();
-}
-
-// CTAs of a cluster that share a tile, of `tiles` in the call: a share should be
-// eight steps long, two where the SMs would have four CTAs at most, one where
-// there is a CTA an SM at most.  `steps` is that of a key tile in a sequence of
-// the mean length.  (3,000 tokens, 2 / 1 heads, no window: 1 CTA 0.926 ms, 8 CTAs
-// 0.299; 1,000, 4 heads: 1, 4, 8: 163, 87, 117 us; 2,600, 8 / 2, window 300: 1, 2, 4:
-// 279, 231, 280; 1,000 in two, 8 heads, window 64, two steps: 1, 2: 37, 47.)
-int split_of(const Win& w, long tiles) {
-  const long mean = (w.Tq + w.B - 1) / w.B, rows = w.window > 0 ? min(mean, (long)w.window + kKeys) : mean;
-  const long steps = (rows * w.G + kRows - 1) / kRows, sms = sm_count();
-  auto good = [&](long S) {
-    return (tiles * S <= sms && steps >= S) || (tiles * S <= 4 * sms && steps >= 2 * S) ||
-           (tiles * S <= 8 * sms && steps >= 8 * S);
-  };
-  int S = 1;
-  while (S < 8 && good(2 * S)) S *= 2;
-  return S;
-}
-
-template <bool kSplit>
-cudaError_t launch_bwd(const Win& w, int key_grid, int key_ctas, int query_ctas, int S, cudaStream_t st) {
-  cudaError_t e = allow(window_bwd_f32_kernel<kSplit>, 6);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = S;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(key_ctas + query_ctas) * w.Hkv * S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 6 * kTileFloats * 4;
-  cfg.stream = st;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = kSplit ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, window_bwd_f32_kernel<kSplit>, w, key_grid, key_ctas, query_ctas);
+  const int tokens = kRows >> w.gshift;
+  const long tiles = tile_grid(w.Tq, tokens, w.B);
+  const dim3 grid((unsigned)tiles, w.Hkv);
+  const int S = split_of(tiles * w.Hkv, (reach(w, w.Tk, tokens) + kKeys - 1) / kKeys);
+  return S > 1 ? launch_shared(window_attn_f32_kernel<true>, grid, 4, S, st, w)
+               : launch_shared(window_attn_f32_kernel<false>, grid, 4, 1, st, w);
 }
 
 cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st) {
   const int key_grid = (int)tile_grid(w.Tk, kKeys, w.B), key_ctas = key_grid + (int)far_grid<kRows>(w);
   const int query_ctas = (int)tile_grid(w.Tq, kRows >> w.gshift, w.B);
-  const int S = split_of(w, ((long)key_ctas + query_ctas) * w.Hkv);
-  const cudaError_t e = S > 1 ? launch_bwd<true>(w, key_grid, key_ctas, query_ctas, S, st)
-                              : launch_bwd<false>(w, key_grid, key_ctas, query_ctas, 1, st);
+  const dim3 grid((unsigned)(key_ctas + query_ctas) * w.Hkv);
+  const int S = split_of(grid.x, (reach(w, w.Tq, kKeys) * w.G + kRows - 1) / kRows);
+  const cudaError_t e =
+      S > 1 ? launch_shared(window_bwd_f32_kernel<true>, grid, 6, S, st, w, key_grid, key_ctas, query_ctas)
+            : launch_shared(window_bwd_f32_kernel<false>, grid, 6, 1, st, w, key_grid, key_ctas, query_ctas);
   if (e != cudaSuccess) return e;
   return launch_window_sinks<float, kKeys, kRows>(w, st);
 }

@@ -86,6 +86,7 @@ def test_hundreds_of_sequences(p3, cuda_device, Hq, Hkv, W, S, dtype):
     check_window(p3, lens, klens, Hq, Hkv, W, S, dtype, cuda_device)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("lens,klens,Hq,Hkv,W,S", [
     ([65], [65], 320, 320, 33, 64),                    # every key a sink
     ([300], [300], 240, 120, 33, 64),                  # two tiles of sinks
@@ -96,9 +97,9 @@ def test_hundreds_of_sequences(p3, cuda_device, Hq, Hkv, W, S, dtype):
     ([500], [500], 1024, 128, 100, 64),
     ([31, 32, 33], [64, 96, 160], 400, 200, 32, 33),
 ])
-def test_as_many_heads_as_fill_the_gpu(p3, cuda_device, lens, klens, Hq, Hkv, W, S):
-    """Enough tiles for the narrow key tiles of the bf16 forward, at the masks' edges."""
-    check_window(p3, lens, klens, Hq, Hkv, W, S, torch.bfloat16, cuda_device)
+def test_as_many_heads_as_fill_the_gpu(p3, cuda_device, lens, klens, Hq, Hkv, W, S, dtype):
+    """Enough tiles for the narrow key tiles of the bf16 forward, and for a CTA a tile in float, at the masks' edges."""
+    check_window(p3, lens, klens, Hq, Hkv, W, S, dtype, cuda_device)
 
 
 def test_hidden_nan_in_narrow_tiles(p3, cuda_device):
