@@ -251,7 +251,7 @@ cudaError_t launch_cache_evict(const Cache& c, const float* weights, int budget,
   const int chunks = c.Hkv * kDh * c.elem_bytes / 16;
   const long want = ((long)budget * chunks + 255) / 256;
   const dim3 grid((unsigned)min(want, 148L * 16), c.B);
-  return launch_behind(cache_move_kernel, grid, 256, 0, st, c, kept, budget, new_table, new_max_pages, chunks);
+  return launch_behind(cache_move_kernel, grid, 256, 0, st, 1, c, kept, budget, new_table, new_max_pages, chunks);
 }
 
 }  // namespace seq

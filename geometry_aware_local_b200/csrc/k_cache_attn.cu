@@ -748,7 +748,7 @@ cudaError_t launch_g(DecodeArgs& a, cudaStream_t st) {
   cache_attn_kernel<T, G><<<ctas, kThreads, kSmem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
-  return launch_behind(cache_join_kernel<T, G>, c.B * c.Hq, 256, 0, st, a);
+  return launch_behind(cache_join_kernel<T, G>, c.B * c.Hq, 256, 0, st, 1, a);
 }
 
 template <typename T>
@@ -791,7 +791,7 @@ cudaError_t launch_cache_attn(const Cache& c, int dtype, const void* q, void* ou
   cudaError_t e = dtype == PACK3D_BF16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
   if (e != cudaSuccess || !weights || c.cap == 0) return e;
   const dim3 grid((unsigned)((c.cap + 255) / 256), c.B);
-  return launch_behind(cache_weights_kernel, grid, 256, 0, st, c, a.logits, a.row_lse2, weights, (int)accumulate);
+  return launch_behind(cache_weights_kernel, grid, 256, 0, st, 1, c, a.logits, a.row_lse2, weights, (int)accumulate);
 }
 
 }  // namespace seq

@@ -25,7 +25,9 @@
 //   dK += dS^T Q and dV += P^T dout (M = 128 keys, N = 64, K = 64 rows).  Two
 //   groups of eight softmax warps take every other step, each with its own
 //   tensor memory.  Where no key of a warp is seen by any row of its chunk it
-//   writes zeros without an exponential.
+//   writes zeros without an exponential.  Where there are few key tiles the CTAs
+//   of a cluster share a tile's steps and join their dK and dV through each
+//   other's shared memory (split_of).
 //   65,536 tokens, window 1,024 / 8,192 tokens, 16 / 2 heads, no window, both
 //   kernels: S and dP by rows, dS and P through 64 KiB of shared memory for the
 //   second product 0.874 / - ms; transposed, with the terms added by the threads
@@ -47,6 +49,8 @@
 // A gradient row that is not finite may be spoilt by 0 times a NaN or an
 // infinity of a row it does not depend on; it is computed again from its
 // visible pairs alone (dq_row, dkv_row).
+#include <cooperative_groups.h>
+
 #include "seq_tc.cuh"
 #include "window_sinks.cuh"
 
@@ -464,6 +468,15 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kKeys, kStep, false);             // S^T, dP^T: N = 64 rows
 constexpr uint32_t kIdescKV = ptx::idesc_bf16_f32(kKeys, kDh, true);               // dK, dV: B MN-major
 
+// A CTA's share of a tile whose steps a cluster splits, over its stages (which
+// are idle by then): each key's dK and dV.
+struct Share {
+  float o[kKeys][2 * kDh + 4];
+};
+static_assert(sizeof(Share) <= kStages * kStageBytes, "share slot");
+
+// kSplit: the CTAs of a cluster share the tile's steps.
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -491,8 +504,14 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
   const int tokens = kStep >> w.gshift;
   let_next_begin();
-  const bool far = (int)blockIdx.x >= key_grid;         // a CTA of the sinks' far queries
-  const int x = far ? blockIdx.x - key_grid : blockIdx.x;
+  int rank = 0, size = 1;
+  if constexpr (kSplit) {
+    rank = cooperative_groups::this_cluster().block_rank();
+    size = cooperative_groups::this_cluster().num_blocks();
+  }
+  const int at = blockIdx.x / size;
+  const bool far = at >= key_grid;                      // a CTA of the sinks' far queries
+  const int x = far ? at - key_grid : at;
 
   if (warp == 0) {
     Tile s;
@@ -534,7 +553,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   __syncthreads();
   wait_for_last();                                      // for delta and the rows' terms
   if (*found_slot != 1) {
-    if (!far && *found_slot == 0 && w.zero_outside && blockIdx.y == 0) {
+    if (!far && *found_slot == 0 && w.zero_outside && blockIdx.y == 0 && rank == 0) {
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dk, w.Hkv * kDh / 2, 0u);
       fill_outside(w, w.cu_k, w.Tk, kKeys, x, key_grid, kThreads / 32, w.dv, w.Hkv * kDh / 2, 0u);
     }
@@ -561,7 +580,11 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     rb = s.lq - 1;
     if (w.window > 0) rb = min(rb, j1 + w.window - 1 - shift);
   }
-  const int nsteps = rb >= ra ? (rb - ra) / tokens + 1 : 0;
+  const int all = rb >= ra ? (rb - ra) / tokens + 1 : 0;
+  // This CTA's steps.
+  const int first = kSplit ? (int)((long)all * rank / size) : 0;
+  const int nsteps = kSplit ? (int)((long)all * (rank + 1) / size) - first : all;
+  ra += first * tokens;
   // Rows below `split_rows` of this tile leave float partial sums.
   const bool shared = far || (j0 == 0 && far_pieces<kKeys, kRowsPerTile>(w, s.lq, s.lk) > 0);
   const int split_rows = shared ? min(w.sinks, s.lk) : 0;
@@ -729,31 +752,39 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      const float f = is_k ? w.scale : 1.f;
-      float sum = 0.f;                                 // not finite where any element is not
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float y = __uint_as_float(o[e]) * f;
-        sum = fmaf(y, 0.f, sum);
-        o[e] = __float_as_uint(y);
-      }
-      const int slot = far ? x + s.b + 1 : part_slot<kRowsPerTile>(w, s);       // of the sink rows' partial sums
-      if (rl < split_rows) {
-        float4* dst = reinterpret_cast<float4*>(part_row(w, slot, g, rl) + col0);
+      if constexpr (kSplit) {
+        Share* mine = reinterpret_cast<Share*>(smem + kStageOff);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
-                               __uint_as_float(o[4 * q + 3]));
-      } else if (!far && j0 + rl <= j1) {
-        __nv_bfloat16* base = (__nv_bfloat16*)(is_k ? w.dk : w.dv);
-        uint4* dst = reinterpret_cast<uint4*>(base + ((size_t)(s.k0 + j0 + rl) * w.Hkv + g) * kDh + (col0 % kDh));
+          *reinterpret_cast<uint4*>(&mine->o[rl][col0 + 4 * q]) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2],
+                                                                              o[4 * q + 3]);
+      } else {
+        const float f = is_k ? w.scale : 1.f;
+        float sum = 0.f;                                 // not finite where any element is not
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float* y = reinterpret_cast<const float*>(o + 8 * q);
-          dst[q] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                              pack_bf16x2(y[6], y[7]));
+        for (int e = 0; e < 32; ++e) {
+          const float y = __uint_as_float(o[e]) * f;
+          sum = fmaf(y, 0.f, sum);
+          o[e] = __float_as_uint(y);
         }
-        if (!(sum == 0.f)) redo[rl] = 1;
+        const int slot = far ? x + s.b + 1 : part_slot<kRowsPerTile>(w, s);       // of the sink rows' partial sums
+        if (rl < split_rows) {
+          float4* dst = reinterpret_cast<float4*>(part_row(w, slot, g, rl) + col0);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                                 __uint_as_float(o[4 * q + 3]));
+        } else if (!far && j0 + rl <= j1) {
+          __nv_bfloat16* base = (__nv_bfloat16*)(is_k ? w.dk : w.dv);
+          uint4* dst = reinterpret_cast<uint4*>(base + ((size_t)(s.k0 + j0 + rl) * w.Hkv + g) * kDh + (col0 % kDh));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* y = reinterpret_cast<const float*>(o + 8 * q);
+            dst[q] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                pack_bf16x2(y[6], y[7]));
+          }
+          if (!(sum == 0.f)) redo[rl] = 1;
+        }
       }
     }
   }
@@ -781,6 +812,34 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+  if constexpr (kSplit) {
+    // Every CTA of the cluster comes here, whatever its waits did.  Each joins its
+    // part of the keys, a warp a key (lanes 0-15 dK, 16-31 dV), in the steps' order.
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    Share* mine = reinterpret_cast<Share*>(smem + kStageOff);
+    const int slot = far ? x + s.b + 1 : part_slot<kRowsPerTile>(w, s);
+#pragma unroll 1
+    for (int row = kKeys * rank / size + warp; row < kKeys * (rank + 1) / size; row += kThreads / 32) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int z = 0; z < size; ++z) {
+        const float4 a = *reinterpret_cast<const float4*>(&cluster.map_shared_rank(mine, z)->o[row][4 * lane]);
+        y = make_float4(y.x + a.x, y.y + a.y, y.z + a.z, y.w + a.w);
+      }
+      const float f = lane < 16 ? w.scale : 1.f;
+      y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+      if (row < split_rows) {
+        reinterpret_cast<float4*>(part_row(w, slot, g, row))[lane] = y;
+      } else if (!far && j0 + row <= j1) {
+        __nv_bfloat16* base = (__nv_bfloat16*)(lane < 16 ? w.dk : w.dv);
+        reinterpret_cast<uint2*>(base + ((size_t)(s.k0 + j0 + row) * w.Hkv + g) * kDh)[lane & 15] =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        const float zero = fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, y.w * 0.f)));
+        if (__any_sync(0xffffffffu, !(zero == 0.f)) && lane == 0) redo[row] = 1;
+      }
+    }
+    cluster.sync();           // no CTA ends while another reads its share
+  }
   if (ctl->abort) {
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
     return;
@@ -790,6 +849,23 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 }  // namespace k_side
+
+// CTAs of a cluster that share a key tile's steps: a share should be four steps
+// long where every CTA has an SM of its own, and 64 where some SMs get a second
+// one, which pays where the tiles' lengths differ.  (Both kernels, no window:
+// 2,048 tokens, 8 / 2 heads, 1, 4, 8 CTAs 97, 55, 72 us; 4,096, 1, 2, 4 CTAs 198, 140,
+// 121; 8,192, 16 / 2 heads, 1, 2 CTAs 758, 512; window 512, 2,048 tokens, 1, 4, 8 CTAs
+// 45, 39, 47.)
+int split_of(const Win& w, long key_ctas) {
+  const long mean = (w.Tq + w.B - 1) / w.B, rows = w.window > 0 ? min(mean, (long)w.window + k_side::kKeys) : mean;
+  const long steps = (rows * w.G + k_side::kStep - 1) / k_side::kStep, tiles = key_ctas * w.Hkv, sms = sm_count();
+  auto good = [&](long S) {
+    return (tiles * S <= sms && steps >= 4 * S) || (tiles * S <= 2 * sms && steps >= 64 * S);
+  };
+  int S = 1;
+  while (S < 8 && good(2 * S)) S *= 2;
+  return S;
+}
 
 // Win::terms viewed as [2][Tq][Hkv][G][8]: boxes of both planes of a step's rows.
 inline bool map_terms(CUtensorMap* m, const Win& w) {
@@ -807,7 +883,10 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(q_side::window_dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        q_side::kSmemBytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_side::window_dkv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_side::window_dkv_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             k_side::kSmemBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_side::window_dkv_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              k_side::kSmemBytes);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, to, tk, tv, tk128, tv128, tq64, to64, tt;
@@ -821,9 +900,13 @@ cudaError_t launch_window_bwd_tc(const Win& w, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int key_grid = (int)tile_grid(w.Tk, k_side::kKeys, w.B);
-  const dim3 gk((unsigned)(key_grid + far_grid<kRowsPerTile>(w)), w.Hkv);
-  e = launch_behind(k_side::window_dkv_tc_kernel, gk, k_side::kThreads, k_side::kSmemBytes, st, tq64, to64, tk128, tv128,
-                    tt, w, key_grid);
+  const long key_ctas = key_grid + far_grid<kRowsPerTile>(w);
+  const int S = split_of(w, key_ctas);
+  const dim3 gk((unsigned)(key_ctas * S), w.Hkv);
+  e = S > 1 ? launch_behind(k_side::window_dkv_tc_kernel<true>, gk, k_side::kThreads, k_side::kSmemBytes, st, S, tq64, to64,
+                            tk128, tv128, tt, w, key_grid)
+            : launch_behind(k_side::window_dkv_tc_kernel<false>, gk, k_side::kThreads, k_side::kSmemBytes, st, 1, tq64,
+                            to64, tk128, tv128, tt, w, key_grid);
   if (e != cudaSuccess) return e;
   return launch_window_sinks<__nv_bfloat16, k_side::kKeys, kRowsPerTile>(w, st);
 }

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256) window_sinks_kernel(const Win w) {
 template <typename T, int Keys, int Rows>
 cudaError_t launch_window_sinks(const Win& w, cudaStream_t st) {
   if (w.sinks == 0 || w.window == 0) return cudaSuccess;
-  return launch_behind(window_sinks_kernel<T, Keys, Rows>, dim3(min(w.B, kSinksGrid), w.Hkv, w.sinks), 256, 0, st, w);
+  return launch_behind(window_sinks_kernel<T, Keys, Rows>, dim3(min(w.B, kSinksGrid), w.Hkv, w.sinks), 256, 0, st, 1, w);
 }
 
 }  // namespace seq

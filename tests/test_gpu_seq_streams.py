@@ -64,6 +64,28 @@ def test_hidden_nan_in_a_shared_tile(p3):
     assert torch.isnan(out[:2].float()).all() and torch.isnan(out[30:].float()).all()
 
 
+@pytest.mark.parametrize("lens,klens,Hq,Hkv,W,S", [
+    ([1100], [1100], 8, 2, 0, 0), ([900, 1, 300], [900, 1, 300], 4, 1, 700, 5), ([130], [700], 8, 1, 0, 0),
+    ([2100], [2100], 8, 1, 100, 64), ([700], [650], 2, 1, 0, 0), ([1500], [1500], 1, 1, 300, 2),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_of_few_tiles(p3, lens, klens, Hq, Hkv, W, S, dtype):
+    """The CTAs of a cluster share a tile's steps in the backward, some of them without one."""
+    q, k, v, dout = (t.to(dtype) for t in tensors(sum(lens), sum(klens), Hq, Hkv))
+    cfg = p3.make_seq_config(Hq=Hq, Hkv=Hkv, window=W, sinks=S, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+    cu_q, cu_k = offsets(lens), offsets(klens)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = p3.window_attn(cfg, q, k, v, cu_q, cu_k, err=err)
+    grads = p3.window_attn_bwd(cfg, q, k, v, cu_q, cu_k, out, lse, dout, err=err)
+    again = p3.window_attn_bwd(cfg, q, k, v, cu_q, cu_k, out, lse, dout, err=err)
+    assert p3.check_status(err) == 0
+    r = ref.window(q, k, v, lens, klens, W, S, cfg.softmax_scale, dout)
+    ref.close(out, r["out"], r["out_tol"], "out")
+    for n, a, b in zip(("dq", "dk", "dv"), grads, again):
+        ref.close(a, r[n], r[n + "_tol"], n)
+        assert torch.equal(a, b)
+
+
 # ---- bounded waits -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("lens,klens,W,S", [([5], [5], 0, 0), ([700], [700], 100, 4), ([70], [4000], 0, 0),
