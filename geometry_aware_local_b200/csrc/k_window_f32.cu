@@ -11,10 +11,12 @@
 // kept in 32 bits, two multiply-adds an instruction.  Bound: the shared-memory
 // reads (8 loads of 16 bytes per 64 multiply-adds and thread; 77 % of their
 // rate).  128 threads with 8 x 4 values read less, but where a call has few
-// tiles their warps are too few.  2,050 tokens in three sequences, 4 / 2 heads,
-// window 200, one sink: forward 33 us (128 threads, a multiply-add an
-// instruction: 42), backward 119 us (166, with the two sides one after the
-// other).  16,384 tokens, 8 / 2 heads: 0.323 and 1.05 ms (0.330, 1.14).
+// tiles their warps are too few.  There the CTAs of a cluster share a tile besides,
+// and join what they have through each other's shared memory.  2,050 tokens in
+// three sequences, 4 / 2 heads, window 200, one sink: forward 34 us (128 threads, a
+// multiply-add an instruction: 42), backward 99 us (166, with the two sides one
+// after the other and a CTA a tile).  16,384 tokens, 8 / 2 heads: 0.323 and 1.05 ms
+// (0.330, 1.14).
 //
 // What is hidden has P = 0; rows that 0 times a NaN or an infinity spoilt are
 // computed again (out_row, dq_row, dkv_row), as in the tensor-core kernels.
@@ -332,7 +334,8 @@ __device__ __forceinline__ void store_grads(const Win& w, const Tile& s, int r0,
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int row = ty + kSub * i, r = r0 + (row >> w.gshift), p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
+    const int row = ty + kSub * i, r = r0 + (row >> w.gshift);
+    const int p = r <= r1 ? position(s, r) : -1, low = window_low(w, p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = tx + 16 * j, key = k0 + col;
@@ -526,15 +529,17 @@ cudaError_t allow(K kernel, int tiles) {
 }
 
 // CTAs of a cluster that share a tile, of `tiles` in the call: a share should be
-// eight steps long, two where the SMs would have four CTAs at most, one where
-// there is a CTA an SM at most.  (Backward: 3,000 tokens, 2 / 1 heads, no window,
-// 1 CTA 0.926 ms, 8 CTAs 0.299; 1,000, 4 heads: 1, 4, 8 CTAs 163, 87, 117 us; 2,600,
-// 8 / 2 heads, window 300: 1, 2, 4: 279, 231, 280; 1,000 in two, 8 heads, window 64,
-// which is two steps: 1, 2: 37, 47.)
-int split_of(long tiles, long steps) {
+// eight steps long, `least` where the SMs would have four CTAs at most (two in the
+// backward; the forward's are half as long: four), one where there is a CTA an SM
+// at most.  (Backward: 3,000 tokens, 2 / 1 heads, no window, 1 CTA 0.926 ms, 8 CTAs
+// 0.299; 1,000, 4 heads: 1, 4, 8 CTAs 163, 87, 117 us; 2,600, 8 / 2 heads, window
+// 300: 1, 2, 4: 279, 231, 280; 1,000 in two, 8 heads, window 64, which is two steps:
+// 1, 2: 37, 47.  Forward: the first 255 us with 1, 95 with 4; 2,050 in three, window
+// 200, four steps: 1, 2: 34, 38.)
+int split_of(long tiles, long steps, long least) {
   const long sms = sm_count();
   auto good = [&](long S) {
-    return (tiles * S <= sms && steps >= S) || (tiles * S <= 4 * sms && steps >= 2 * S) ||
+    return (tiles * S <= sms && steps >= S) || (tiles * S <= 4 * sms && steps >= least * S) ||
            (tiles * S <= 8 * sms && steps >= 8 * S);
   };
   int S = 1;
@@ -582,7 +587,7 @@ cudaError_t launch_window_attn_f32(const Win& w, cudaStream_t st) {
   const int tokens = kRows >> w.gshift;
   const long tiles = tile_grid(w.Tq, tokens, w.B);
   const dim3 grid((unsigned)tiles, w.Hkv);
-  const int S = split_of(tiles * w.Hkv, (reach(w, w.Tk, tokens) + kKeys - 1) / kKeys);
+  const int S = split_of(tiles * w.Hkv, (reach(w, w.Tk, tokens) + kKeys - 1) / kKeys, 4);
   return S > 1 ? launch_shared(window_attn_f32_kernel<true>, grid, 4, S, st, w)
                : launch_shared(window_attn_f32_kernel<false>, grid, 4, 1, st, w);
 }
@@ -591,7 +596,7 @@ cudaError_t launch_window_bwd_f32(const Win& w, cudaStream_t st) {
   const int key_grid = (int)tile_grid(w.Tk, kKeys, w.B), key_ctas = key_grid + (int)far_grid<kRows>(w);
   const int query_ctas = (int)tile_grid(w.Tq, kRows >> w.gshift, w.B);
   const dim3 grid((unsigned)(key_ctas + query_ctas) * w.Hkv);
-  const int S = split_of(grid.x, (reach(w, w.Tq, kKeys) * w.G + kRows - 1) / kRows);
+  const int S = split_of(grid.x, (reach(w, w.Tq, kKeys) * w.G + kRows - 1) / kRows, 2);
   const cudaError_t e =
       S > 1 ? launch_shared(window_bwd_f32_kernel<true>, grid, 6, S, st, w, key_grid, key_ctas, query_ctas)
             : launch_shared(window_bwd_f32_kernel<false>, grid, 6, 1, st, w, key_grid, key_ctas, query_ctas);
