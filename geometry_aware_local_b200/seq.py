@@ -245,19 +245,11 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     if workspace is not None:
         _check_workspace(what, workspace, dev)
     _check_err_word(what, err, dev, torch)
-    return _window_bwd(torch, what, cfg, q, k, v, cu_q, cu_k, out, lse, dout, None if new else (dq, dk, dv), workspace,
-                       err, stream)
-
-
-def _window_bwd(torch, what, cfg, q, k, v, cu_q, cu_k, out, lse, dout, grads, workspace, err, stream):
-    """window_attn_bwd behind its checks; grads None: made here."""
-    new = grads is None
     if new:
-        grads = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
-            return tuple(t.zero_() for t in grads)
-    dq, dk, dv = grads
-    batch, q_rows, k_rows, dev = cu_q.shape[0] - 1, q.shape[0], k.shape[0], q.device
+            return dq.zero_(), dk.zero_(), dv.zero_()
+    batch, q_rows, k_rows = cu_q.shape[0] - 1, q.shape[0], k.shape[0]
     if workspace is None:
         n = window_attn_bwd_workspace_bytes(cfg, batch, q_rows, k_rows)
         workspace = _new(dev, torch.uint8, max(n, 256))
@@ -266,7 +258,7 @@ def _window_bwd(torch, what, cfg, q, k, v, cu_q, cu_k, out, lse, dout, grads, wo
     _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), batch, q_rows, k_rows,
           cu_q.data_ptr(), cu_k.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
           dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), int(new), workspace.data_ptr(), n, _p(err))
-    return grads
+    return dq, dk, dv
 
 
 def window_attention(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, err=None):
@@ -298,10 +290,11 @@ def _autograd():
             @staticmethod
             @once_differentiable
             def backward(ctx, dout):
-                q, k, v, cu_q, cu_k, out, lse = ctx.saved_tensors      # checked by the forward
-                dq, dk, dv = _window_bwd(torch, "pack3d_window_attn_bwd", ctx.cfg, q, k, v, cu_q, cu_k, out, lse,
-                                         dout.to(q.dtype).contiguous(), None, None, ctx.err, None)
-                return None, dq, dk, dv, None, None, None
+                # Saved-tensor hooks may give back other tensors than the forward saved: of equal values but other
+                # strides, which is put right here, or of another type or device, which the call refuses.
+                saved = [t.contiguous() for t in ctx.saved_tensors]
+                return None, *window_attn_bwd(ctx.cfg, *saved, dout.to(saved[0].dtype).contiguous(),
+                                              err=ctx.err), None, None, None
 
         _autograd_class = WindowAttention
     return _autograd_class
