@@ -707,7 +707,9 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const Cache c, const
     if (i >= 0)
       for (int h = 0; h < c.Hq; ++h) {
         const size_t at = (size_t)b * c.Hq + h;
-        total += ptx::ex2(logits[at * c.cap + i] - row_lse2[at]);
+        // A head whose scores are all -infinity has no weight to give, as its output is 0.
+        const float lse2 = row_lse2[at];
+        if (lse2 != -INFINITY) total += ptx::ex2(logits[at * c.cap + i] - lse2);
       }
     float* dst = weights + (size_t)b * c.cap + j;
     *dst = accumulate ? *dst + total : total;

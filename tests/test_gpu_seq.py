@@ -394,6 +394,35 @@ def test_decode(p3, cuda_device, lengths, page, Hq, Hkv, W, S, dtype):
     ref.close(added[inside], r["weights"][inside] + 2.0, r["weights_tol"][inside] + 2.0 ** -24 * (2 + Hq), "added")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lengths,page", [([50, 9], 16), ([3000, 700, 1], 64)], ids=["short", "split"])
+def test_decode_where_no_score_is_finite(p3, cuda_device, lengths, page, dtype):
+    """Heads whose visible scores are all -infinity: output 0, log-sum-exp -infinity and no weight; the other heads and
+    sequences as ever.  With accumulate nothing but their weights is added."""
+    dev = cuda_device
+    k, v, table, n, _ = make_cache(lengths, page, 2, dtype, dev)
+    q = torch.randn(len(lengths), 8, 64, device=dev, generator=torch.Generator(device=dev).manual_seed(1)).to(dtype)
+    cfg = p3.make_seq_config(page=page, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+    r = ref.decode(q[:, 4:], k[:, :, 1:], v[:, :, 1:], table, n, 0, 0, cfg.softmax_scale)
+    # key head 0: -infinity in one dim of every row of the first sequence, met by a positive query there
+    used = table[0, :-(-lengths[0] // page)].long()
+    k[used, :, 0, 7] = -float("inf")
+    q[:, :4, 7] = 1.0
+    whole = ref.decode(q[1:], k, v, table[1:], n[1:], 0, 0, cfg.softmax_scale)
+    weights = torch.zeros(len(lengths), table.shape[1] * page, device=dev)
+    out, lse = p3.cache_attn(cfg, q, k, v, table, n, weights=weights)
+    added = torch.full_like(weights, 2.0)
+    p3.cache_attn(cfg, q, k, v, table, n, weights=added, accumulate=True)
+    assert (out[0, :4] == 0).all() and (lse[0, :4] == -float("inf")).all()
+    ref.close(out[:, 4:], r["out"], r["out_tol"], "out")
+    ref.close(out[1:], whole["out"], whole["out_tol"], "out")
+    ref.close(weights[0], r["weights"][0], r["weights_tol"][0], "weights")
+    ref.close(weights[1:], whole["weights"], whole["weights_tol"], "weights")
+    inside = torch.arange(weights.shape[1], device=dev)[None] < n[:, None]
+    assert (added[~inside] == 2.0).all()
+    ref.close(added[0], r["weights"][0] + 2.0, r["weights_tol"][0] + 2.0 ** -24 * 10, "added")
+
+
 def test_decode_is_window_attention_of_one_query(p3, cuda_device):
     """The same tokens through the packed operator and through the cache."""
     dev = cuda_device
