@@ -118,18 +118,6 @@ def _torch():
     return _modules[0]
 
 
-_templates = {}
-
-
-def _new(device, dtype, *shape):
-    """torch.empty, from an empty tensor of the device and type: it takes half as long as naming both."""
-    key = device.index, dtype
-    t = _templates.get(key)
-    if t is None:
-        t = _templates[key] = _torch()[0].empty(0, dtype=dtype, device=device)
-    return t.new_empty(*shape)
-
-
 def _check_err_word(what, err, device, torch):
     if err is not None and (err.dtype != torch.int32 or err.numel() < 1 or err.device != device):
         raise ValueError(f"{what}: the error word must be an int32 tensor of at least one element on {device}")
@@ -207,7 +195,7 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
     new = out is None
     if new:
         out = torch.empty_like(q)
-        lse = _new(dev, torch.float32, q.shape[0], cfg.Hq)
+        lse = q.new_empty((q.shape[0], cfg.Hq), dtype=torch.float32)
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
             return out.zero_(), lse.fill_(-math.inf)
     else:
@@ -252,7 +240,7 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     batch, q_rows, k_rows = cu_q.shape[0] - 1, q.shape[0], k.shape[0]
     if workspace is None:
         n = window_attn_bwd_workspace_bytes(cfg, batch, q_rows, k_rows)
-        workspace = _new(dev, torch.uint8, max(n, 256))
+        workspace = q.new_empty(max(n, 256), dtype=torch.uint8)
     else:
         n = workspace.numel() * workspace.element_size()
     _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), batch, q_rows, k_rows,
@@ -355,7 +343,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     else:
         _require(what, cfg, "out", out, T, tuple(q.shape), dev)
     if lse is None:
-        lse = _new(dev, torch.float32, batch, cfg.Hq)
+        lse = q.new_empty((batch, cfg.Hq), dtype=torch.float32)
     else:
         _require(what, cfg, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
     if weights is not None:
@@ -366,7 +354,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
         n = workspace.numel() * workspace.element_size()
     elif weights is not None and batch:                # always needs one
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, True)
-        workspace = _new(dev, torch.uint8, n)
+        workspace = q.new_empty(n, dtype=torch.uint8)
     _check_err_word(what, err, dev, torch)
     args = (ctypes.byref(cfg), batch, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
             max_pages, k_pages.shape[0], lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), _p(weights),
@@ -374,7 +362,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, _p(workspace), n, _p(err))
     if st == ERR_WORKSPACE and workspace is None:      # short calls need none: asked for only when missed
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
-        workspace = _new(dev, torch.uint8, n)
+        workspace = q.new_empty(n, dtype=torch.uint8)
         st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, workspace.data_ptr(), n, _p(err))
     if st != 0:
         raise Pack3DError(st, what)
@@ -400,7 +388,7 @@ def cache_evict(cfg: SeqConfig, k_pages, v_pages, table, lengths, weights, new_t
     for name, t, dt, shape in (("kept", kept, torch.int32, shapes[0]), ("new_weights", new_weights, torch.float32,
                                shapes[1]), ("new_lengths", new_lengths, torch.int32, shapes[2])):
         if t is None:
-            t = _new(dev, dt, *shape)
+            t = table.new_empty(shape, dtype=dt)
         else:
             _require(what, cfg, name, t, dt, shape, dev)
         outs.append(t)

@@ -1,4 +1,4 @@
-"""The differentiable sequence operator inside PyTorch: saved-tensor hooks."""
+"""The sequence operators inside PyTorch: saved-tensor hooks, fake tensors."""
 import pytest
 import torch
 
@@ -52,3 +52,27 @@ def test_saved_tensors_that_are_something_else(p3, unpack, match):
         o = p3.window_attention(cfg, *leaves, cu)
     with pytest.raises(ValueError, match=match):
         torch.autograd.grad(o, leaves, dout)
+
+
+def test_a_call_with_fake_tensors_leaves_nothing_behind(p3):
+    """Under FakeTensorMode there is no memory to run on: the call is refused, and the next one, on tensors that exist,
+    makes its results and workspaces of memory that exists too."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    q, k, v, dout = tensors(100, 8, 2)
+    cfg = p3.make_seq_config(window=16, sinks=2, page=16)
+    cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    with FakeTensorMode() as mode, pytest.warns(UserWarning, match="data pointer"):
+        with pytest.raises(p3.Pack3DError):
+            p3.window_attn(cfg, *(mode.from_tensor(t) for t in (q, k, v, cu)))
+    out, lse = p3.window_attn(cfg, q, k, v, cu)
+    grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, out, lse, dout)
+    cache = p3.PagedCache(cfg, 1, 2048, budget=32)
+    cache.append(k, v, cu)
+    got, got_lse = p3.cache_attn(cfg, q[99:], cache.k_pages, cache.v_pages, cache.table, cache.lengths)
+    kept = cache.evict(8)
+    cache.check()
+    for t in (out, lse, *grads, got, got_lse, kept):
+        assert type(t) is torch.Tensor and t.data_ptr() != 0
+    ref_lse = torch.logsumexp((q[99].double().view(2, 4, 64) @ torch.cat((k[:2], k[84:])).double().permute(1, 2, 0)) / 8, -1)
+    assert torch.allclose(lse[99].double(), ref_lse.view(-1), atol=1e-4)
+    assert torch.allclose(got_lse[0].double(), ref_lse.view(-1), atol=1e-4)
