@@ -97,8 +97,8 @@ constexpr int kStages = 8;
 constexpr int kQOff = 0, kDOOff = kQTileBytes, kStageOff = 2 * kQTileBytes;
 constexpr int kStageBytes = 2 * kKVBytes;       // K at +0, V at +kKVBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2]
-constexpr int kNumBars = 2 * kStages + 12;
+// barriers: full[S], empty[S], qfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], cleared
+constexpr int kNumBars = 2 * kStages + 13;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kHalfOff = kCtlOff + 32;          // float [2][128]: the groups' shares of D
 constexpr int kRedoOff = kHalfOff + 2 * kRowsPerTile * 4;       // one byte per row
@@ -134,6 +134,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto p_full = [&](int b) { return qfull + 48 + 8 * b; };
   auto p_free = [&](int b) { return qfull + 64 + 8 * b; };
   auto drain = [&](int i) { return qfull + 80 + 8 * i; };
+  const uint32_t cleared = qfull + 96;
   float* shares = reinterpret_cast<float*>(smem + kHalfOff);
   volatile uint8_t* redo = smem + kRedoOff;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
@@ -162,6 +163,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ptx::mbar_init(drain(b), 1);
     }
     ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(cleared, 1);
     ctl->abort = 0;
     ctl->issued = 0;
     ctl->limit_ns = w.wait_ns;
@@ -184,6 +186,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const SmallTiles kt = small_tiles(w, p0, p1);
   const int T = kt.n, T_load = w.stall ? T - 1 : T;
   const int first = T <= kTwice ? T : 0;      // steps of the first pass
+  const bool tail = T > 0 && kt.begin(T - 1) + kBN > s.lk;      // the last tile reaches behind the sequence's end
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
@@ -220,6 +223,13 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ctl->issued = issued;
     }
     __syncwarp();
+    if (tail) {
+      const int st = (T - 1) % kStages;
+      if (__all_sync(0xffffffffu, wait(full(st), ((T - 1) / kStages) & 1))) {
+        clear_rows(sbase + kStageOff + st * kStageBytes, s.lk - kt.begin(T - 1), kBN);
+        say_cleared(cleared);
+      }
+    }
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     if (T > 0 && ptx::elect_one()) {
       const uint32_t tDQ = tmem + kColDQ;
@@ -250,11 +260,13 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       bool ok = true;
       if (warp == kMmaWarp) {
         ok = wait(qfull, 0);
+        const int tail_tile = tail ? T - 1 : T;
         // The first pass's tiles, then all.
 #pragma unroll 1
         for (int u = 0; ok && u < first + T; ++u) {
           const int j = u < first ? u : u - first;
           ok = wait(full(j % kStages), (j / kStages) & 1) && (u < 2 || wait(s_free(u & 1), ((u >> 1) - 1) & 1));
+          if (ok && j == tail_tile) ok = wait(cleared, 0);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_sdp(j, u & 1);
@@ -458,8 +470,8 @@ constexpr int kStages = 8;
 constexpr int kKOff = kStageOff + kStages * kStageBytes, kVOff = kKOff + kKeyTileBytes;
 static_assert(kStageOff % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles");
 constexpr int kBarOff = kVOff + kKeyTileBytes;
-// barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2]
-constexpr int kNumBars = 2 * kStages + 12;
+// barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], cleared
+constexpr int kNumBars = 2 * kStages + 13;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kTileOff = kCtlOff + 32;
 constexpr int kRedoOff = kTileOff + 64;         // one byte per key row
@@ -496,6 +508,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   auto p_full = [&](int b) { return kvfull + 48 + 8 * b; };
   auto p_free = [&](int b) { return kvfull + 64 + 8 * b; };
   auto drain = [&](int i) { return kvfull + 80 + 8 * i; };
+  const uint32_t cleared = kvfull + 96;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
   Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
@@ -535,6 +548,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::mbar_init(p_free(b), 1);
     }
     ptx::mbar_init(o_final, 1);
+    ptx::mbar_init(cleared, 1);
     ptx::mbar_init(drain(0), 1);
     ptx::mbar_init(drain(1), 1);
     ctl->abort = 0;
@@ -588,6 +602,9 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   // Rows below `split_rows` of this tile leave float partial sums.
   const bool shared = far || (j0 == 0 && far_pieces<kKeys, kRowsPerTile>(w, s.lq, s.lk) > 0);
   const int split_rows = shared ? min(w.sinks, s.lk) : 0;
+  // Rows of the last step up to the sequence's end, where the step reaches behind it.
+  const int left = (s.lq - (ra + (nsteps - 1) * tokens)) << w.gshift;
+  const bool tail = nsteps > 0 && left < kStep;
 
   if (warp == kTmaWarp) {
     if (lane == 0 && nsteps > 0) {
@@ -616,6 +633,14 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ctl->issued = issued;
     }
     __syncwarp();
+    if (tail) {
+      const int st = (nsteps - 1) % kStages;
+      if (__all_sync(0xffffffffu, wait(full(st), ((nsteps - 1) / kStages) & 1))) {
+        clear_rows(sbase + kStageOff + st * kStageBytes, left, kStep);
+        clear_rows(sbase + kStageOff + st * kStageBytes + kStepBytes, left, kStep);
+        say_cleared(cleared);
+      }
+    }
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     if (nsteps > 0 && ptx::elect_one()) {
       const uint32_t tDK = tmem + kColDK, tDV = tmem + kColDV;
@@ -653,11 +678,13 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       };
       bool ok = true;
       if (warp == kMmaWarp) {
+        const int tail_step = tail ? nsteps - 1 : nsteps;
         ok = wait(kvfull, 0);
 #pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
           if (!(ok = wait(full(t % kStages), (t / kStages) & 1))) break;
           if (t > 1 && !(ok = wait(s_free(t & 1), ((t >> 1) - 1) & 1))) break;
+          if (t == tail_step && !(ok = wait(cleared, 0))) break;
           ptx::tc_fence_after();
           issue_sdp(t);
         }

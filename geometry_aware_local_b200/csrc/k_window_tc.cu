@@ -77,8 +77,8 @@ struct Smem {
   static constexpr int kColO = 2 * BN;          // tile j: S, then P over it, at (j & 1) * BN
   static constexpr int kStageOff = kQBytes, kStageBytes = 2 * kTileBytes;      // K at +0, V at +kTileBytes
   static constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-  // barriers: full[S], empty[S], qfull, s_full[2], p_full[2], pv_done[2], o_final, drain
-  static constexpr int kNumBars = 2 * kStages + 9;
+  // barriers: full[S], empty[S], qfull, s_full[2], p_full[2], pv_done[2], o_final, drain, cleared
+  static constexpr int kNumBars = 2 * kStages + 10;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;
   static constexpr int kPlanOff = kCtlOff + 32;
   static constexpr int kBytes = kPlanOff + 64 + 1024;
@@ -131,6 +131,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   auto s_full = [&](int b) { return qfull + 24 + 8 * b; };
   auto p_full = [&](int b) { return qfull + 40 + 8 * b; };
   auto pv_done = [&](int b) { return qfull + 56 + 8 * b; };
+  const uint32_t cleared = qfull + 72;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + M::kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::kCtlOff + sizeof(ptx::WaitCtl));
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_bounded(bar, parity, ctl); };
@@ -154,6 +155,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     }
     ptx::mbar_init(o_final, 1);
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(cleared, 1);
     ctl->abort = 0;
     ctl->issued = 0;
     ctl->limit_ns = w.wait_ns;
@@ -180,6 +182,8 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   const int jo = kSplit ? (int)((long)kt.n * blockIdx.z / gridDim.z) : 0;
   const int T = kSplit ? (int)((long)kt.n * (blockIdx.z + 1) / gridDim.z) - jo : kt.n;
   const int T_load = w.stall ? max(T - 1, 0) : T;
+  // Whether the last tile reaches behind the sequence's end.
+  const bool tail = T > 0 && kt.begin(jo + T - 1) + kt.cols(jo + T - 1) > s.lk;
   volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + M::kPlanOff);
   auto load_tile = [&](int j) {
     const int st = j % kStages;
@@ -222,6 +226,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       ctl->issued = issued;
     }
     __syncwarp();
+    if (tail) {
+      const int st = (T - 1) % kStages;
+      if (__all_sync(0xffffffffu, wait(full(st), ((T - 1) / kStages) & 1))) {
+        clear_rows(sbase + kStageOff + st * kStageBytes + kTileBytes, s.lk - kt.begin(jo + T - 1), kt.cols(jo + T - 1));
+        say_cleared(cleared);
+      }
+    }
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issuer ----------------
     if (T > 0 && ptx::elect_one()) {
@@ -247,11 +258,13 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         ptx::tc_commit(empty(j % kStages));
         if (j == T - 1) ptx::tc_commit(o_final);
       };
+      const int tail_tile = tail ? T - 1 : T;
       bool ok = wait(qfull, 0);
 #pragma unroll 1
       for (int j = -2; ok && j < T; ++j) {
         if (j >= 0) {
           if (!(ok = wait(p_full(j & 1), (j >> 1) & 1))) break;
+          if (j == tail_tile && !(ok = wait(cleared, 0))) break;
           ptx::tc_fence_after();
           issue_pv(j);
         }

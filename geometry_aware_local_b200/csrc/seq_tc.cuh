@@ -23,6 +23,21 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   return ptx::mbar_try_wait(bar, parity) || wait_on(bar, parity, ctl);
 }
 
+// A box reaches behind the end of its sequence, where the next one's rows lie or rows
+// of no sequence; multiplied by zeros in a tile's second products they would be NaNs
+// wherever they are not finite.  So the producer's warp, which is idle by then, puts
+// zeros into the rows [from, to) of the sequence's last tile (rows of 128 bytes) when
+// the tile is there, and says so on a barrier.
+__device__ __forceinline__ void clear_rows(uint32_t tile, int from, int to) {
+#pragma unroll 1
+  for (int i = 8 * from + (threadIdx.x & 31); i < 8 * to; i += 32) ptx::st_shared_v4(tile + 16 * i, 0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+}
+__device__ __forceinline__ void say_cleared(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
+
 // The key tiles of a query tile: number j starts at key begin(j) of the
 // sequence and has cols(j) columns, a multiple of 32, BN at most.
 template <int BN>
