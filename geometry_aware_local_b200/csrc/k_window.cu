@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_dkv_rows_kernel(const Win 
   bool bad;
   if (!find_tile(w, blockIdx.x, kWarps, true, &s, &bad)) return no_key_tile<T>(w, bad);
   const int j = s.t * kWarps + (threadIdx.x >> 5);
-  if (j < s.lk) dkv_row<T>(w, s, j, blockIdx.y);
+  if (j < s.lk) dkv_row<T>(w, s, j, blockIdx.y, false);
 }
 
 }  // namespace

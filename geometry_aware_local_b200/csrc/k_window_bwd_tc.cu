@@ -48,7 +48,7 @@
 //
 // A gradient row that is not finite may be spoilt by 0 times a NaN or an
 // infinity of a row it does not depend on; it is computed again from its
-// visible pairs alone (dq_row, dkv_row).
+// visible pairs alone, unless those make it so (dq_again, dkv_row).
 #include <cooperative_groups.h>
 
 #include "seq_tc.cuh"
@@ -68,11 +68,15 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 // A term of row `orow` for the key side's products, as three bf16 pieces whose sum
-// is off by 2^-24 of it: each takes what the ones before leave.
+// is off by 2^-24 of it: each takes what the ones before leave.  (The largest floats
+// would round up to infinity; an infinity or a NaN is a first piece alone.)
 __device__ __forceinline__ void write_terms(const Win& w, int plane, size_t orow, float x) {
-  const float hi = __bfloat162float(__float2bfloat16(x)), mid = __bfloat162float(__float2bfloat16(x - hi));
+  constexpr float kMax = 3.3895314e38f;                 // bf16's largest
+  const bool finite = fabsf(x) < INFINITY;
+  const float hi = finite ? fminf(fmaxf(__bfloat162float(__float2bfloat16(x)), -kMax), kMax) : x;
+  const float rest = finite ? x - hi : 0.f, mid = __bfloat162float(__float2bfloat16(rest));
   reinterpret_cast<uint4*>(w.terms)[(size_t)plane * w.Tq * w.Hq + orow] =
-      make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(x - hi - mid, 0.f), 0u, 0u);
+      make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(rest - mid, 0.f), 0u, 0u);
 }
 
 // The halves of a bf16 pair that bits 2 k and 2 k + 1 of `see` keep.
@@ -118,7 +122,8 @@ constexpr uint32_t kIdescDQ = ptx::idesc_bf16_f32(kRowsPerTile, kDh, true);  // 
 
 __global__ void __launch_bounds__(kThreads, 2)
 window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Win w) {
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ Win w) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -211,6 +216,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  bool again = false;                   // something of this thread's row is not finite
   if (warp == kTmaWarp) {
     if (lane == 0) {
       int issued = min(T_load, kStages);
@@ -336,7 +342,8 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     delta = shares[row] + shares[kRowsPerTile + row];
     if (valid && group == 0) {
       w.delta[orow] = delta;
-      write_terms(w, 0, orow, -lse / w.scale);
+      const float term = -lse / w.scale;
+      write_terms(w, 0, orow, fabsf(term) == INFINITY && fabsf(lse) < INFINITY ? NAN : term);
       write_terms(w, 1, orow, -delta);
     }
     const float2 nd2 = make_float2(-delta, -delta);
@@ -400,13 +407,16 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           dst[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                               pack_bf16x2(x[6], x[7]));
         }
-        if (!(sum == 0.f)) redo[row] = 1;
+        if (!(sum == 0.f)) {
+          redo[row] = 1;
+          again = true;
+        }
       }
     }
   }
 
   ptx::tc_fence_before();
-  __syncthreads();
+  const bool some_again = __syncthreads_or(again);
   if (ctl->abort) {
     // Every role has finished: the MMAs and loads this CTA started complete
     // before its tensor and shared memory are released.
@@ -432,9 +442,10 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
     return;
   }
+  if (!some_again) return;
 #pragma unroll 1
   for (int row = warp; row < kRowsPerTile; row += kThreads / 32)
-    if (redo[row]) dq_row<__nv_bfloat16>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
+    if (redo[row]) dq_again<__nv_bfloat16>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
 }
 
 }  // namespace q_side
@@ -460,16 +471,19 @@ __device__ __forceinline__ constexpr int col_p(int b) { return 384 + 64 * b; }
 __device__ __forceinline__ constexpr int col_ds(int b) { return 416 + 64 * b; }
 constexpr int kStepBytes = kStep * kDh * 2;     // 8 KiB
 constexpr int kKeyTileBytes = kKeys * kDh * 2;  // 16 KiB
-// Three planes of 128 rows x 8 elements: (1, 1, 1, 0, ..), zeros, (1, 1, 1, 0, ..).
+// Two planes of 128 rows x 8 elements: (1, 1, 1, 0, ..), then zeros.
 constexpr int kPlaneBytes = kKeys * 16, kOnesOff = 0;
-constexpr int kStageOff = 3 * kPlaneBytes;
+constexpr int kStageOff = 2 * kPlaneBytes;
 // Q at +0, dout at +kStepBytes, then the rows' terms: planes of -lse / scale and -D.
 constexpr int kTermBytes = kStep * 16, kTermsAt = 2 * kStepBytes;
 constexpr int kStageBytes = 2 * kStepBytes + 2 * kTermBytes;
 constexpr int kStages = 8;
 constexpr int kKOff = kStageOff + kStages * kStageBytes, kVOff = kKOff + kKeyTileBytes;
 static_assert(kStageOff % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles");
-constexpr int kBarOff = kVOff + kKeyTileBytes;
+// A term's second eight elements of K: zeros (the other term there, times zeros,
+// would carry its NaNs over).
+constexpr int kZeroOff = kVOff + kKeyTileBytes;
+constexpr int kBarOff = kZeroOff + kTermBytes;
 // barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], cleared
 constexpr int kNumBars = 2 * kStages + 13;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
@@ -492,7 +506,7 @@ template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmT, const Win w, int key_grid) {
+                     const __grid_constant__ CUtensorMap tmT, const __grid_constant__ Win w, int key_grid) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -561,7 +575,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const uint32_t at = sbase + kOnesOff + 16 * threadIdx.x;
     ptx::st_shared_v4(at, 0x3f803f80u, 0x3f80u, 0u, 0u);
     ptx::st_shared_v4(at + kPlaneBytes, 0u, 0u, 0u, 0u);
-    ptx::st_shared_v4(at + 2 * kPlaneBytes, 0x3f803f80u, 0x3f80u, 0u, 0u);
+    if (threadIdx.x < kStep) ptx::st_shared_v4(sbase + kZeroOff + 16 * threadIdx.x, 0u, 0u, 0u, 0u);
     ptx::fence_proxy_async_smem();
   }
   __syncthreads();
@@ -606,6 +620,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const int left = (s.lq - (ra + (nsteps - 1) * tokens)) << w.gshift;
   const bool tail = nsteps > 0 && left < kStep;
 
+  bool again = false;                   // something of this thread's key is not finite
   if (warp == kTmaWarp) {
     if (lane == 0 && nsteps > 0) {
       ptx::tma_prefetch(&tmQ);
@@ -646,19 +661,19 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const uint32_t tDK = tmem + kColDK, tDV = tmem + kColDV;
       auto issue_sdp = [&](int t) {
         const uint32_t qaddr = sbase + kStageOff + (t % kStages) * kStageBytes;
-        const uint32_t oaddr = qaddr + kStepBytes, ones = sbase + kOnesOff;
-        const uint64_t terms = ptx::smem_desc_plain(qaddr + kTermsAt, kTermBytes, 128);
+        const uint32_t oaddr = qaddr + kStepBytes, taddr = qaddr + kTermsAt;
+        const uint64_t ones = ptx::smem_desc_plain(sbase + kOnesOff, kPlaneBytes, 128);
+        auto terms = [&](uint32_t at) { return ptx::smem_desc_plain(at, sbase + kZeroOff - at, 128); };
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
           ptx::mma_ss(tmem + col_s(t & 1), ptx::smem_desc_sw128(sbase + kKOff + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(qaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
-        ptx::mma_ss(tmem + col_s(t & 1), ptx::smem_desc_plain(ones, kPlaneBytes, 128), terms, kIdescS, 1u);
+        ptx::mma_ss(tmem + col_s(t & 1), ones, terms(taddr), kIdescS, 1u);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk)
           ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_sw128(sbase + kVOff + kk * 32, 16, 1024),
                       ptx::smem_desc_sw128(oaddr + kk * 32, 16, 1024), kIdescS, kk > 0);
-        ptx::mma_ss(tmem + col_dp(t & 1), ptx::smem_desc_plain(ones + kPlaneBytes, kPlaneBytes, 128), terms, kIdescS,
-                    1u);
+        ptx::mma_ss(tmem + col_dp(t & 1), ones, terms(taddr + kTermBytes), kIdescS, 1u);
         ptx::tc_commit(s_full(t & 1));
       };
       auto issue_dkv = [&](int t) {
@@ -810,14 +825,17 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             dst[q] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
                                 pack_bf16x2(y[6], y[7]));
           }
-          if (!(sum == 0.f)) redo[rl] = 1;
+          if (!(sum == 0.f)) {
+            redo[rl] = 1;
+            again = true;
+          }
         }
       }
     }
   }
 
   ptx::tc_fence_before();
-  __syncthreads();
+  const bool some_again = __syncthreads_or(again);
   if (ctl->abort) {
     // Every role has finished: the MMAs of both issuing warps and the
     // producer's loads complete before tensor and shared memory are released.
@@ -871,8 +889,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     if (threadIdx.x == 0) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
     return;
   }
+  if (!kSplit && !some_again) return;
+#pragma unroll 1
   for (int rl = warp; rl < kKeys; rl += kThreads / 32)
-    if (redo[rl]) dkv_row<__nv_bfloat16>(w, s, j0 + rl, g);
+    if (redo[rl]) dkv_row<__nv_bfloat16>(w, s, j0 + rl, g, w.scale >= kLeastScale);
 }
 
 }  // namespace k_side

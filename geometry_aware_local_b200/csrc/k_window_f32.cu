@@ -19,7 +19,7 @@
 // (0.330, 1.14).
 //
 // What is hidden has P = 0; rows that 0 times a NaN or an infinity spoilt are
-// computed again (out_row, dq_row, dkv_row), as in the tensor-core kernels.
+// computed again (out_again, dq_again, dkv_row), as in the tensor-core kernels.
 #include <cooperative_groups.h>
 
 #include "seq_tc.cuh"
@@ -227,7 +227,7 @@ __device__ __forceinline__ bool not_finite(float4 c) {
 __device__ __forceinline__ float4 times(float4 c, float f) { return make_float4(c.x * f, c.y * f, c.z * f, c.w * f); }
 
 template <bool kSplit>
-__global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win w) {
+__global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const __grid_constant__ Win w) {
   extern __shared__ float4 smem4[];
   float* Q = reinterpret_cast<float*>(smem4);
   float *K = Q + kTileFloats, *V = K + kTileFloats, *P = V + kTileFloats;
@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, 2) window_attn_f32_kernel(const Win 
     const size_t at = (size_t)(s.q0 + r) * w.Hq + (g << w.gshift) + (row & (w.G - 1));
     *reinterpret_cast<float4*>((float*)w.out + at * kDh + 4 * tx) = f;
     if (tx == 0 && w.lse) w.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
-    if (not_finite(f)) redo[row] = 1;
+    if (not_finite(f) && sum == sum) redo[row] = 1;
   }
   part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kRows; row += kThreads / 32)
-    if (redo[row]) out_row<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
+    if (redo[row]) out_again<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
 }
 
 // P (and dS) of a tile pair from S and dP in registers, stored by row and key.
@@ -407,7 +407,7 @@ __device__ __forceinline__ void query_side(const Win& w, int x, int grid, int g,
   part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kRows; row += kThreads / 32)
-    if (redo[row]) dq_row<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
+    if (redo[row]) dq_again<float>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
 }
 
 // dK and dV of key tile `at`, or from key_grid on of a piece of the sinks' far
@@ -504,7 +504,7 @@ __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int
   part.meet();
 #pragma unroll 1
   for (int row = threadIdx.x >> 5; row < kKeys; row += kThreads / 32)
-    if (redo[row]) dkv_row<float>(w, s, j0 + row, g);
+    if (redo[row]) dkv_row<float>(w, s, j0 + row, g, true);
 }
 
 // Both sides in one launch, so that few tiles fill more of the GPU: neither reads
@@ -512,7 +512,7 @@ __device__ __forceinline__ void key_side(const Win& w, int at, int key_grid, int
 // first, as the longer ones (behind the query sides 6 % later), and a tile's
 // heads side by side (heads one after the other: up to a third later).
 template <bool kSplit>
-__global__ void __launch_bounds__(kThreads, 2) window_bwd_f32_kernel(const Win w, int key_grid, int key_ctas,
+__global__ void __launch_bounds__(kThreads, 2) window_bwd_f32_kernel(const __grid_constant__ Win w, int key_grid, int key_ctas,
                                                                      int query_ctas) {
   extern __shared__ float4 smem4[];
   __shared__ int redo[64];

@@ -45,7 +45,8 @@
 //
 // A key that a row does not see has P = 0 exactly; where its value row holds a
 // NaN or an infinity, 0 times it is a NaN.  A row whose result is not finite is
-// therefore computed again from its visible keys alone (out_row).
+// therefore computed again from its visible keys alone, unless what it sees makes it
+// so (out_again).
 #include <cooperative_groups.h>
 
 #include "seq_tc.cuh"
@@ -81,7 +82,8 @@ struct Smem {
   static constexpr int kNumBars = 2 * kStages + 10;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;
   static constexpr int kPlanOff = kCtlOff + 32;
-  static constexpr int kBytes = kPlanOff + 64 + 1024;
+  static constexpr int kRedoOff = kPlanOff + 64;        // one byte a row
+  static constexpr int kBytes = kRedoOff + kBM + 1024;
   static_assert(kColO + kDh <= Layout<BN>::kTmemCols, "tensor memory plan");
   static_assert(Layout<BN>::kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
 };
@@ -114,7 +116,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <int kBN, bool kSplit>
 __global__ void __launch_bounds__(kThreads, Layout<kBN>::kCtas)
 window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const Win w) {
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Win w) {
   using M = Smem<kBN>;
   constexpr int kStages = M::kStages, kStageOff = M::kStageOff, kStageBytes = M::kStageBytes;
   constexpr int kTileBytes = M::kTileBytes, kTmemCols = Layout<kBN>::kTmemCols;
@@ -185,6 +187,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   // Whether the last tile reaches behind the sequence's end.
   const bool tail = T > 0 && kt.begin(jo + T - 1) + kt.cols(jo + T - 1) > s.lk;
   volatile Plan* plan = reinterpret_cast<volatile Plan*>(smem + M::kPlanOff);
+  volatile uint8_t* redo = smem + M::kRedoOff;
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
@@ -213,6 +216,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  bool again = false;         // a row of this thread's is to be computed again
   if (warp == kTmaWarp) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
@@ -408,7 +412,8 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           sum = fmaf(x, 0.f, sum);
           o[e] = __float_as_uint(x);
         }
-        const bool again = valid && !(sum == 0.f);
+        // (A denominator that is a NaN is made of visible scores alone.)
+        redo[row] = again = valid && !(sum == 0.f) && l == l;
         if (valid) {
           uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)w.out + orow * kDh);
 #pragma unroll
@@ -419,17 +424,12 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           }
           if (w.lse) w.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718f;
         }
-        __syncwarp();
-        for (uint32_t todo = __ballot_sync(0xffffffffu, again); todo; todo &= todo - 1) {
-          const int rr = lane_base + __ffs(todo) - 1;
-          out_row<__nv_bfloat16>(w, at, r0 + (rr >> w.gshift), (g << w.gshift) + (rr & (w.G - 1)));
-        }
       }
     }
   }
 
   ptx::tc_fence_before();
-  __syncthreads();
+  const bool some_again = __syncthreads_or(again);
   if (ctl->abort) {
     // Every role has finished.  Before tensor memory and shared memory are
     // released, the MMAs and the loads this CTA started complete.
@@ -451,7 +451,12 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
   if (threadIdx.x == 0 && ctl->abort) set_err(w.err, PACK3D_DEVERR_TIMEOUT);
-  if constexpr (kSplit) {
+  if constexpr (!kSplit) {
+    if (!some_again || ctl->abort) return;
+#pragma unroll 1
+    for (int row = warp; row < kBM; row += kThreads / 32)
+      if (redo[row]) out_again<__nv_bfloat16>(w, s, r0 + (row >> w.gshift), (g << w.gshift) + (row & (w.G - 1)));
+  } else {
     // Every CTA of the cluster comes here, whatever its waits did.  CTA z joins
     // the rows z * 128 / S .., a warp a row, the shares in the keys' order.
     auto cluster = cooperative_groups::this_cluster();
@@ -487,8 +492,9 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       const size_t orow = (size_t)(at.q0 + r) * w.Hq + h;
       store2((__nv_bfloat16*)w.out + orow * kDh, o);
       if (w.lse && lane == 0) w.lse[orow] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718f;
-      const bool again = __any_sync(0xffffffffu, !(fmaf(o.x, 0.f, o.y * 0.f) == 0.f));
-      if (again) out_row<__nv_bfloat16>(w, at, r, h);
+      const bool again = l == l && __any_sync(0xffffffffu, !(fmaf(o.x, 0.f, o.y * 0.f) == 0.f));
+      __syncwarp();
+      if (again) out_again<__nv_bfloat16>(w, at, r, h);
     }
     cluster.sync();           // no CTA ends while another reads its share
   }

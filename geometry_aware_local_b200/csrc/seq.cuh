@@ -180,11 +180,10 @@ inline int sm_count() {
 }
 
 // ---- row by row -----------------------------------------------------------------
-// The operators from their definition, one row by one warp, in float: lane l
-// holds the dims 2l and 2l+1, a key that is not visible is never read.  The
-// tiled kernels multiply a hidden key's value by a zero probability; where that
-// value is a NaN or an infinity the product is a NaN, and the row is computed
-// again here.
+// The operators from their definition, one row by one warp, in float: a key that
+// is not visible is never read.  Eight lanes (float: 16) share a key's row, 16
+// bytes each, so that a load of the warp is of four (two) whole rows; the groups of
+// lanes keep sums of their own, joined at the end.
 
 template <typename T> __device__ __forceinline__ float2 load2(const T* row);
 template <> __device__ __forceinline__ float2 load2<float>(const float* row) {
@@ -207,96 +206,368 @@ __device__ __forceinline__ float dot2(float2 a, float2 b) {
   return s;
 }
 
-// Calls f(j) for every key j that position p sees, in order.
-template <typename F>
-__device__ __forceinline__ void for_visible(const Win& w, int p, F f) {
-  const int low = window_low(w, p);
-#pragma unroll 1
-  for (int j = 0; j < min(w.sinks, low); ++j) f(j);
-#pragma unroll 1
-  for (int j = low; j <= p; ++j) f(j);
-}
+// This lane's part of the rows: the dims x .. x + N - 1 of every R-th row from u on.
+template <typename T>
+struct Part32 {
+  static constexpr int N = Elem<T>::kPerChunk, L = kDh / N, R = 32 / L;
+  int x, u;
+  __device__ __forceinline__ Part32() : x((threadIdx.x & 31) % L * N), u((threadIdx.x & 31) / L) {}
+  static __device__ __forceinline__ void floats(const uint4& c, float* f) { chunk_to_float(c, f, T()); }
+  // <a, b> of the group's rows.
+  static __device__ __forceinline__ float dot(const float* a, const float* b) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) s = fmaf(a[e], b[e], s);
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
+  }
+  // Sums of the groups' values, in every group.
+  template <int n>
+  static __device__ __forceinline__ void join(float (&f)[n]) {
+#pragma unroll
+    for (int d = L; d < 32; d <<= 1)
+#pragma unroll
+      for (int e = 0; e < n; ++e) f[e] += __shfl_xor_sync(0xffffffffu, f[e], d);
+  }
+  static __device__ __forceinline__ uint32_t join_bits(uint32_t m) {
+#pragma unroll
+    for (int d = L; d < 32; d <<= 1) m |= __shfl_xor_sync(0xffffffffu, m, d);
+    return m;
+  }
+  // Which of the lane's dims are not finite, and which are NaNs.
+  static __device__ __forceinline__ uint32_t odd(const float* f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m |= (uint32_t)!(fabsf(f[e]) < INFINITY) << e;
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t nans(const float* f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m |= (uint32_t)(f[e] != f[e]) << e;
+    return m;
+  }
+  __device__ __forceinline__ void store(T* row, const float* f) const {
+    if (u == 0) stg16(row + x, float_to_chunk(f, T()));
+  }
+};
+
+// The keys that position p sees, by number: first the sinks, then the window.
+struct Visible {
+  int low, sinks, n;
+  __device__ __forceinline__ Visible(const Win& w, int p) {
+    low = window_low(w, p);
+    sinks = min(w.sinks, low);
+    n = p < 0 ? 0 : sinks + p + 1 - low;
+  }
+  __device__ __forceinline__ int key(int i) const { return i < sinks ? i : i - sinks + low; }
+};
 
 // Output (and log-sum-exp) of head h of query row r.
 template <typename T>
 __device__ __noinline__ void out_row(const Win& w, const Tile& s, int r, int h) {
-  const int g = h >> w.gshift, p = position(s, r);
-  const size_t at = (size_t)(s.q0 + r) * w.Hq + h;
-  const T* k = (const T*)w.k + ((size_t)s.k0 * w.Hkv + g) * kDh;
-  const T* v = (const T*)w.v + ((size_t)s.k0 * w.Hkv + g) * kDh;
+  using P = Part32<T>;
+  constexpr int N = P::N, kAhead = 4;           // rows of a group on their way
+  const P me;
+  const Visible see(w, position(s, r));
+  const size_t at = (size_t)(s.q0 + r) * w.Hq + h, first = ((size_t)s.k0 * w.Hkv + (h >> w.gshift)) * kDh + me.x;
+  const T *k = (const T*)w.k + first, *v = (const T*)w.v + first;
   const size_t step = (size_t)w.Hkv * kDh;
-  const float2 q = load2((const T*)w.q + at * kDh);
-  float m = -INFINITY, l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
-  for_visible(w, p, [&](int j) {
-    const float x = dot2(q, load2(k + j * step)) * w.scale;
-    const float2 vv = load2(v + j * step);
-    float f = 1.f;
-    if (x > m) {
-      f = expf(m - x);
-      m = x;
+  const float scale = w.scale;
+  float q[N], o[N], m = -INFINITY, l[1] = {0.f};
+  P::floats(ldg16((const T*)w.q + at * kDh + me.x), q);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = me.u; i0 - me.u < see.n; i0 += kAhead * P::R) {
+    uint4 kc[kAhead], vc[kAhead];
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      const size_t key = see.key(min(i0 + t * P::R, see.n - 1)) * step;
+      kc[t] = ldg16(k + key);
+      vc[t] = ldg16(v + key);
     }
-    // A row whose scores so far are all -infinity keeps weight 0 for them.
-    const float e = x == -INFINITY ? 0.f : expf(x - m);
-    l = l * f + e;
-    o.x = fmaf(e, vv.x, o.x * f);
-    o.y = fmaf(e, vv.y, o.y * f);
-  });
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  store2((T*)w.out + at * kDh, make_float2(o.x * inv, o.y * inv));
-  if (w.lse && (threadIdx.x & 31) == 0) w.lse[at] = m + logf(l);
-}
-
-// P and dS of one visible pair, from the row's q, dout, lse and delta.
-__device__ __forceinline__ float2 pair_grad(const Win& w, float2 q, float2 d, float lse, float delta, float2 k,
-                                            float2 v) {
-  const float p = expf(dot2(q, k) * w.scale - lse);
-  return make_float2(p, p * (dot2(d, v) - delta));
+    float y[kAhead], top = m;
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      float f[N];
+      P::floats(kc[t], f);
+      y[t] = P::dot(q, f) * scale;
+      if (i0 + t * P::R >= see.n) y[t] = -INFINITY;
+      top = fmaxf(top, y[t]);
+    }
+    const float f = m == top ? 1.f : expf(m - top);
+    m = top;
+    l[0] *= f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] *= f;
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      if (i0 + t * P::R >= see.n) break;
+      // A row whose scores so far are all -infinity keeps weight 0 for them.
+      const float p = y[t] == -INFINITY ? 0.f : expf(y[t] - top);
+      float c[N];
+      P::floats(vc[t], c);
+      l[0] += p;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = fmaf(p, c[e], o[e]);
+    }
+  }
+  float top = m;
+#pragma unroll
+  for (int d = P::L; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float f = m == top ? 1.f : expf(m - top);
+  l[0] *= f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] *= f;
+  P::join(l);
+  P::join(o);
+  const float inv = l[0] > 0.f ? 1.f / l[0] : (l[0] == 0.f ? 0.f : l[0]);
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] *= inv;
+  me.store((T*)w.out + at * kDh, o);
+  if (w.lse && (threadIdx.x & 31) == 0) w.lse[at] = top + logf(l[0]);
 }
 
 // dq of head h of query row r; delta[at] is up to date.
 template <typename T>
 __device__ __noinline__ void dq_row(const Win& w, const Tile& s, int r, int h) {
-  const int g = h >> w.gshift, p = position(s, r);
-  const size_t at = (size_t)(s.q0 + r) * w.Hq + h;
-  const T* k = (const T*)w.k + ((size_t)s.k0 * w.Hkv + g) * kDh;
-  const T* v = (const T*)w.v + ((size_t)s.k0 * w.Hkv + g) * kDh;
+  using P = Part32<T>;
+  constexpr int N = P::N, kAhead = 2;
+  const P me;
+  const Visible see(w, position(s, r));
+  const size_t at = (size_t)(s.q0 + r) * w.Hq + h, first = ((size_t)s.k0 * w.Hkv + (h >> w.gshift)) * kDh + me.x;
+  const T *k = (const T*)w.k + first, *v = (const T*)w.v + first;
   const size_t step = (size_t)w.Hkv * kDh;
-  const float2 q = load2((const T*)w.q + at * kDh), d = load2((const T*)w.dout + at * kDh);
-  const float lse = w.lse[at], delta = w.delta[at];
-  float2 acc = make_float2(0.f, 0.f);
-  for_visible(w, p, [&](int j) {
-    const float2 kk = load2(k + j * step);
-    const float2 pd = pair_grad(w, q, d, lse, delta, kk, load2(v + j * step));
-    acc.x = fmaf(pd.y, kk.x, acc.x);
-    acc.y = fmaf(pd.y, kk.y, acc.y);
-  });
-  store2((T*)w.dq + at * kDh, make_float2(acc.x * w.scale, acc.y * w.scale));
+  const float lse = w.lse[at], delta = w.delta[at], scale = w.scale;
+  float q[N], d[N], acc[N];
+  P::floats(ldg16((const T*)w.q + at * kDh + me.x), q);
+  P::floats(ldg16((const T*)w.dout + at * kDh + me.x), d);
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = me.u; i0 - me.u < see.n; i0 += kAhead * P::R) {
+    uint4 kc[kAhead], vc[kAhead];
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      const size_t key = see.key(min(i0 + t * P::R, see.n - 1)) * step;
+      kc[t] = ldg16(k + key);
+      vc[t] = ldg16(v + key);
+    }
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      float a[N], b[N];
+      P::floats(kc[t], a);
+      P::floats(vc[t], b);
+      const float p = expf(P::dot(q, a) * scale - lse), ds = p * (P::dot(d, b) - delta);
+      if (i0 + t * P::R < see.n) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(ds, a[e], acc[e]);
+      }
+    }
+  }
+  P::join(acc);
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] *= scale;
+  me.store((T*)w.dq + at * kDh, acc);
 }
 
-// dk and dv of key j of key head g, over every query that sees it.
+// The query rows or keys of a sequence that one tile of any of the kernels takes at most.
+constexpr int kTileRows = 128;
+
+// The tiled kernels multiply a hidden key's value (or, for a key's gradients, a
+// query's row that does not see it) by a zero probability; where that value is a
+// NaN or an infinity the product is a NaN.  So a row of results that is not finite
+// is formed again from what it sees, here - but only if something hidden that its
+// tile has read, a few hundred rows at most, is not finite in the same dims, and
+// what it sees does not make them NaN anyway: a NaN that is the right answer costs
+// a look at those rows, not at all that the row sees.
+
+// Whether the rows [from, to) of `base`, `step` apart, are not finite in one of this
+// lane's dims of `odd`.
 template <typename T>
-__device__ __noinline__ void dkv_row(const Win& w, const Tile& s, int j, int g) {
-  const size_t at = (size_t)(s.k0 + j) * w.Hkv + g;
-  const float2 k = load2((const T*)w.k + at * kDh), v = load2((const T*)w.v + at * kDh);
-  float2 ak = make_float2(0.f, 0.f), av = ak;
-  const int first = max(0, j - (s.lk - s.lq));
-  int last = s.lq - 1;
-  if (w.window > 0 && j >= w.sinks) last = min(last, j + w.window - 1 - (s.lk - s.lq));
-  for (int r = first; r <= last; ++r)
-    for (int h = g << w.gshift; h < (g + 1) << w.gshift; ++h) {
-      const size_t row = (size_t)(s.q0 + r) * w.Hq + h;
-      const float2 q = load2((const T*)w.q + row * kDh), d = load2((const T*)w.dout + row * kDh);
-      // (The float kernels run both sides at once: there may be no delta yet.)
-      const float delta = sizeof(T) == 4 ? dot2(d, load2((const T*)w.out + row * kDh)) : w.delta[row];
-      const float2 pd = pair_grad(w, q, d, w.lse[row], delta, k, v);
-      ak.x = fmaf(pd.y, q.x, ak.x);
-      ak.y = fmaf(pd.y, q.y, ak.y);
-      av.x = fmaf(pd.x, d.x, av.x);
-      av.y = fmaf(pd.x, d.y, av.y);
+__device__ __forceinline__ bool met(const Part32<T>& me, uint32_t odd, const T* base, size_t step, int from, int to) {
+  uint32_t m = 0;
+#pragma unroll 8
+  for (int j = from + me.u; j < to; j += Part32<T>::R) {
+    float f[Part32<T>::N];
+    Part32<T>::floats(ldg16(base + j * step + me.x), f);
+    m |= Part32<T>::odd(f);
+  }
+  return (m & odd) != 0;
+}
+// The lane's part of a row of results that this kernel has written.
+template <typename T>
+__device__ __forceinline__ void written(const Part32<T>& me, const T* row, float* f) {
+  Part32<T>::floats(*reinterpret_cast<const uint4*>(row + me.x), f);
+}
+
+// Whether a hidden key of `keys` (of head g's first key on) that the tile of query
+// row r has read is not finite in a dim of `odd`.
+template <typename T>
+__device__ __forceinline__ bool hidden_key(const Win& w, const Tile& s, int r, const Part32<T>& me, const T* keys,
+                                           uint32_t odd) {
+  const int tokens = kTileRows >> w.gshift, r0 = r & ~(tokens - 1);
+  const int p = position(s, r), p1 = position(s, min(s.lq, r0 + tokens) - 1), low = window_low(w, p);
+  const size_t step = (size_t)w.Hkv * kDh;
+  int lo = window_low(w, max(position(s, r0), 0));
+  if (lo <= 64) lo = 0;                         // the sinks' columns reach it: one range from key 0
+  bool hit = met(me, odd, keys, step, max(p + 1, 0), min(p1 + 32, s.lk)) || met(me, odd, keys, step, lo, low);
+  if (w.sinks > 0) hit |= met(me, odd, keys, step, w.sinks, min(64, low));
+  return __any_sync(0xffffffffu, hit);
+}
+
+// out_row of a result that is not finite, whose denominator is a number.
+template <typename T>
+__device__ __noinline__ void out_again(const Win& w, const Tile& s, int r, int h) {
+  using P = Part32<T>;
+  constexpr int N = P::N, kAhead = 8;
+  const P me;
+  const T* v = (const T*)w.v + ((size_t)s.k0 * w.Hkv + (h >> w.gshift)) * kDh;
+  float f[N];
+  written(me, (const T*)w.out + ((size_t)(s.q0 + r) * w.Hq + h) * kDh, f);
+  const uint32_t odd = P::odd(f);
+  if (!hidden_key(w, s, r, me, v, odd)) return;
+  // Visible values that are not finite, from the nearest key back: a NaN, or
+  // infinities of both signs, leave a NaN whatever their weights are.
+  const Visible see(w, position(s, r));
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = 0.f;
+#pragma unroll 1
+  for (int end = see.n - 1 - me.u; end + me.u >= 0; end -= kAhead * P::R) {
+    uint4 c[kAhead];
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) c[t] = ldg16(v + see.key(max(end - t * P::R, 0)) * ((size_t)w.Hkv * kDh) + me.x);
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      float y[N];
+      P::floats(c[t], y);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (!(fabsf(y[e]) < INFINITY)) f[e] += y[e];
     }
-  store2((T*)w.dk + at * kDh, make_float2(ak.x * w.scale, ak.y * w.scale));
-  store2((T*)w.dv + at * kDh, av);
+    if (__all_sync(0xffffffffu, (odd & ~P::join_bits(P::nans(f))) == 0)) return;
+  }
+  out_row<T>(w, s, r, h);
+}
+
+// dq_row of a result that is not finite.  (Where the row sees a NaN its
+// log-sum-exp or its delta is one.)
+template <typename T>
+__device__ __noinline__ void dq_again(const Win& w, const Tile& s, int r, int h) {
+  const Part32<T> me;
+  const size_t at = (size_t)(s.q0 + r) * w.Hq + h;
+  const float lse = w.lse[at], delta = w.delta[at];
+  if (position(s, r) >= 0 && (lse != lse || delta != delta)) return;
+  float f[Part32<T>::N];
+  written(me, (const T*)w.dq + at * kDh, f);
+  const T* k = (const T*)w.k + ((size_t)s.k0 * w.Hkv + (h >> w.gshift)) * kDh;
+  if (hidden_key(w, s, r, me, k, Part32<T>::odd(f))) dq_row<T>(w, s, r, h);
+}
+
+// dk and dv of key j of key head g, over every query that sees it.  again: of a
+// result that is not finite, as above (a query row that sees a NaN has one in its
+// log-sum-exp, its delta or its own values).
+template <typename T>
+__device__ __noinline__ void dkv_row(const Win& w, const Tile& s, int j, int g, bool again) {
+  using P = Part32<T>;
+  constexpr int N = P::N, kAhead = 2;
+  const P me;
+  const int shift = s.lk - s.lq;                // position minus row
+  const size_t at = ((size_t)(s.k0 + j) * w.Hkv + g) * kDh, heads = (size_t)w.Hq * kDh;
+  const size_t row0 = (size_t)s.q0 * w.Hq + (g << w.gshift);
+  const T *q = (const T*)w.q + row0 * kDh, *dout = (const T*)w.dout + row0 * kDh;
+  const int first = max(0, j - shift);
+  const bool windowed = w.window > 0 && j >= w.sinks;
+  const int last = windowed ? min(s.lq - 1, j + w.window - 1 - shift) : s.lq - 1;
+  uint32_t odd_k = 0, odd_v = 0;
+  if (again) {
+    float f[N];
+    written(me, (const T*)w.dk + at, f);
+    odd_k = P::odd(f);
+    written(me, (const T*)w.dv + at, f);
+    odd_v = P::odd(f);
+    // Rows that the key's tile has read besides: before the first that sees the key,
+    // and behind the last (for a sink behind those that its own tile takes), to the
+    // end of a step of at most 64.
+    const int j0 = j & ~(kTileRows - 1), beyond = min(j0 + kTileRows, s.lk) - 1 + w.window - shift;
+    const int before = max(0, j0 - shift), before_end = min(first, s.lq);
+    const int behind = max(0, windowed ? last + 1 : beyond), behind_end = w.window > 0 ? min(s.lq, beyond + 64) : 0;
+    bool hit = false;
+#pragma unroll 1
+    for (int h = 0; h < w.G; ++h) {
+      const T *qh = q + h * kDh, *dh = dout + h * kDh;
+      hit |= met(me, odd_k, qh, heads, before, before_end) || met(me, odd_v, dh, heads, before, before_end) ||
+             met(me, odd_k, qh, heads, behind, behind_end) || met(me, odd_v, dh, heads, behind, behind_end);
+    }
+    if (!__any_sync(0xffffffffu, hit)) return;
+  }
+  float k[N], v[N], ak[N], av[N];
+  P::floats(ldg16((const T*)w.k + at + me.x), k);
+  P::floats(ldg16((const T*)w.v + at + me.x), v);
+#pragma unroll
+  for (int e = 0; e < N; ++e) ak[e] = av[e] = 0.f;
+  const float scale = w.scale;
+  const int n = last >= first ? (last - first + 1) << w.gshift : 0;      // (row, head) pairs
+  auto place = [&](int i) { return (size_t)(first + (i >> w.gshift)) * w.Hq + (i & (w.G - 1)); };
+  int turn = 0;
+#pragma unroll 1
+  for (int i0 = me.u; i0 - me.u < n; i0 += kAhead * P::R, ++turn) {
+    uint4 qc[kAhead], dc[kAhead];
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      const size_t row = place(min(i0 + t * P::R, n - 1));
+      qc[t] = ldg16(q + row * kDh + me.x);
+      dc[t] = ldg16(dout + row * kDh + me.x);
+    }
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) {
+      const size_t row = row0 + place(min(i0 + t * P::R, n - 1));
+      float a[N], b[N];
+      P::floats(qc[t], a);
+      P::floats(dc[t], b);
+      float delta;
+      if constexpr (sizeof(T) == 4) {           // both sides run at once: there may be no delta yet
+        float c[N];
+        P::floats(ldg16((const T*)w.out + row * kDh + me.x), c);
+        delta = P::dot(b, c);
+      } else {
+        delta = w.delta[row];
+      }
+      const float p = expf(P::dot(a, k) * scale - w.lse[row]), ds = p * (P::dot(b, v) - delta);
+      if (i0 + t * P::R < n) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          ak[e] = fmaf(ds, a[e], ak[e]);
+          av[e] = fmaf(p, b[e], av[e]);
+        }
+      }
+    }
+    // Dims that are NaN stay so, whatever comes; the others are as they were.
+    if (again && (turn & 7) == 0) {
+      const uint32_t left = (odd_k & ~P::join_bits(P::nans(ak))) | (odd_v & ~P::join_bits(P::nans(av)));
+      if (__all_sync(0xffffffffu, left == 0)) {
+        written(me, (const T*)w.dk + at, ak);
+        written(me, (const T*)w.dv + at, av);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if ((odd_k >> e) & 1u) ak[e] = NAN;
+          if ((odd_v >> e) & 1u) av[e] = NAN;
+        }
+        me.store((T*)w.dk + at, ak);
+        me.store((T*)w.dv + at, av);
+        return;
+      }
+    }
+  }
+  P::join(ak);
+  P::join(av);
+#pragma unroll
+  for (int e = 0; e < N; ++e) ak[e] *= scale;
+  me.store((T*)w.dk + at, ak);
+  me.store((T*)w.dv + at, av);
 }
 
 // delta[at] = <dout, out> of one row, by one warp.

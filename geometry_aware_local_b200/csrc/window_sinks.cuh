@@ -57,11 +57,16 @@ __device__ __forceinline__ float* part_row(const Win& w, int slot, int g, int ro
   return w.part + (((size_t)slot * w.Hkv + g) * w.sinks + row) * 2 * kDh;
 }
 
+// Softmax scales below this can make lse / scale, which the bf16 kernels subtract,
+// overflow: a row's term is a NaN then, and what it spoils is computed again
+// whatever has spoilt it.
+constexpr float kLeastScale = 0x1p-100f;
+
 // dK and dV of one sink row of one sequence: eight warps add every eighth part,
 // then the eight sums in order.  (With very many sequences a CTA takes several.)
 constexpr int kSinksGrid = 1024;
 template <typename T, int Keys, int Rows>
-__global__ void __launch_bounds__(256) window_sinks_kernel(const Win w) {
+__global__ void __launch_bounds__(256) window_sinks_kernel(const __grid_constant__ Win w) {
   __shared__ float4 sums[8][32];
   const int g = blockIdx.y, j = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_last();
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(256) window_sinks_kernel(const Win w) {
       const float zero = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
       const bool again = __any_sync(0xffffffffu, !(zero == 0.f));
       __syncwarp();
-      if (again) dkv_row<T>(w, s, j, g);
+      if (again) dkv_row<T>(w, s, j, g, sizeof(T) == 4 || w.scale >= kLeastScale);
     }
     __syncthreads();
   }
