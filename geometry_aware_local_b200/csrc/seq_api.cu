@@ -4,6 +4,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "seq.cuh"
 
 using namespace pack3d;
@@ -20,6 +22,24 @@ pack3d_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return PACK3D_OK;
   cudaGetLastError();  // clear a sticky launch-configuration error
   return PACK3D_ERR_CUDA;
+}
+
+// A buffer of a call: `n` elements of `size` bytes (none where p is null).
+struct Span {
+  uintptr_t from, to;
+  Span(const void* p, int64_t n, int size) : from((uintptr_t)p), to(p ? from + (uintptr_t)n * size : from) {}
+  bool meets(const Span& o) const { return from < o.to && o.from < to; }
+};
+// Whether a written buffer meets a read one or another written one.  (Other CTAs
+// still read the inputs when the first results are written.)
+bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* a = written.begin(); a != written.end(); ++a) {
+    for (const Span* b = written.begin(); b != a; ++b)
+      if (a->meets(*b)) return true;
+    for (const Span& b : read)
+      if (a->meets(b)) return true;
+  }
+  return false;
 }
 
 int shift_of(int x) {
@@ -146,6 +166,11 @@ pack3d_status pack3d_window_attn(const pack3d_seq_config* cfg, int32_t batch, in
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
       !aligned(cu_k, 4) || !aligned(lse, 4))
     return PACK3D_ERR_ALIGNMENT;
+  const int e = elem_bytes(*cfg) * kDh;
+  const int64_t nq = q_rows * cfg->Hq, nk = k_rows * cfg->Hkv;
+  if (overlap({{out, nq, e}, {lse, nq, 4}},
+              {{q, nq, e}, {k, nk, e}, {v, nk, e}, {cu_q, batch + 1, 4}, {cu_k, batch + 1, 4}}))
+    return PACK3D_ERR_INVALID_ARG;
   seq::Win w = make_win(*cfg, batch, q_rows, k_rows, cu_q, cu_k);
   w.q = q;
   w.k = k;
@@ -182,6 +207,12 @@ pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config* cfg, int32_t batch
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return PACK3D_ERR_ALIGNMENT;
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(lse, 4)) return PACK3D_ERR_ALIGNMENT;
+  const int e = elem_bytes(*cfg) * kDh;
+  const int64_t nq = q_rows * cfg->Hq, nk = k_rows * cfg->Hkv;
+  if (overlap({{dq, nq, e}, {dk, nk, e}, {dv, nk, e}, {workspace, (int64_t)bwd_bytes(w, cfg->dtype), 1}},
+              {{q, nq, e}, {k, nk, e}, {v, nk, e}, {out, nq, e}, {lse, nq, 4}, {dout, nq, e}, {cu_q, batch + 1, 4},
+               {cu_k, batch + 1, 4}}))
+    return PACK3D_ERR_INVALID_ARG;
   w.q = q;
   w.k = k;
   w.v = v;
@@ -238,6 +269,15 @@ pack3d_status pack3d_cache_attn(const pack3d_seq_config* cfg, int32_t batch, con
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(lse, 4) ||
       !aligned(weights, 4) || !aligned(lengths, 4) || !aligned(table, 4))
     return PACK3D_ERR_ALIGNMENT;
+  const int e = elem_bytes(*cfg) * kDh;
+  const int64_t nq = (int64_t)batch * cfg->Hq, pool = (int64_t)num_pages * cfg->page * cfg->Hkv;
+  // The results may take the queries' place: a head's are written when it has been read.
+  const bool in_place = out == q;
+  if (overlap({{out, nq, e}, {lse, nq, 4}, {weights, (int64_t)batch * max_pages * cfg->page, 4},
+               {workspace, (int64_t)need, 1}},
+              {{in_place ? nullptr : q, nq, e}, {k_pages, pool, e}, {v_pages, pool, e},
+               {table, (int64_t)batch * max_pages, 4}, {lengths, batch, 4}}))
+    return PACK3D_ERR_INVALID_ARG;
   const seq::Cache c = make_cache(*cfg, batch, lengths, table, max_pages, num_pages, k_pages, v_pages, err_word);
   return cuda_status(seq::launch_cache_attn(c, cfg->dtype, q, out, lse, weights, accumulate != 0, workspace,
                                             (cudaStream_t)stream));
@@ -262,6 +302,10 @@ pack3d_status pack3d_cache_evict(const pack3d_seq_config* cfg, int32_t batch, vo
   const void* words[] = {table, lengths, weights, new_table, kept, new_weights, new_lengths};
   for (const void* p : words)
     if (!aligned(p, 4)) return PACK3D_ERR_ALIGNMENT;
+  const int64_t old_slots = (int64_t)batch * max_pages, new_slots = (int64_t)batch * new_max_pages;
+  if (overlap({{kept, (int64_t)batch * budget, 4}, {new_weights, new_slots * cfg->page, 4}, {new_lengths, batch, 4}},
+              {{table, old_slots, 4}, {lengths, batch, 4}, {weights, old_slots * cfg->page, 4}, {new_table, new_slots, 4}}))
+    return PACK3D_ERR_INVALID_ARG;
   const seq::Cache c = make_cache(*cfg, batch, lengths, table, max_pages, num_pages, k_pages, v_pages, err_word);
   return cuda_status(seq::launch_cache_evict(c, weights, budget, recent, new_table, new_max_pages, kept, new_weights,
                                              new_lengths, (cudaStream_t)stream));

@@ -12,7 +12,10 @@
  *   the operator's type 16-byte aligned, index and float tensors 4-byte
  *   aligned.  Nothing is allocated, freed or kept.  Every call is asynchronous
  *   on `stream`, runs on the current device and can be captured into a CUDA
- *   graph (workspaces of calls that may overlap must be distinct).
+ *   graph (workspaces of calls that may overlap must be distinct).  What a call
+ *   writes overlaps none of its inputs and nothing else that it writes
+ *   (PACK3D_ERR_INVALID_ARG; the pages are the caller's to keep apart), but
+ *   pack3d_cache_attn's out may be its q.
  * - T = float or bf16 (config.dtype); d_h = 64; Hq / Hkv in {1, 2, 4, 8};
  *   query head h reads key head floor(h * Hkv / Hq).  Rotations (or any other
  *   position code) are applied to q and k by the caller.

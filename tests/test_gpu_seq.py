@@ -440,6 +440,30 @@ def test_decode_is_window_attention_of_one_query(p3, cuda_device):
         ref.close(l, r["lse"], r["lse_tol"], "lse")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lengths,Hq,Hkv", [([300, 7], 8, 2), ([5000, 0, 90], 8, 2), ([3] * 300 + [2000], 4, 2)])
+def test_results_next_to_and_over_the_queries(p3, cuda_device, lengths, Hq, Hkv, dtype):
+    """Outputs that lie right behind the inputs in one buffer, and attention over the cache whose output takes its
+    queries' place: the same bits."""
+    dev, B = cuda_device, len(lengths)
+    k, v, table, n, _ = make_cache(lengths, 64, Hkv, dtype, dev)
+    q = torch.randn(B, Hq, 64, device=dev, generator=torch.Generator(device=dev).manual_seed(1)).to(dtype)
+    cfg = p3.make_seq_config(Hq=Hq, Hkv=Hkv, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+    want, lse = p3.cache_attn(cfg, q, k, v, table, n)
+    both = torch.empty(2, B, Hq, 64, dtype=dtype, device=dev)
+    both[0] = q
+    got, got_lse = p3.cache_attn(cfg, both[0], k, v, table, n, out=both[1])
+    assert torch.equal(got, want) and torch.equal(got_lse, lse) and torch.equal(both[0], q)
+    got, got_lse = p3.cache_attn(cfg, both[0], k, v, table, n, out=both[0])
+    assert got is not want and torch.equal(got, want) and torch.equal(got_lse, lse)
+    with pytest.raises(p3.Pack3DError, match="INVALID_ARG"):
+        p3.cache_attn(cfg, both.view(-1, Hq, 64)[:B], k, v, table, n, out=both.view(-1, Hq, 64)[1:B + 1])
+    with pytest.raises(p3.Pack3DError, match="INVALID_ARG"):
+        w = torch.rand(B, table.shape[1] * 64, device=dev)
+        p3.cache_evict(cfg, k, v, table, n, w, table, 64, 0, new_weights=w, new_lengths=torch.empty_like(n),
+                       kept=torch.empty(B, 64, dtype=torch.int32, device=dev))
+
+
 def test_pool_beyond_32_bit_offsets(p3, cuda_device):
     """Pages whose elements and bytes lie beyond 2^31 and 2^32: written, read and moved there.  (Keys and values in
     one pool of 10.5 GB: append writes equal rows to both.)"""

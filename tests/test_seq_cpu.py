@@ -137,6 +137,56 @@ def test_cache_refusals(p3):
         assert evict(**{name: bad16 if name in ("k_pages", "v_pages") else bad4}) == 3, name
 
 
+def test_outputs_over_inputs_are_refused(p3):
+    """A result that lies over an input, or over another result, by its first or its last byte: refused, since other
+    parts of the call still read there.  (Every call here is refused: the addresses are of nothing.)"""
+    c, L = p3.make_seq_config(window=16, page=16), p3.lib
+    cp, gap = ctypes.byref(c), 1 << 24
+
+    def each(call, names, sizes, outputs, allowed=()):
+        at = {n: gap * (i + 1) for i, n in enumerate(names)}
+        for a in outputs:
+            for b in names:
+                if a == b or (a, b) in allowed:
+                    continue
+                for where in (at[b], at[b] + sizes[b] - 16 if sizes[b] > 16 else at[b], at[b] - sizes[a] + 16):
+                    if where % 256 and a == "workspace":
+                        continue
+                    assert call(**dict(at, **{a: where})) == 1, (a, b, where - at[b])
+
+    tq, tk, row_q, row_k = 96, 80, 8 * 128, 2 * 128
+    sizes = {"q": tq * row_q, "k": tk * row_k, "v": tk * row_k, "out": tq * row_q, "lse": tq * 32, "cu_q": 16, "cu_k": 16,
+             "dout": tq * row_q, "dq": tq * row_q, "dk": tk * row_k, "dv": tk * row_k}
+    sizes["workspace"] = need = p3.window_attn_bwd_workspace_bytes(c, 3, tq, tk)
+    each(lambda **a: L.pack3d_window_attn(cp, 3, tq, tk, *a.values(), 0, None, None),
+         ("cu_q", "cu_k", "q", "k", "v", "out", "lse"), sizes, ("out", "lse"))
+    each(lambda workspace, **a: L.pack3d_window_attn_bwd(cp, 3, tq, tk, *a.values(), 0, workspace, need, None, None),
+         ("cu_q", "cu_k", "q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv", "workspace"), sizes,
+         ("dq", "dk", "dv", "workspace"))
+
+    batch, wide, pages = 4, 8, 40
+    sizes = {"q": batch * row_q, "out": batch * row_q, "lse": batch * 32, "k_pages": pages * 16 * row_k,
+             "v_pages": pages * 16 * row_k, "table": batch * wide * 4, "lengths": batch * 4, "weights": batch * wide * 64,
+             "kept": batch * 256, "new_table": batch * 16, "new_weights": batch * 4 * 64, "new_lengths": batch * 4}
+    sizes["workspace"] = need = p3.cache_attn_workspace_bytes(c, batch, wide, True)
+    each(lambda q, k_pages, v_pages, table, lengths, out, lse, weights, workspace:
+         L.pack3d_cache_attn(cp, batch, q, k_pages, v_pages, table, wide, pages, lengths, out, lse, weights, 0, workspace,
+                             need, None, None),
+         ("q", "k_pages", "v_pages", "table", "lengths", "out", "lse", "weights", "workspace"),
+         sizes, ("lse", "weights", "workspace"))
+    each(lambda q, k_pages, v_pages, table, lengths, out, lse, weights, workspace:
+         L.pack3d_cache_attn(cp, batch, q, k_pages, v_pages, table, wide, pages, lengths, out, lse, weights, 0, workspace,
+                             need, None, None),
+         ("q", "k_pages", "v_pages", "table", "lengths", "out", "lse", "weights", "workspace"),
+         sizes, ("out",), allowed=(("out", "q"),))
+    each(lambda k_pages, v_pages, table, lengths, weights, new_table, kept, new_weights, new_lengths:
+         L.pack3d_cache_evict(cp, batch, k_pages, v_pages, pages, table, wide, lengths, weights, 64, 8, new_table, 4, kept,
+                              new_weights, new_lengths, None, None),
+         ("k_pages", "v_pages", "table", "lengths", "weights", "new_table", "kept", "new_weights", "new_lengths"),
+         sizes, ("kept", "new_weights", "new_lengths"),
+         allowed=[(a, b) for a in ("kept", "new_weights", "new_lengths") for b in ("k_pages", "v_pages")])
+
+
 def test_status_texts(p3):
     assert p3.STATUS[9] == "LENGTHS" and p3.STATUS[10] == "PAGE"
     for st in (9, 10):
