@@ -418,6 +418,8 @@ class PagedCache:
             raise ValueError("PagedCache: batch and capacity are at least 1, the budget is at most the capacity")
         self.cfg, self.budget = cfg, budget
         dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"PagedCache: lives on a CUDA device, not on {dev}")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         wide, spare = -(-capacity // cfg.page), -(-budget // cfg.page)

@@ -215,6 +215,12 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(p3):
         p3.PagedCache(c, 1, 64, budget=65)
 
 
+def test_cache_refuses_another_kind_of_device(p3):
+    for device in ("cpu", "meta"):
+        with pytest.raises(ValueError, match="CUDA device"):
+            p3.PagedCache(p3.make_seq_config(), 1, 64, device=device)
+
+
 # ---- the reference itself ------------------------------------------------------------
 
 def test_reference_masks():
