@@ -69,6 +69,12 @@ def test_window_and_gradients(p3, cuda_device, lens, klens, Hq, Hkv, W, S, dtype
     check_window(p3, lens, klens, Hq, Hkv, W, S, dtype, cuda_device)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,W,S", [([9000, 1200], 700, 5), ([8300, 1, 40], 0, 0)])
+def test_long_sequences(p3, cuda_device, lens, W, S, dtype):
+    check_window(p3, lens, lens, 2, 1, W, S, dtype, cuda_device)
+
+
 def test_many_sequences(p3, cuda_device):
     """More sequences than one pass over the offsets takes at once, most of them short."""
     lens = [(7 * i) % 23 for i in range(150)]
@@ -421,6 +427,26 @@ def test_decode_where_no_score_is_finite(p3, cuda_device, lengths, page, dtype):
     inside = torch.arange(weights.shape[1], device=dev)[None] < n[:, None]
     assert (added[~inside] == 2.0).all()
     ref.close(added[0], r["weights"][0] + 2.0, r["weights_tol"][0] + 2.0 ** -24 * 10, "added")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,longest", [(512, 3000), (511, 3000), (511, 1000)])
+def test_decode_at_the_splits_borders(p3, cuda_device, batch, longest, dtype):
+    """4,096 (sequence, key head) pairs and fewer, capacities of 1,024 slots and more: one long sequence among short
+    ones, split over the GPU or not."""
+    dev = cuda_device
+    lengths = [(7 * i) % 20 for i in range(batch)]
+    lengths[batch // 3] = longest
+    k, v, table, n, _ = make_cache(lengths, 16, 8, dtype, dev)
+    q = torch.randn(batch, 8, 64, device=dev, generator=torch.Generator(device=dev).manual_seed(1)).to(dtype)
+    cfg = p3.make_seq_config(Hq=8, Hkv=8, page=16, dtype="bf16" if dtype == torch.bfloat16 else "f32")
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = p3.cache_attn(cfg, q, k, v, table, n, err=err)
+    assert p3.check_status(err) == 0
+    some = sorted(set(range(0, batch, 9)) | {batch // 3 + d for d in (-1, 0, 1)} | {batch - 1})
+    r = ref.decode(q[some], k, v, table[some], n[some], 0, 0, cfg.softmax_scale)
+    ref.close(out[some], r["out"], r["out_tol"], "out")
+    ref.close(lse[some], r["lse"], r["lse_tol"], "lse")
 
 
 def test_decode_is_window_attention_of_one_query(p3, cuda_device):
