@@ -118,6 +118,22 @@ def _torch():
     return _modules[0]
 
 
+_templates = {}
+
+
+def _new(device, dtype, *shape):
+    """torch.empty, from an empty tensor of the device and type: it takes half as long as naming both.  Only a plain
+    tensor is kept for it: under FakeTensorMode and the like torch.empty gives something else."""
+    key = device.index, dtype
+    t = _templates.get(key)
+    if t is None:
+        torch = _torch()[0]
+        t = torch.empty(0, dtype=dtype, device=device)
+        if type(t) is torch.Tensor:
+            _templates[key] = t
+    return t.new_empty(*shape)
+
+
 def _check_err_word(what, err, device, torch):
     if err is not None and (err.dtype != torch.int32 or err.numel() < 1 or err.device != device):
         raise ValueError(f"{what}: the error word must be an int32 tensor of at least one element on {device}")
@@ -195,7 +211,7 @@ def window_attn(cfg: SeqConfig, q, k, v, cu_q, cu_k=None, out=None, lse=None, er
     new = out is None
     if new:
         out = torch.empty_like(q)
-        lse = q.new_empty((q.shape[0], cfg.Hq), dtype=torch.float32)
+        lse = _new(dev, torch.float32, q.shape[0], cfg.Hq)
         if cu_q.shape[0] == 1:     # no sequence at all: nothing is launched
             return out.zero_(), lse.fill_(-math.inf)
     else:
@@ -221,9 +237,10 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     torch, T, dev = _window_args(what, cfg, q, k, v, cu_q, cu_k)
     if stream is not None:
         _owned(what, dq, dk, dv, workspace)
-    for name, t in (("out", out), ("dout", dout)):
-        _require(what, cfg, name, t, T, tuple(q.shape), dev)
-    _require(what, cfg, "lse", lse, torch.float32, tuple(q.shape[:2]), dev)
+    shape = q.shape
+    _require(what, cfg, "out", out, T, shape, dev)
+    _require(what, cfg, "dout", dout, T, shape, dev)
+    _require(what, cfg, "lse", lse, torch.float32, shape[:2], dev)
     new = dq is None
     if (dk is None) != new or (dv is None) != new:
         raise ValueError(f"{what}: give all of dq, dk and dv or none of them")
@@ -240,7 +257,7 @@ def window_attn_bwd(cfg: SeqConfig, q, k, v, cu_q, cu_k, out, lse, dout, dq=None
     batch, q_rows, k_rows = cu_q.shape[0] - 1, q.shape[0], k.shape[0]
     if workspace is None:
         n = window_attn_bwd_workspace_bytes(cfg, batch, q_rows, k_rows)
-        workspace = q.new_empty(max(n, 256), dtype=torch.uint8)
+        workspace = _new(dev, torch.uint8, max(n, 256))
     else:
         n = workspace.numel() * workspace.element_size()
     _call(torch, what, lib.pack3d_window_attn_bwd, dev, stream, ctypes.byref(cfg), batch, q_rows, k_rows,
@@ -281,8 +298,9 @@ def _autograd():
                 # Saved-tensor hooks may give back other tensors than the forward saved: of equal values but other
                 # strides, which is put right here, or of another type or device, which the call refuses.
                 saved = [t.contiguous() for t in ctx.saved_tensors]
-                return None, *window_attn_bwd(ctx.cfg, *saved, dout.to(saved[0].dtype).contiguous(),
-                                              err=ctx.err), None, None, None
+                if dout.dtype is not saved[0].dtype:
+                    dout = dout.to(saved[0].dtype)
+                return None, *window_attn_bwd(ctx.cfg, *saved, dout.contiguous(), err=ctx.err), None, None, None
 
         _autograd_class = WindowAttention
     return _autograd_class
@@ -343,7 +361,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     else:
         _require(what, cfg, "out", out, T, tuple(q.shape), dev)
     if lse is None:
-        lse = q.new_empty((batch, cfg.Hq), dtype=torch.float32)
+        lse = _new(dev, torch.float32, batch, cfg.Hq)
     else:
         _require(what, cfg, "lse", lse, torch.float32, (batch, cfg.Hq), dev)
     if weights is not None:
@@ -354,7 +372,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
         n = workspace.numel() * workspace.element_size()
     elif weights is not None and batch:                # always needs one
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, True)
-        workspace = q.new_empty(n, dtype=torch.uint8)
+        workspace = _new(dev, torch.uint8, n)
     _check_err_word(what, err, dev, torch)
     args = (ctypes.byref(cfg), batch, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
             max_pages, k_pages.shape[0], lengths.data_ptr(), out.data_ptr(), lse.data_ptr(), _p(weights),
@@ -362,7 +380,7 @@ def cache_attn(cfg: SeqConfig, q, k_pages, v_pages, table, lengths, out=None, ls
     st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, _p(workspace), n, _p(err))
     if st == ERR_WORKSPACE and workspace is None:      # short calls need none: asked for only when missed
         n = cache_attn_workspace_bytes(cfg, batch, max_pages, weights is not None)
-        workspace = q.new_empty(n, dtype=torch.uint8)
+        workspace = _new(dev, torch.uint8, n)
         st = _run(torch, lib.pack3d_cache_attn, dev, stream, *args, workspace.data_ptr(), n, _p(err))
     if st != 0:
         raise Pack3DError(st, what)
@@ -388,7 +406,7 @@ def cache_evict(cfg: SeqConfig, k_pages, v_pages, table, lengths, weights, new_t
     for name, t, dt, shape in (("kept", kept, torch.int32, shapes[0]), ("new_weights", new_weights, torch.float32,
                                shapes[1]), ("new_lengths", new_lengths, torch.int32, shapes[2])):
         if t is None:
-            t = table.new_empty(shape, dtype=dt)
+            t = _new(dev, dt, *shape)
         else:
             _require(what, cfg, name, t, dt, shape, dev)
         outs.append(t)

@@ -54,10 +54,11 @@ def test_saved_tensors_that_are_something_else(p3, unpack, match):
         torch.autograd.grad(o, leaves, dout)
 
 
-def test_a_call_with_fake_tensors_leaves_nothing_behind(p3):
+def test_a_call_with_fake_tensors_leaves_nothing_behind(p3, monkeypatch):
     """Under FakeTensorMode there is no memory to run on: the call is refused, and the next one, on tensors that exist,
     makes its results and workspaces of memory that exists too."""
     from torch._subclasses.fake_tensor import FakeTensorMode
+    monkeypatch.setattr(p3.seq, "_templates", {})        # as in a new process
     q, k, v, dout = tensors(100, 8, 2)
     cfg = p3.make_seq_config(window=16, sinks=2, page=16)
     cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
@@ -76,3 +77,19 @@ def test_a_call_with_fake_tensors_leaves_nothing_behind(p3):
     ref_lse = torch.logsumexp((q[99].double().view(2, 4, 64) @ torch.cat((k[:2], k[84:])).double().permute(1, 2, 0)) / 8, -1)
     assert torch.allclose(lse[99].double(), ref_lse.view(-1), atol=1e-4)
     assert torch.allclose(got_lse[0].double(), ref_lse.view(-1), atol=1e-4)
+
+
+def test_a_first_call_in_inference_mode(p3, monkeypatch):
+    """What the first call of a process leaves behind does not make later results inference tensors."""
+    monkeypatch.setattr(p3.seq, "_templates", {})
+    q, k, v, dout = tensors(100, 8, 2)
+    cfg, cu = p3.make_seq_config(window=16), torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    with torch.inference_mode():
+        want, lse = p3.window_attn(cfg, q, k, v, cu)
+        grads = p3.window_attn_bwd(cfg, q, k, v, cu, None, want, lse, dout)
+    leaves = [t.detach().clone().requires_grad_(True) for t in (q, k, v)]
+    out = p3.window_attention(cfg, *leaves, cu)
+    assert torch.equal(out, want)
+    for a, b in zip(torch.autograd.grad(out, leaves, dout), grads):
+        assert torch.equal(a, b) and not a.is_inference()
+    assert not p3.window_attn(cfg, q, k, v, cu)[1].is_inference()
