@@ -101,7 +101,7 @@ constexpr int kStages = 8;
 constexpr int kQOff = 0, kDOOff = kQTileBytes, kStageOff = 2 * kQTileBytes;
 constexpr int kStageBytes = 2 * kKVBytes;       // K at +0, V at +kKVBytes
 constexpr int kBarOff = kStageOff + kStages * kStageBytes;
-// barriers: full[S], empty[S], qfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], cleared
+// barriers: full[S], empty[S], qfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], landed
 constexpr int kNumBars = 2 * kStages + 13;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kHalfOff = kCtlOff + 32;          // float [2][128]: the groups' shares of D
@@ -139,7 +139,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto p_full = [&](int b) { return qfull + 48 + 8 * b; };
   auto p_free = [&](int b) { return qfull + 64 + 8 * b; };
   auto drain = [&](int i) { return qfull + 80 + 8 * i; };
-  const uint32_t cleared = qfull + 96;
+  const uint32_t landed = qfull + 96;          // for the tile that is cleared in part
   float* shares = reinterpret_cast<float*>(smem + kHalfOff);
   volatile uint8_t* redo = smem + kRedoOff;
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
@@ -168,7 +168,7 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ptx::mbar_init(drain(b), 1);
     }
     ptx::mbar_init(o_final, 1);
-    ptx::mbar_init(cleared, 1);
+    ptx::mbar_init(landed, 1);
     ctl->abort = 0;
     ctl->issued = 0;
     ctl->limit_ns = w.wait_ns;
@@ -195,9 +195,10 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   auto load_tile = [&](int j) {
     const int st = j % kStages;
     const uint32_t dst = sbase + kStageOff + st * kStageBytes;
-    ptx::mbar_expect_tx(full(st), kStageBytes);
-    ptx::tma_load_3d(dst, &tmK, 0, g, s.k0 + kt.begin(j), full(st));
-    ptx::tma_load_3d(dst + kKVBytes, &tmV, 0, g, s.k0 + kt.begin(j), full(st));
+    const uint32_t bar = tail && j == T - 1 ? landed : full(st);
+    ptx::mbar_expect_tx(bar, kStageBytes);
+    ptx::tma_load_3d(dst, &tmK, 0, g, s.k0 + kt.begin(j), bar);
+    ptx::tma_load_3d(dst + kKVBytes, &tmV, 0, g, s.k0 + kt.begin(j), bar);
   };
   if (warp == kTmaWarp && lane == 0 && T > 0) {
     ptx::mbar_expect_tx(qfull, 2 * kQTileBytes);
@@ -231,9 +232,9 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     __syncwarp();
     if (tail) {
       const int st = (T - 1) % kStages;
-      if (__all_sync(0xffffffffu, wait(full(st), ((T - 1) / kStages) & 1))) {
+      if (__all_sync(0xffffffffu, wait(landed, 0))) {
         clear_rows(sbase + kStageOff + st * kStageBytes, s.lk - kt.begin(T - 1), kBN);
-        say_cleared(cleared);
+        say_cleared(full(st));
       }
     }
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
@@ -266,13 +267,11 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       bool ok = true;
       if (warp == kMmaWarp) {
         ok = wait(qfull, 0);
-        const int tail_tile = tail ? T - 1 : T;
         // The first pass's tiles, then all.
 #pragma unroll 1
         for (int u = 0; ok && u < first + T; ++u) {
           const int j = u < first ? u : u - first;
           ok = wait(full(j % kStages), (j / kStages) & 1) && (u < 2 || wait(s_free(u & 1), ((u >> 1) - 1) & 1));
-          if (ok && j == tail_tile) ok = wait(cleared, 0);
           if (!ok) break;
           ptx::tc_fence_after();
           issue_sdp(j, u & 1);
@@ -429,7 +428,8 @@ window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ptx::mbar_wait_drain(qfull, 0, ctl->limit_ns);
       const int issued = ctl->issued;
       for (int j = max(0, issued - kStages); j < issued; ++j)
-        ptx::mbar_wait_drain(full(j % kStages), (j / kStages) & 1, ctl->limit_ns);
+        if (tail && j == T - 1) ptx::mbar_wait_drain(landed, 0, ctl->limit_ns);
+        else ptx::mbar_wait_drain(full(j % kStages), (j / kStages) & 1, ctl->limit_ns);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -484,7 +484,7 @@ static_assert(kStageOff % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles"
 // would carry its NaNs over).
 constexpr int kZeroOff = kVOff + kKeyTileBytes;
 constexpr int kBarOff = kZeroOff + kTermBytes;
-// barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], cleared
+// barriers: full[S], empty[S], kvfull, o_final, s_full[2], s_free[2], p_full[2], p_free[2], drain[2], landed
 constexpr int kNumBars = 2 * kStages + 13;
 constexpr int kCtlOff = kBarOff + kNumBars * 8;
 constexpr int kTileOff = kCtlOff + 32;
@@ -522,7 +522,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   auto p_full = [&](int b) { return kvfull + 48 + 8 * b; };
   auto p_free = [&](int b) { return kvfull + 64 + 8 * b; };
   auto drain = [&](int i) { return kvfull + 80 + 8 * i; };
-  const uint32_t cleared = kvfull + 96;
+  const uint32_t landed = kvfull + 96;         // for the step that is cleared in part
   volatile ptx::WaitCtl* ctl = reinterpret_cast<volatile ptx::WaitCtl*>(smem + kCtlOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kCtlOff + sizeof(ptx::WaitCtl));
   Tile* tile_slot = reinterpret_cast<Tile*>(smem + kTileOff);
@@ -562,7 +562,7 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::mbar_init(p_free(b), 1);
     }
     ptx::mbar_init(o_final, 1);
-    ptx::mbar_init(cleared, 1);
+    ptx::mbar_init(landed, 1);
     ptx::mbar_init(drain(0), 1);
     ptx::mbar_init(drain(1), 1);
     ctl->abort = 0;
@@ -639,10 +639,11 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         if (t >= kStages && !wait(empty(st), ((t / kStages) - 1) & 1)) break;
         const uint32_t dst = sbase + kStageOff + st * kStageBytes;
         const int tok0 = s.q0 + ra + t * tokens;
-        ptx::mbar_expect_tx(full(st), kStageBytes);
-        ptx::tma_load_4d(dst, &tmQ, 0, 0, g, tok0, full(st));
-        ptx::tma_load_4d(dst + kStepBytes, &tmO, 0, 0, g, tok0, full(st));
-        ptx::tma_load_5d(dst + kTermsAt, &tmT, 0, 0, g, tok0, 0, full(st));
+        const uint32_t bar = tail && t == nsteps - 1 ? landed : full(st);
+        ptx::mbar_expect_tx(bar, kStageBytes);
+        ptx::tma_load_4d(dst, &tmQ, 0, 0, g, tok0, bar);
+        ptx::tma_load_4d(dst + kStepBytes, &tmO, 0, 0, g, tok0, bar);
+        ptx::tma_load_5d(dst + kTermsAt, &tmT, 0, 0, g, tok0, 0, bar);
         issued = t + 1;
       }
       ctl->issued = issued;
@@ -650,10 +651,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     __syncwarp();
     if (tail) {
       const int st = (nsteps - 1) % kStages;
-      if (__all_sync(0xffffffffu, wait(full(st), ((nsteps - 1) / kStages) & 1))) {
+      if (__all_sync(0xffffffffu, wait(landed, 0))) {
         clear_rows(sbase + kStageOff + st * kStageBytes, left, kStep);
         clear_rows(sbase + kStageOff + st * kStageBytes + kStepBytes, left, kStep);
-        say_cleared(cleared);
+        say_cleared(full(st));
       }
     }
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
@@ -693,13 +694,11 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       };
       bool ok = true;
       if (warp == kMmaWarp) {
-        const int tail_step = tail ? nsteps - 1 : nsteps;
         ok = wait(kvfull, 0);
 #pragma unroll 1
         for (int t = 0; ok && t < nsteps; ++t) {
           if (!(ok = wait(full(t % kStages), (t / kStages) & 1))) break;
           if (t > 1 && !(ok = wait(s_free(t & 1), ((t >> 1) - 1) & 1))) break;
-          if (t == tail_step && !(ok = wait(cleared, 0))) break;
           ptx::tc_fence_after();
           issue_sdp(t);
         }
@@ -848,7 +847,8 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ptx::mbar_wait_drain(kvfull, 0, ctl->limit_ns);
       const int issued = ctl->issued;
       for (int t = max(0, issued - kStages); t < issued; ++t)
-        ptx::mbar_wait_drain(full(t % kStages), (t / kStages) & 1, ctl->limit_ns);
+        if (tail && t == nsteps - 1) ptx::mbar_wait_drain(landed, 0, ctl->limit_ns);
+        else ptx::mbar_wait_drain(full(t % kStages), (t / kStages) & 1, ctl->limit_ns);
     }
     ptx::tc_fence_before();
     __syncthreads();
