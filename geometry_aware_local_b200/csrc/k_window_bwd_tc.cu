@@ -13,7 +13,7 @@
 //   issues dQ += dS K with the same K tile read MN-major.  It also forms D of its
 //   rows and leaves it for the second kernel.  (65,536 tokens, window 1,024, both
 //   kernels: one group and 64 keys a step 0.748 ms, two warps a row quarter on the
-//   same step 0.751, now 0.711.)
+//   same step 0.751, two groups 0.711.)
 //
 // window_dkv_tc_kernel: one 128-key tile of one key head per CTA and the
 //   queries whose window reaches it, 64 rows a step, one CTA per SM.  S^T and
@@ -41,7 +41,7 @@
 // the tile itself leave float partial sums of the sink rows; window_sinks_kernel
 // adds them in a fixed order.  No atomics: the same inputs give the same bits.
 //
-// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.711 ms, 483 TFLOP/s (five
+// 65,536 tokens, 8 / 2 heads, window 1,024, 4 sinks: 0.69 ms, 498 TFLOP/s (five
 // products), about 0.33 ms of it the query side.  As in the forward the pace is
 // that of the softmax warps' chains (load, exponentials, store, arrive), not of
 // the tensor cores.
@@ -114,7 +114,8 @@ static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 // dK off by 1.5 to 1.8 times bf16's own rounding, now 1.4); where it sees more
 // it averages out.  The tiles stay in shared memory for the second pass, so
 // the first costs two products and the exponentials, and saves the reads of out
-// and dout by rows (65,536 tokens, window 65: 0.365 -> 0.349 ms).
+// and dout by rows (65,536 tokens, window 65: 245 us without, 218 with it; with 4
+// sinks 301, 281).
 constexpr int kTwice = 6;
 static_assert(kTwice <= kStages, "the first pass's tiles stay");
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kRowsPerTile, kBN, false);
@@ -900,9 +901,10 @@ window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 // CTAs of a cluster that share a key tile's steps: a share should be four steps
 // long where every CTA has an SM of its own, and 64 where some SMs get a second
 // one, which pays where the tiles' lengths differ.  (Both kernels, no window:
-// 2,048 tokens, 8 / 2 heads, 1, 4, 8 CTAs 97, 55, 72 us; 4,096, 1, 2, 4 CTAs 198, 140,
-// 121; 8,192, 16 / 2 heads, 1, 2 CTAs 758, 512; window 512, 2,048 tokens, 1, 4, 8 CTAs
-// 45, 39, 47.)
+// 2,048 tokens, 8 / 2 heads, 1, 4, 8 CTAs 99, 56, 71 us; 4,096, 1, 2, 4 CTAs 195, 137,
+// 115; 8,192, 16 / 2 heads, 1, 2 CTAs 747, 524; window 512, 2,048 tokens, 1, 4, 8 CTAs
+// 46, 34, 56.)  The host knows the mean length only: 4,096 tokens with 31 sequences of
+// one count as short and get 1 CTA, 202 us (143 with 2).
 int split_of(const Win& w, long key_ctas) {
   const long mean = (w.Tq + w.B - 1) / w.B, rows = w.window > 0 ? min(mean, (long)w.window + k_side::kKeys) : mean;
   const long steps = (rows * w.G + k_side::kStep - 1) / k_side::kStep, tiles = key_ctas * w.Hkv, sms = sm_count();

@@ -14,9 +14,8 @@
 // tiles their warps are too few.  There the CTAs of a cluster share a tile besides,
 // and join what they have through each other's shared memory.  2,050 tokens in
 // three sequences, 4 / 2 heads, window 200, one sink: forward 34 us (128 threads, a
-// multiply-add an instruction: 42), backward 99 us (166, with the two sides one
-// after the other and a CTA a tile).  16,384 tokens, 8 / 2 heads: 0.323 and 1.05 ms
-// (0.330, 1.14).
+// multiply-add an instruction: 42), backward 97 us (166, with the two sides one
+// after the other and a CTA a tile).  16,384 tokens, 8 / 2 heads: 0.318 and 1.03 ms.
 //
 // What is hidden has P = 0; rows that 0 times a NaN or an infinity spoilt are
 // computed again (out_again, dq_again, dkv_row), as in the tensor-core kernels.
@@ -531,11 +530,12 @@ cudaError_t allow(K kernel, int tiles) {
 // CTAs of a cluster that share a tile, of `tiles` in the call: a share should be
 // eight steps long, `least` where the SMs would have four CTAs at most (two in the
 // backward; the forward's are half as long: four), one where there is a CTA an SM
-// at most.  (Backward: 3,000 tokens, 2 / 1 heads, no window, 1 CTA 0.926 ms, 8 CTAs
-// 0.299; 1,000, 4 heads: 1, 4, 8 CTAs 163, 87, 117 us; 2,600, 8 / 2 heads, window
-// 300: 1, 2, 4: 279, 231, 280; 1,000 in two, 8 heads, window 64, which is two steps:
-// 1, 2: 37, 47.  Forward: the first 255 us with 1, 95 with 4; 2,050 in three, window
-// 200, four steps: 1, 2: 34, 38.)
+// at most.  (Backward: 3,000 tokens, 2 / 1 heads, no window, 1 CTA 0.911 ms, 8 CTAs
+// 0.294; 1,000, 4 heads: 1, 4, 8 CTAs 161, 84, 112 us; 2,600, 8 / 2 heads, window
+// 300: 1, 2, 4: 251, 209, 241; 1,000 in two, 8 heads, window 64, which is two steps:
+// 1, 2: 36, 46.  Forward: the first 255 us with 1, 93 with 4; 2,050 in three, window
+// 200, four steps: 1, 2: 33, 36.)  The host knows the mean length only: 3,000 tokens
+// with 31 sequences of one count as short, 965 us backward with 1 CTA (316 with 4).
 int split_of(long tiles, long steps, long least) {
   const long sms = sm_count();
   auto good = [&](long S) {

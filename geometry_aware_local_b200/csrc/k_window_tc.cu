@@ -35,8 +35,8 @@
 // purpose: the roles' loops evict one another from the instruction cache, and a
 // second copy of the softmax body for tiles without masks made the kernel a
 // quarter slower.
-// 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.230 ms, 595 TFLOP/s, with
-// narrow tiles; 0.287 with wide ones (0.298 with S and two P buffers apart, 0.320
+// 65,536 tokens, 8/2 heads, window 1,024, 4 sinks: 0.228 ms, 600 TFLOP/s, with
+// narrow tiles; 0.288 with wide ones (0.298 with S and two P buffers apart, 0.320
 // with persistent CTAs that walk the tiles).
 //
 // Few query tiles before many keys (a piece of a long prompt) would leave most
@@ -502,7 +502,7 @@ window_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 
 // CTAs of a cluster per query tile: as many as keep two CTAs an SM busy and
 // leave each at least four key tiles (2,048 queries before 16,384 keys, 8 heads
-// to one key head: 0.238 ms with 1, 0.131 with 2).
+// to one key head: 0.197 ms with 1, 0.130 with 2, 0.138 with 4).
 int split_of(const Win& w, long tiles) {
   const long keys = w.window > 0 ? min((long)w.Tk, (long)w.window + 2 * kWide) : w.Tk;
   int S = 1;
@@ -513,9 +513,9 @@ int split_of(const Win& w, long tiles) {
 // Whether the key tiles are narrow, with four CTAs an SM: where there are CTAs
 // for them.  Without a window the CTAs' lengths differ, and it takes more than
 // four an SM for the short ones to fill the gaps.  Narrow against wide: 65,536
-// tokens, window 1,024 0.230 : 0.287 ms; 6,300 tokens, 8 key heads, window 256
-// (400 CTAs) 23 : 27 us; 4,096, window 512 (256) 19.5 : 18.5; 8,192, no window
-// (512) 163 : 154; the same with 16 heads (1,024) 225 : 238.
+// tokens, window 1,024 0.228 : 0.288 ms; 6,300 tokens, 8 key heads, window 256
+// (400 CTAs) 21 : 26 us; 4,096, window 512 (256) 19.3 : 18.6; 8,192, no window
+// (512) 162 : 155; the same with 16 heads (1,024) 225 : 238.
 bool narrow(const Win& w, long tiles) {
   return tiles * w.Hkv > (w.window > 0 ? 2L : 4L) * sm_count();
 }

@@ -18,7 +18,10 @@ Every function runs asynchronously on the current stream of its tensors' device,
 an explicit ``stream`` the caller also gives every output and the workspace, since memory allocated here belongs to
 the current stream.  ``err`` is an int32 error word on the device (zeroed by the caller before its first use), read
 by ``check_status``; without one, errors that only the device can see (offsets, lengths or page numbers out of
-range) go unreported.
+range, a wait that ran out) go unreported, and the results are then whatever was in their memory.
+
+Sums, softmax and its statistics are in float whatever the type; with bf16 the probabilities, and in the backward the
+scores' gradients, are rounded to bf16 for the tensor cores' second product, as the results are at the end.
 """
 from __future__ import annotations
 

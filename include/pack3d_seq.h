@@ -38,7 +38,8 @@
  *   V(p) = { j : 0 <= j <= p and (window == 0 or p - j < window or j < sinks) }.
  * With Lq > Lk the first queries see no key; their output is 0 and their
  * log-sum-exp -infinity.  What a query does not see never reaches its results,
- * not even a NaN or an infinity.
+ * not even a NaN or an infinity.  (Results that a hidden one has spoilt are formed
+ * again, on a slower path: a tile's rows for each such token.)
  */
 #ifndef PACK3D_SEQ_H
 #define PACK3D_SEQ_H
@@ -92,8 +93,9 @@ size_t pack3d_window_attn_bwd_workspace_bytes(const pack3d_seq_config *cfg, int3
  *   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
  * summed over the query heads of a key head.  dq T [q_rows,Hq,64], dk, dv T
  * [k_rows,Hkv,64]; rows of keys that no query sees get 0.  Float accumulation
- * in a fixed order: the same inputs give the same bits.  workspace: 256-byte
- * aligned, contents on entry do not matter. */
+ * in a fixed order: the same inputs give the same bits.  bf16 runs on tcgen05
+ * tensor cores with P and dS rounded to bf16 for the products with dout, q and k.
+ * workspace: 256-byte aligned, contents on entry do not matter. */
 pack3d_status pack3d_window_attn_bwd(const pack3d_seq_config *cfg, int32_t batch, int64_t q_rows, int64_t k_rows,
                                      const int32_t *cu_q, const int32_t *cu_k, const void *q, const void *k,
                                      const void *v, const void *out, const float *lse, const void *dout, void *dq,
@@ -132,7 +134,10 @@ size_t pack3d_cache_attn_workspace_bytes(const pack3d_seq_config *cfg, int32_t b
  * lse = -infinity.  weights float [batch, max_pages*page] (nullable): the
  * softmax weights of this token, summed over the Hq heads, are written
  * (accumulate == 0) or added (accumulate != 0) to the slots below lengths[b];
- * other slots stay as they were.  The cache's length is split over the GPU's
+ * other slots stay as they were.  Float accumulation and softmax; with bf16 the
+ * probabilities are rounded to bf16 for the product with v (not the weights).
+ * A head whose visible scores are all -infinity gives 0 and no weight, its
+ * log-sum-exp is -infinity.  The cache's length is split over the GPU's
  * processors and the parts are joined in a fixed order: the same inputs give
  * the same bits on the same GPU.  workspace: 256-byte aligned, contents on
  * entry do not matter. */
