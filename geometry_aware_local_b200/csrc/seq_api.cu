@@ -28,7 +28,7 @@ pack3d_status cuda_status(cudaError_t e) {
 struct Span {
   uintptr_t from, to;
   Span(const void* p, int64_t n, int size) : from((uintptr_t)p), to(p ? from + (uintptr_t)n * size : from) {}
-  bool meets(const Span& o) const { return from < o.to && o.from < to; }
+  bool meets(const Span& o) const { return from < to && o.from < o.to && from < o.to && o.from < to; }
 };
 // Whether a written buffer meets a read one or another written one.  (Other CTAs
 // still read the inputs when the first results are written.)

@@ -490,6 +490,22 @@ def test_results_next_to_and_over_the_queries(p3, cuda_device, lengths, Hq, Hkv,
                        kept=torch.empty(B, 64, dtype=torch.int32, device=dev))
 
 
+def test_an_empty_buffer_lies_over_nothing(p3, cuda_device):
+    """No query rows: their buffers hold nothing, wherever the pointers point."""
+    import ctypes
+    dev = cuda_device
+    k, v, dk, dv = (torch.full((40, 2, 64), 3.0, dtype=torch.bfloat16, device=dev) for _ in range(4))
+    cu_q, cu_k = offsets([0], dev), offsets([40], dev)
+    cfg = p3.make_seq_config()
+    ws = torch.empty(max(256, p3.window_attn_bwd_workspace_bytes(cfg, 1, 0, 40)), dtype=torch.uint8, device=dev)
+    inside = dk.data_ptr() + 64
+    st = p3.lib.pack3d_window_attn_bwd(ctypes.byref(cfg), 1, 0, 40, cu_q.data_ptr(), cu_k.data_ptr(), inside, k.data_ptr(),
+                                       v.data_ptr(), inside, inside, inside, inside, dk.data_ptr(), dv.data_ptr(), 0,
+                                       ws.data_ptr(), ws.numel(), None, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (dk == 0).all() and (dv == 0).all()
+
+
 def test_pool_beyond_32_bit_offsets(p3, cuda_device):
     """Pages whose elements and bytes lie beyond 2^31 and 2^32: written, read and moved there.  (Keys and values in
     one pool of 10.5 GB: append writes equal rows to both.)"""
